@@ -30,12 +30,14 @@ __all__ = ["GdrError", "load", "chunk_fwd", "decode_step", "chunk_decay", "chunk
            "status_string", "version", "library_path", "STATUS", "PATHS", "OPTIONS",
            "set_option", "get_option", "option", "mla_decode", "mla_decode_workspace_size",
            "chunk_bwd", "chunk_bwd_workspace_size", "chunk_saved_size", "chunk_fwd_train",
-           "chunk_bwd_saved"]
+           "chunk_bwd_saved", "page_plan", "kv8_append", "kv8_attn", "kv8_attn_workspace_size",
+           "KV8"]
 
 DECAY = {"affine": 0, "log": 1}   # gdr_decay_t
 STATUS = {0: "GDR_OK", 1: "GDR_ERR_INVALID_ARG", 2: "GDR_ERR_UNSUPPORTED", 3: "GDR_ERR_RANGE",
           4: "GDR_ERR_CUDA", 5: "GDR_ERR_TIMEOUT"}
 DTYPE = {torch.float32: 0, torch.bfloat16: 1}
+KV8 = {torch.float8_e4m3fn: 0, torch.int8: 1}   # gdr_kv8_t
 # gdr_option_t
 OPTIONS = {"wait_limit_ns": 0, "fused_variant": 1, "chain_split": 2, "segments": 3,
            "bwd_variant": 4}
@@ -68,6 +70,7 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         _build.build()
     lib = ctypes.CDLL(path)
     vp, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    i64 = ctypes.c_int64
     sig = {
         "gdr_chunk_fwd": [vp, vp, vp, vp, vp, f, vp, vp, vp, i, i, i, i, i, i, i, vp],
         "gdr_chunk_fwd_ws": [vp, vp, vp, vp, vp, f, vp, vp, vp, i, i, i, i, i, i, i, vp, sz, vp],
@@ -97,6 +100,9 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         "gdr_version": [],
         "gdr_set_option": [i, ctypes.c_int64],
         "gdr_mla_decode": [vp, vp, vp, vp, vp, f, vp, i, i, i, i, i, vp, sz, vp],
+        "gdr_page_plan": [vp] * 11 + [i] * 5 + [vp],
+        "gdr_kv8_append": [vp, vp, i64, i64, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp],
+        "gdr_kv8_attn": [vp, i64, vp, vp, vp, vp, vp, vp, vp, f, vp, vp] + [i] * 11 + [vp, sz, vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -110,6 +116,8 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         fn.restype = sz
     lib.gdr_mla_decode_workspace_size.argtypes = [i, i, i, i, i]
     lib.gdr_mla_decode_workspace_size.restype = sz
+    lib.gdr_kv8_attn_workspace_size.argtypes = [i] * 7
+    lib.gdr_kv8_attn_workspace_size.restype = sz
     lib.gdr_get_option.argtypes = [i]
     lib.gdr_get_option.restype = ctypes.c_int64
     lib.gdr_status_string.restype = ctypes.c_char_p
@@ -558,3 +566,122 @@ def last_device_error(device=None) -> int:
     as a status code (0 = ok, 5 = a bounded wait timed out)."""
     lib = load()
     return int(lib.gdr_last_device_error(_stream(device)))
+
+
+# ---- the paged 8-bit cache of the exact-attention layers
+
+def _int(t, name, shape=None):
+    """Device pointer of a contiguous int32 CUDA tensor."""
+    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 CUDA tensor")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _rows(t, name):
+    """Device pointer and token stride of a [tokens, heads, D] CUDA tensor whose tokens may
+    be strided (a slice of a wider projection) and whose heads are contiguous."""
+    if t.dtype not in DTYPE:
+        raise TypeError(f"{name} must be float32 or bfloat16")
+    if not t.is_cuda or t.dim() != 3:
+        raise ValueError(f"{name} must be a [tokens, heads, D] CUDA tensor")
+    n, h, d = t.shape
+    st = t.stride()
+    if (st[2] != 1 and d > 1) or (st[1] != d and h > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), st[0] if n > 1 else h * d
+
+
+def _kv8_cache(k_cache, v_cache, k_scale, v_scale):
+    if k_cache.dtype not in KV8 or v_cache.dtype != k_cache.dtype:
+        raise TypeError("k_cache, v_cache must share one dtype, float8_e4m3fn or int8")
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError("k_cache, v_cache must be [num_pages, Hkv, page, D]")
+    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+        raise TypeError("k_scale, v_scale must be float32")
+    if k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
+        raise ValueError("k_scale, v_scale must be [num_pages, Hkv]")
+    for t in (k_cache, v_cache, k_scale, v_scale):
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError("libgdr takes contiguous CUDA tensors")
+    return shape
+
+
+def page_plan(kv_len, q_len, block_table, free_ring, free_state, page: int, max_tokens: int):
+    """Places for the new tokens of a step, on the device.  kv_len, q_len [S] (q_len < 0:
+    finished), block_table [S,W], free_ring [num_pages], free_state [2] = (head, count), all
+    int32; block_table and free_ring are updated in place.  Returns int32 (kv_len_out [S],
+    cu_q [S+1], slots [max_tokens], positions [max_tokens], granted [S], free_state_out [2])."""
+    lib = load()
+    S, W = block_table.shape
+    n = int(max_tokens)
+    slots, positions, cu, kv, granted, st, _ = torch.empty(
+        2 * n + 3 * S + 4, dtype=torch.int32, device=block_table.device).split((n, n, S + 1, S, S, 2, 1))
+    _check(lib.gdr_page_plan(_int(kv_len, "kv_len", (S,)), _int(q_len, "q_len", (S,)),
+                             _int(block_table, "block_table"), _int(free_ring, "free_ring"),
+                             _int(free_state, "free_state", (2,)), kv.data_ptr(), cu.data_ptr(),
+                             slots.data_ptr(), positions.data_ptr(), granted.data_ptr(),
+                             st.data_ptr(), S, W, int(page), free_ring.numel(), n,
+                             _stream(block_table.device)), "gdr_page_plan")
+    return kv, cu, slots, positions, granted, st
+
+
+def kv8_append(k, v, slots, k_cache, v_cache, k_scale, v_scale) -> None:
+    """Quantise the new tokens' k, v [T,Hkv,D] (fp32 or bf16; tokens may be strided) into the
+    paged cache at slots [T] int32 (negative: dropped).  k_cache, v_cache [num_pages,Hkv,page,D]
+    float8_e4m3fn or int8, k_scale, v_scale [num_pages,Hkv] fp32, all updated in place."""
+    lib = load()
+    N, H, P, D = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    (kp, kst), (vp, vst) = _rows(k, "k"), _rows(v, "v")
+    T = k.shape[0]
+    if k.dtype != v.dtype:
+        raise TypeError("k, v must share one dtype, float32 or bfloat16")
+    if k.shape != (T, H, D) or v.shape != (T, H, D):
+        raise ValueError(f"k, v must be [T, {H}, {D}]")
+    _check(lib.gdr_kv8_append(kp, vp, kst, vst, _int(slots, "slots", (T,)), k_cache.data_ptr(),
+                              v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), T, H, D,
+                              P, N, DTYPE[k.dtype], KV8[k_cache.dtype], _stream(k.device)),
+           "gdr_kv8_append")
+
+
+def kv8_attn_workspace_size(S, max_q, total_q, Hq, Hkv, D, dtype=torch.bfloat16) -> int:
+    """Bytes of workspace kv8_attn needs (0: none)."""
+    return int(load().gdr_kv8_attn_workspace_size(S, max_q, total_q, Hq, Hkv, D, DTYPE[dtype]))
+
+
+def kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, scale: float, *,
+             cu_q=None, max_q: int = 1, out=None, want_lse: bool = False, workspace=None):
+    """Attention over the paged 8-bit cache.  q [total_q,Hq,D] fp32 or bf16 (tokens may be
+    strided), block_table [S,W] and kv_len [S] int32, cu_q [S+1] int32 first query of each
+    request (None: one query a request), max_q the most queries of a request.  Query i of n
+    sees the first kv_len - n + 1 + i keys.  workspace: None (allocated here) or a uint8 CUDA
+    tensor of kv8_attn_workspace_size bytes.  Returns out [total_q,Hq,D], or (out, lse
+    [total_q,Hq] fp32) if want_lse."""
+    lib = load()
+    N, Hkv, P, D = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    qp, qst = _rows(q, "q")
+    T, Hq, dq = q.shape
+    S, W = block_table.shape
+    if dq != D:
+        raise ValueError(f"q must be [total_q, Hq, {D}]")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_cuda or not out.is_contiguous():
+        raise ValueError("out must be a contiguous CUDA tensor of q's shape and dtype")
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if want_lse else None
+    need = lib.gdr_kv8_attn_workspace_size(S, int(max_q), T, Hq, Hkv, D, DTYPE[q.dtype])
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+    elif workspace.dtype != torch.uint8 or not workspace.is_cuda or workspace.numel() < need:
+        raise ValueError(f"workspace must be a uint8 CUDA tensor of at least {need} bytes")
+    _check(lib.gdr_kv8_attn(qp, qst, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                            v_scale.data_ptr(), _int(block_table, "block_table"),
+                            _int(kv_len, "kv_len", (S,)),
+                            None if cu_q is None else _int(cu_q, "cu_q", (S + 1,)), float(scale),
+                            out.data_ptr(), None if lse is None else lse.data_ptr(), S, int(max_q),
+                            T, Hq, Hkv, D, W, P, N, DTYPE[q.dtype], KV8[k_cache.dtype],
+                            workspace.data_ptr(), workspace.numel(), _stream(q.device)),
+           "gdr_kv8_attn")
+    return (out, lse) if want_lse else out

@@ -48,6 +48,26 @@ gdr_status_t check_staged(int BH, int T, int dk, int dv, int chunk) {
     return GDR_OK;
 }
 
+// ---- the 8-bit paged cache ----
+constexpr int kMaxRequests = 8192;
+bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
+bool fits31(int64_t a, int64_t b) { return a * b <= 0x7fffffff; }
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+gdr::Kv8 kv8_of(gdr_kv8_t kv) { return kv == GDR_KV8_INT8 ? gdr::Kv8::INT8 : gdr::Kv8::E4M3; }
+// Rows of the cache (pages x heads x tokens) are 31-bit coordinates, byte offsets 64-bit.
+bool kv8_shape_ok(int Hkv, int D, int page, int num_pages, gdr_dtype_t dtype, gdr_kv8_t kv) {
+    return (D == 64 || D == 128) && page_ok(page) && dtype_ok(dtype) &&
+           (kv == GDR_KV8_E4M3 || kv == GDR_KV8_INT8) && Hkv <= 4096 &&
+           fits31((int64_t)num_pages * Hkv, page);
+}
+bool kv8_heads_ok(int Hq, int Hkv, int total_q, int S) {
+    return Hq <= 65536 && Hkv <= 4096 && S <= kMaxRequests && fits31(total_q, Hq);
+}
+// A row of H heads of D values, `stride` elements from the next one, 16-byte aligned.
+bool row_stride_ok(int64_t stride, int H, int D, int esz) {
+    return stride >= (int64_t)H * D && stride < ((int64_t)1 << 40) && stride * esz % 16 == 0;
+}
+
 // Process-wide options (gdr_set_option).  Relaxed atomics: a value set before a
 // call is seen by that call's launches on any thread.
 std::atomic<uint64_t> g_wait_limit_ns{2000000000ull};
@@ -688,6 +708,80 @@ gdr_status_t gdr_mla_decode(const void *q_abs, const void *ckv, const int *seqle
         return GDR_ERR_INVALID_ARG;
     return from_cuda(gdr::launch_mla_decode(q_abs, ckv, seqlens, w_uv, gate, scale, out, N, H, Lmax,
                                             dh, workspace, static_cast<cudaStream_t>(stream)));
+}
+
+// ---- the 8-bit paged cache ----
+
+gdr_status_t gdr_page_plan(const int *kv_len, const int *q_len, int *block_table, int *free_ring,
+                           const int *free_state, int *kv_len_out, int *cu_q, int *slots,
+                           int *positions, int *granted, int *free_state_out, int S,
+                           int table_width, int page, int num_pages, int max_tokens, void *stream) {
+    if (S < 0 || table_width <= 0 || num_pages <= 0 || max_tokens < 0) return GDR_ERR_INVALID_ARG;
+    if (!page_ok(page) || S > kMaxRequests || max_tokens > (1 << 30) ||
+        !fits31(num_pages, page) || !fits31(table_width, page) || !fits31(S, table_width))
+        return GDR_ERR_UNSUPPORTED;
+    if (!free_ring || !free_state || !cu_q || !free_state_out || free_state == free_state_out)
+        return GDR_ERR_INVALID_ARG;
+    if (S > 0 && (!kv_len || !q_len || !block_table || !kv_len_out || !granted ||
+                  kv_len == kv_len_out || q_len == kv_len_out))
+        return GDR_ERR_INVALID_ARG;
+    if (max_tokens > 0 && (!slots || !positions)) return GDR_ERR_INVALID_ARG;
+    return from_cuda(gdr::launch_page_plan(kv_len, q_len, block_table, free_ring, free_state, kv_len_out,
+                                           cu_q, slots, positions, granted, free_state_out, S, table_width,
+                                           page, num_pages, max_tokens, static_cast<cudaStream_t>(stream)));
+}
+
+gdr_status_t gdr_kv8_append(const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                            const int *slots, void *k_cache, void *v_cache, float *k_scale,
+                            float *v_scale, int T, int Hkv, int D, int page, int num_pages,
+                            gdr_dtype_t dtype, gdr_kv8_t kv, void *stream) {
+    if (T < 0 || Hkv < 0 || num_pages < 0) return GDR_ERR_INVALID_ARG;
+    if (!kv8_shape_ok(Hkv, D, page, num_pages, dtype, kv)) return GDR_ERR_UNSUPPORTED;
+    if (T == 0 || Hkv == 0 || num_pages == 0) return GDR_OK;
+    if (!k || !v || !slots || !k_cache || !v_cache || !k_scale || !v_scale) return GDR_ERR_INVALID_ARG;
+    const int esz = dtype == GDR_DTYPE_F32 ? 4 : 2;
+    if (!row_stride_ok(k_stride, Hkv, D, esz) || !row_stride_ok(v_stride, Hkv, D, esz))
+        return GDR_ERR_INVALID_ARG;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(k_cache) || !aligned16(v_cache))
+        return GDR_ERR_INVALID_ARG;
+    return from_cuda(gdr::launch_kv8_append(k, v, k_stride, v_stride, slots, k_cache, v_cache, k_scale,
+                                            v_scale, T, Hkv, D, page, num_pages, elem_of(dtype),
+                                            kv8_of(kv), static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdr_kv8_attn_workspace_size(int S, int max_q, int total_q, int Hq, int Hkv, int D,
+                                   gdr_dtype_t dtype) {
+    if (S <= 0 || max_q <= 0 || total_q <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0) return 0;
+    if (!kv8_shape_ok(Hkv, D, 16, 1, dtype, GDR_KV8_E4M3) || !kv8_heads_ok(Hq, Hkv, total_q, S)) return 0;
+    return gdr::kv8_attn_workspace_bytes(S, max_q, total_q, Hq, Hkv, D, elem_of(dtype));
+}
+
+gdr_status_t gdr_kv8_attn(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                          const float *k_scale, const float *v_scale, const int *block_table,
+                          const int *kv_len, const int *cu_q, float scale, void *out, float *lse,
+                          int S, int max_q, int total_q, int Hq, int Hkv, int D, int table_width,
+                          int page, int num_pages, gdr_dtype_t dtype, gdr_kv8_t kv,
+                          void *workspace, size_t workspace_bytes, void *stream) {
+    if (S < 0 || max_q < 0 || total_q < 0 || Hq < 0 || Hkv < 0 || table_width < 0 || num_pages < 0)
+        return GDR_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return GDR_ERR_INVALID_ARG;
+    if (!kv8_shape_ok(Hkv, D, page, num_pages, dtype, kv)) return GDR_ERR_UNSUPPORTED;
+    if (S == 0 || total_q == 0 || Hq == 0 || max_q == 0) return GDR_OK;
+    if (Hkv == 0 || Hq % Hkv != 0 || table_width == 0 || num_pages == 0) return GDR_ERR_INVALID_ARG;
+    if (!cu_q && (total_q != S || max_q != 1)) return GDR_ERR_INVALID_ARG;
+    if (!kv8_heads_ok(Hq, Hkv, total_q, S) || !fits31(table_width, page)) return GDR_ERR_UNSUPPORTED;
+    if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !kv_len || !out)
+        return GDR_ERR_INVALID_ARG;
+    if (!row_stride_ok(q_stride, Hq, D, dtype == GDR_DTYPE_F32 ? 4 : 2)) return GDR_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+        return GDR_ERR_INVALID_ARG;
+    const size_t need = gdr::kv8_attn_workspace_bytes(S, max_q, total_q, Hq, Hkv, D, elem_of(dtype));
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+        return GDR_ERR_INVALID_ARG;
+    return from_cuda(gdr::launch_kv8_attn(q, q_stride, k_cache, v_cache, k_scale, v_scale, block_table,
+                                          kv_len, cu_q, scale, out, lse, S, max_q, total_q, Hq, Hkv, D,
+                                          table_width, page, num_pages, elem_of(dtype), kv8_of(kv),
+                                          workspace, static_cast<cudaStream_t>(stream)));
 }
 
 gdr_status_t gdr_last_device_error(void *stream) {

@@ -12,6 +12,8 @@ namespace gdr {
 
 // Element type of q, k, v and out.
 enum class Elem { F32 = 0, BF16 = 1 };
+// Codes of the 8-bit paged cache.
+enum class Kv8 { E4M3 = 0, INT8 = 1 };
 
 // ---- staged chunked form (gdr_staged.cu) ----
 cudaError_t launch_decay(const float *g, float a_min, float *gamma, int BH, int T, int C,
@@ -183,6 +185,24 @@ cudaError_t launch_mla_decode(const void *q_abs, const void *ckv, const int *seq
                               const float *gate, float scale, void *out, int N, int H, int Lmax, int dh,
                               void *ws, cudaStream_t s);
 cudaError_t take_mla_error_word(unsigned *value);
+
+// ---- the 8-bit paged cache: plan (gdr_page.cu), append (gdr_kv8_append.cu), attention
+// (gdr_kv8_attn.cu); arguments as in include/gdr.h, N = num_pages, W = table_width ----
+size_t page_plan_smem(int S);
+cudaError_t launch_page_plan(const int *kv_len, const int *q_len, int *table, int *ring,
+                             const int *free_state, int *kv_out, int *cu_q, int *slots, int *positions,
+                             int *granted, int *state_out, int S, int W, int page, int N, int max_tokens,
+                             cudaStream_t s);
+cudaError_t launch_kv8_append(const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                              const int *slots, void *k_cache, void *v_cache, float *k_scale,
+                              float *v_scale, int T, int H, int D, int page, int N, Elem e, Kv8 kv,
+                              cudaStream_t s);
+size_t kv8_attn_workspace_bytes(int S, int max_q, int total_q, int Hq, int Hkv, int D, Elem e);
+cudaError_t launch_kv8_attn(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                            const float *k_scale, const float *v_scale, const int *table,
+                            const int *kv_len, const int *cu_q, float scale, void *out, float *lse, int S,
+                            int max_q, int total_q, int Hq, int Hkv, int D, int W, int page, int N, Elem e,
+                            Kv8 kv, void *ws, cudaStream_t s);
 
 // ---- the per-chunk gradients of the bf16 d = 128 chunk-64 backward on tcgen05
 // (gdr_bwd_tc.cu): Wt, Sb, dSb are the value-major bf16 tiles [BH][NC][128][64 / 128]

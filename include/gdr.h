@@ -516,6 +516,110 @@ gdr_status_t gdr_mla_decode(const void *q_abs, const void *ckv, const int *seqle
                             int H, int Lmax, int dc, int dh, void *workspace,
                             size_t workspace_bytes, void *stream);
 
+/* ---- the paged 8-bit cache of the exact-attention layers ----
+ *
+ * The layers interleaved with the incremental ones keep every token's keys and values.
+ * One serving step of such a layer is three calls: gdr_page_plan gives each new token a
+ * place, gdr_kv8_append quantises the new keys and values into it, gdr_kv8_attn attends
+ * over the whole cache (prompts, chunks of prompts, several drafted tokens, one token).
+ *
+ * The cache.  Pages of `page` tokens (16, 32, 64 or 128).  Codes, 8 bits each:
+ *   k_cache, v_cache  [num_pages][Hkv][page][D]      D = 64 or 128
+ * and one fp32 scale for each page and head:
+ *   k_scale, v_scale  [num_pages][Hkv]               value = code * scale
+ *   block_table       [S][table_width] int32         the pages of request s, in order
+ * num_pages * Hkv * page must be below 2^31.  k_cache, v_cache: 16-byte aligned.
+ */
+typedef enum {
+    GDR_KV8_E4M3 = 0,   /* 8-bit floats, 4 exponent and 3 mantissa bits, largest 448 */
+    GDR_KV8_INT8 = 1    /* integers -127 .. 127 */
+} gdr_kv8_t;
+
+/*
+ * Block tables and slot maps, on the device from the requests' lengths.
+ *   kv_len    [S]  tokens cached so far
+ *   q_len     [S]  new tokens of this step; negative: the request is finished and its
+ *                  ceil(kv_len / page) pages return to the free ring
+ *   block_table [S][table_width]  in/out: entries of the pages granted here are written
+ *                  (a finished request's row is left as it is)
+ *   free_ring [num_pages] in/out, free_state [2] = {head, count}: the free pages are
+ *                  free_ring[(head + i) % num_pages], i < count.  Pages are taken at the
+ *                  head; released ones go behind the last and can be taken from the next
+ *                  call on.
+ *   kv_len_out [S]  kv_len + q_len (0 for a finished request, kv_len if not granted);
+ *                   must not be kv_len or q_len itself
+ *   cu_q      [S+1] first new token of each request in the packed batch (at most max_tokens)
+ *   slots     [max_tokens] page * `page` + place of every new token; -1 past the last
+ *                   token and for requests that were not granted
+ *   positions [max_tokens] position of every new token in its request; -1 likewise
+ *   granted   [S]   1, or 0 for a request that does not fit (kv_len + q_len above
+ *                   table_width * page, or its tokens end past max_tokens) or for which no
+ *                   pages are left: requests are served in order, and one that finds too
+ *                   few pages ends the grants of all later ones that need any
+ *   free_state_out [2]  the ring's state after the call; must not be free_state itself
+ * Every output is a function of the inputs, so a step can be planned again with other
+ * requests.  One launch, no workspace.  Errors: S or max_tokens negative, table_width or
+ * num_pages < 1, null pointers, outputs that are inputs: GDR_ERR_INVALID_ARG; S > 8192,
+ * another page size, max_tokens > 2^30, num_pages * page, table_width * page or
+ * S * table_width >= 2^31: GDR_ERR_UNSUPPORTED.
+ */
+gdr_status_t gdr_page_plan(const int *kv_len, const int *q_len, int *block_table, int *free_ring,
+                           const int *free_state, int *kv_len_out, int *cu_q, int *slots,
+                           int *positions, int *granted, int *free_state_out, int S,
+                           int table_width, int page, int num_pages, int max_tokens, void *stream);
+
+/*
+ * Quantises T tokens' keys and values into the cache.
+ *   k, v      [T][Hkv][D] dtype, k_stride / v_stride elements between tokens (at least
+ *             Hkv * D; rows 16-byte aligned)
+ *   slots     [T] int32: page * `page` + place; a negative or too large slot drops the token.
+ *             Tokens of one page follow each other with ascending slots (as gdr_page_plan
+ *             makes them): the places before a run's first hold the page's earlier tokens,
+ *             the places after it nothing yet.  Two runs in one page are not supported.
+ * For each (page, head), keys and values apart: s_req is the least power of two with
+ * max |x| <= Q s_req over the new tokens' finite values (Q = 448 or 127), within [2^-40,
+ * 2^40].  A page that starts here gets scale s_req; otherwise max(old, s_req), and where
+ * that is larger than the old one the codes before the run are re-encoded (code * old /
+ * new, rounded to nearest even).  New codes are x / scale, rounded to nearest even; larger
+ * magnitudes (infinities) saturate, NaN gives 0.  One launch, no workspace.
+ */
+gdr_status_t gdr_kv8_append(const void *k, const void *v, int64_t k_stride, int64_t v_stride,
+                            const int *slots, void *k_cache, void *v_cache, float *k_scale,
+                            float *v_scale, int T, int Hkv, int D, int page, int num_pages,
+                            gdr_dtype_t dtype, gdr_kv8_t kv, void *stream);
+
+/*
+ * Attention of the last queries of S requests over their cached keys and values.
+ *   q         [total_q][Hq][D] dtype, q_stride elements between tokens (at least Hq * D;
+ *             rows 16-byte aligned); query head hq reads cached head hq / (Hq / Hkv)
+ *   kv_len    [S] tokens cached, the new ones included (at most table_width * page)
+ *   cu_q      [S+1] first query of each request, cu_q[0] = 0, cu_q[S] <= total_q; or NULL:
+ *             one query a request (max_q = 1, total_q = S)
+ *   max_q     the most queries any request has (it chooses the kernel, the result does not
+ *             depend on it)
+ *   scale     score scale, for example 1 / sqrt(D)
+ *   out       [total_q][Hq][D] dtype;  lse [total_q][Hq] fp32 or NULL
+ * Query i of a request with n queries and kv tokens sees keys j <= kv - n + i whose page is
+ * in the table: x_j = scale (q . k_j), o = sum_j softmax(x)_j v_j, lse = ln sum_j e^x_j.
+ * A table entry outside [0, num_pages) is a page that is gone: its tokens are not seen.
+ * A query that sees nothing gives o = 0 and lse = -inf.  Rows of q beyond cu_q[S] are not
+ * read and theirs of out not written.  What the pages hold past kv_len is never used.  Value
+ * codes of cached tokens must not be NaN (gdr_kv8_append writes none); value scales are
+ * taken within [2^-40, 2^40].
+ * Sums, maxima and the output accumulate in fp32; the weights meet the value codes in
+ * products of 11-bit operands (22-bit for fp32 q), the codes and bf16 q enter exactly.
+ *   workspace  16-byte aligned, gdr_kv8_attn_workspace_size bytes (0: may be NULL):
+ *             partial results of requests whose cache is split; scratch on entry and exit
+ */
+size_t gdr_kv8_attn_workspace_size(int S, int max_q, int total_q, int Hq, int Hkv, int D,
+                                   gdr_dtype_t dtype);
+gdr_status_t gdr_kv8_attn(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                          const float *k_scale, const float *v_scale, const int *block_table,
+                          const int *kv_len, const int *cu_q, float scale, void *out, float *lse,
+                          int S, int max_q, int total_q, int Hq, int Hkv, int D, int table_width,
+                          int page, int num_pages, gdr_dtype_t dtype, gdr_kv8_t kv,
+                          void *workspace, size_t workspace_bytes, void *stream);
+
 /*
  * Process-wide options, for tests and tuning.  Each takes effect for calls made
  * after it is set, on every thread; the defaults suit production use.
