@@ -642,7 +642,9 @@ cudaError_t read_and_clear_device_error(cudaStream_t s, unsigned *value) {
     if (e == cudaSuccess) e = take_bwd_tc_error_word(&t);
     unsigned r = 0;
     if (e == cudaSuccess) e = take_bwd_error_word(&r);
-    *value = a | b | c | d | f | m | t | r;
+    unsigned x = 0;
+    if (e == cudaSuccess) e = take_kv8_split_error_word(&x);
+    *value = a | b | c | d | f | m | t | r | x;
     return e;
 }
 

@@ -1,0 +1,303 @@
+// gdr_kv8_attn.cuh -- what the two attention kernels over the 8-bit paged cache share: their
+// arguments, the division of the work among CTAs, and the partial results of divided items.
+//
+// Work.  A request's n queries and the G = Hq / Hkv query heads of one cached head form
+// n * G rows (row r: query r / G, head r % G), which all read the same keys.  An item is a
+// block of RB such rows with the keys its last row sees, in units of UT tokens (an item that
+// sees nothing keeps one unit, which writes its zeros).  All units of a call, ordered by
+// (request, head, block, tokens), are divided evenly among the CTAs, whatever the requests'
+// lengths are: a CTA takes units [total c / G, total (c + 1) / G).  Lengths stay on the
+// device; every CTA finds its first unit by a prefix sum over the requests.
+//
+// An item that falls to several CTAs leaves in each an unnormalised partial result (fp32
+// sums, the reference exponent and the weight sum of every row) in the CTA's slot 1 (the CTA
+// where the item begins) or slot 0 (the ones after it), and the first CTA an entry that the
+// merge kernel follows.  The order of the merge is that of the tokens, so results repeat.
+#pragma once
+
+#include "gdr_fused_common.cuh"
+#include "gdr_kv8.cuh"
+
+namespace gdr {
+namespace {
+
+namespace kv8 {
+constexpr float kOff = 7.f;     // weights are 2^(x - M + kOff): room below 1 before a half loses bits
+constexpr float kTau = 8.f;     // M moves only when a score exceeds it by more than this
+constexpr float kVsMin = 9.094947017729282e-13f, kVsMax = 1.099511627776e12f;   // 2^-40, 2^40
+}  // namespace kv8
+
+struct AttnArgs {
+    const void *q;
+    int64_t q_stride;
+    const float *ks, *vs;
+    const int *table, *kv_len, *cu_q;
+    float scale_log2;            // score scale / ln 2
+    void *out;
+    float *lse;
+    float *part_o;               // [CTA][2][RB][D]
+    float *part_ml;              // [CTA][2][RB][2]: reference exponent M, weight sum
+    int4 *entry;                 // [CTA] {last CTA (-1: no divided item), request, head, block}
+    int S, total_q, Hq, Hkv, G, W, page_log2, N;
+    uint64_t limit_ns;
+};
+
+// One request, as every kernel reads it: offsets and lengths are clamped to the tensors.
+struct Request {
+    int q0, n, kv;
+};
+__device__ __forceinline__ Request request_of(const AttnArgs &a, int s) {
+    Request r;
+    r.kv = (int)min((int64_t)max(a.kv_len[s], 0), (int64_t)a.W << a.page_log2);
+    if (a.cu_q) {
+        r.q0 = min(max(a.cu_q[s], 0), a.total_q);
+        r.n = min(max(a.cu_q[s + 1], r.q0), a.total_q) - r.q0;
+    } else {
+        r.q0 = s;
+        r.n = 1;
+    }
+    return r;
+}
+// Keys that query i sees, and those that block b of RB rows does (its last row sees the most).
+__device__ __forceinline__ int seen_by(const Request &r, int i) { return max(0, min(r.kv, r.kv - r.n + i + 1)); }
+template <int RB>
+__device__ __forceinline__ int block_end(const AttnArgs &a, const Request &r, int b) {
+    return seen_by(r, (min(r.n * a.G, (b + 1) * RB) - 1) / a.G);
+}
+template <int RB>
+__device__ __forceinline__ int blocks_of(const AttnArgs &a, const Request &r) { return (r.n * a.G + RB - 1) / RB; }
+template <int UT>
+__device__ __forceinline__ int units_of(int end) { return max(1, (end + UT - 1) / UT); }
+template <int RB, int UT>
+__device__ __forceinline__ int64_t units_of_head(const AttnArgs &a, const Request &r) {
+    const int nb = blocks_of<RB>(a, r);
+    int64_t u = 0;
+    for (int b = 0; b < nb; ++b) u += units_of<UT>(block_end<RB>(a, r, b));
+    return u;
+}
+
+struct Place {      // a unit: request, head, block of rows, unit of the block's keys
+    int s, h, b, t;
+    int ctas;                // CTAs with work
+    int64_t u0, u1, total;   // this CTA's units, all units
+};
+
+// This CTA's units and the place of the first one.  All NT threads call it; `place` is in
+// shared memory and valid after it returns.
+template <int RB, int UT, int NT>
+__device__ __forceinline__ void find_place(const AttnArgs &a, Place *place, int64_t *s_scan) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int NW = NT / 32;
+    int64_t run = 0, mine = 0, before = 0, sum = 0;
+    // units before each request of a chunk of NT requests; the last chunk stays in registers
+    auto scan = [&](int base) {
+        const int s = base + tid;
+        mine = s < a.S ? units_of_head<RB, UT>(a, request_of(a, s)) * a.Hkv : 0;
+        int64_t incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += y;
+        }
+        __syncthreads();
+        if (lane == 31) s_scan[warp] = incl;
+        __syncthreads();
+        before = incl - mine;
+        sum = 0;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            if (w < warp) before += s_scan[w];
+            sum += s_scan[w];
+        }
+    };
+    int64_t total = 0;
+    for (int base = 0; base < a.S; base += NT) {
+        scan(base);
+        total += sum;
+    }
+    // fewer units than CTAs: one each, so that the parts of an item lie in consecutive CTAs
+    const int64_t ctas = min((int64_t)gridDim.x, max(total, (int64_t)1));
+    const int64_t u0 = blockIdx.x < ctas ? total * blockIdx.x / ctas : total;
+    const int64_t u1 = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : total;
+    if (tid == 0) {
+        place->u0 = u0;
+        place->u1 = u1;
+        place->total = total;
+        place->ctas = (int)ctas;
+    }
+    if (u0 < u1) {
+        for (int base = 0; base < a.S; base += NT) {
+            if (a.S > NT) scan(base);
+            if (u0 >= run + before && u0 < run + before + mine) {
+                const int s = base + tid;
+                const Request r = request_of(a, s);
+                int64_t rem = u0 - run - before;
+                const int64_t per = mine / a.Hkv;
+                place->s = s;
+                place->h = (int)(rem / per);
+                rem -= place->h * per;
+                int b = 0;
+                for (;; ++b) {
+                    const int u = units_of<UT>(block_end<RB>(a, r, b));
+                    if (rem < u) break;
+                    rem -= u;
+                }
+                place->b = b;
+                place->t = (int)rem;
+            }
+            run += sum;
+            if (u0 < run) break;
+        }
+    }
+    __syncthreads();
+}
+
+// The CTA that has unit u.
+__device__ __forceinline__ int cta_of(int64_t u, int64_t total, int ctas) {
+    return (int)(((u + 1) * ctas - 1) / total);
+}
+
+// Moves to the next item: next block, head, request with queries.
+template <int RB>
+__device__ __forceinline__ void next_item(const AttnArgs &a, int &s, int &h, int &b, Request &r) {
+    if (++b < blocks_of<RB>(a, r)) return;
+    b = 0;
+    if (++h < a.Hkv) return;
+    h = 0;
+    do {
+        if (++s >= a.S) return;
+        r = request_of(a, s);
+    } while (r.n == 0);
+}
+
+template <typename E> struct Vec16;   // 16 bytes of E as floats and back
+template <> struct Vec16<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void load(const float *p, float *f) {
+        const float4 u = *reinterpret_cast<const float4 *>(p);
+        f[0] = u.x, f[1] = u.y, f[2] = u.z, f[3] = u.w;
+    }
+    static __device__ __forceinline__ void store(float *p, const float *f) {
+        *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    }
+};
+template <> struct Vec16<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float *f) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *f) {
+        uint4 u;
+        u.x = pack_bf16x2(f[0], f[1]);
+        u.y = pack_bf16x2(f[2], f[3]);
+        u.z = pack_bf16x2(f[4], f[5]);
+        u.w = pack_bf16x2(f[6], f[7]);
+        *reinterpret_cast<uint4 *>(p) = u;
+    }
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 2^(m - ref) for exponents of partial results; 0 for a part that saw nothing.
+__device__ __forceinline__ float part_weight(float m, float ref) { return m == -INFINITY ? 0.f : ex2(m - ref); }
+
+// The power of two that brings a row of largest magnitude amax below 2^15, where a half
+// keeps 11 bits of everything that counts (bf16 values exactly, down to 2^-29 of the
+// largest); 1 for a row of zeros or with an infinity or NaN.
+__device__ __forceinline__ float row_factor(float amax) {
+    const int x = (int)(__float_as_uint(amax) >> 23) & 255;   // 2^(x - 127) <= amax
+    if (amax == 0.f || x == 255) return 1.f;
+    return __uint_as_float((uint32_t)(min(max(268 - x, 1), 254)) << 23);   // 2^(14 - (x - 127))
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// ------------------------------------------------------------------ merge of divided items
+// One CTA per (entry, row): its warps take the parts in turn, lanes the D values.
+template <typename E, int D, int RB>
+__global__ void __launch_bounds__(256) kv8_merge_kernel(const AttnArgs a) {
+    constexpr int NWM = 8, VL = D / 32;
+    __shared__ float s_o[NWM][D];
+    __shared__ float s_m[NWM], s_l[NWM];
+    grid_dependency_wait();
+    const int c0 = blockIdx.x, row = blockIdx.y;
+    const int4 en = a.entry[c0];
+    if (en.x < 0) return;
+    const Request r = request_of(a, en.y);
+    const int at = en.w * RB + row;
+    if (at >= r.n * a.G) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int parts = en.x - c0 + 1;
+    auto slot = [&](int p) { return ((int64_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * RB + row; };
+    float M = -INFINITY;
+    for (int p = warp; p < parts; p += NWM) M = fmaxf(M, a.part_ml[2 * slot(p)]);
+    if (lane == 0) s_m[warp] = M;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < NWM; ++w) M = fmaxf(M, s_m[w]);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float o[VL] = {}, l = 0.f;
+    for (int p = warp; p < parts; p += NWM) {
+        const int64_t k = slot(p);
+        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * k);
+        // a part whose scores are all NaN has no exponent but a NaN sum, which has to stay
+        const float w = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : ex2(ml.x - ref);
+        l = fmaf(w, ml.y, l);
+        const float *src = a.part_o + k * D + lane * VL;
+#pragma unroll
+        for (int e = 0; e < VL; ++e) o[e] = fmaf(w, src[e], o[e]);
+    }
+    if (lane == 0) s_l[warp] = l;
+#pragma unroll
+    for (int e = 0; e < VL; ++e) s_o[warp][lane * VL + e] = o[e];
+    __syncthreads();
+    if (warp != 0) return;
+    float L = 0.f;
+#pragma unroll
+    for (int w = 0; w < NWM; ++w) L += s_l[w];
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int hq = en.z * a.G + at % a.G;
+    const int64_t orow = (int64_t)(r.q0 + at / a.G) * a.Hq + hq;
+#pragma unroll
+    for (int e = 0; e < VL; ++e) {
+        float x = 0.f;
+#pragma unroll
+        for (int w = 0; w < NWM; ++w) x += s_o[w][lane * VL + e];
+        x *= inv;
+        if constexpr (sizeof(E) == 4)
+            static_cast<float *>(a.out)[orow * D + lane * VL + e] = x;
+        else
+            static_cast<__nv_bfloat16 *>(a.out)[orow * D + lane * VL + e] = __float2bfloat16_rn(x);
+    }
+    if (a.lse && lane == 0)
+        a.lse[orow] = L == 0.f ? -INFINITY : (ref - kv8::kOff + log2f(L)) * 0.693147180559945f;
+}
+
+template <typename E, int D, int RB>
+cudaError_t launch_merge(const AttnArgs &a, int ctas, int rows, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(rows < RB ? rows : RB));
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv8_merge_kernel<E, D, RB>, a);
+}
+
+}  // namespace
+}  // namespace gdr
