@@ -642,9 +642,10 @@ cudaError_t read_and_clear_device_error(cudaStream_t s, unsigned *value) {
     if (e == cudaSuccess) e = take_bwd_tc_error_word(&t);
     unsigned r = 0;
     if (e == cudaSuccess) e = take_bwd_error_word(&r);
-    unsigned x = 0;
+    unsigned x = 0, y = 0;
     if (e == cudaSuccess) e = take_kv8_split_error_word(&x);
-    *value = a | b | c | d | f | m | t | r | x;
+    if (e == cudaSuccess) e = take_kv8_tile_error_word(&y);
+    *value = a | b | c | d | f | m | t | r | x | y;
     return e;
 }
 

@@ -204,6 +204,15 @@ cudaError_t launch_kv8_attn(const void *q, int64_t q_stride, const void *k_cache
                             int max_q, int total_q, int Hq, int Hkv, int D, int W, int page, int N, Elem e,
                             Kv8 kv, void *ws, cudaStream_t s);
 cudaError_t take_kv8_split_error_word(unsigned *value);
+// The kernel for many bf16 query rows a cached head (gdr_kv8_tile.cu), in items of
+// kKv8TileRows rows.
+constexpr int kKv8TileRows = 256;
+cudaError_t launch_kv8_tile(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                            const float *k_scale, const float *v_scale, const int *table,
+                            const int *kv_len, const int *cu_q, float scale, void *out, float *lse, int S,
+                            int max_q, int total_q, int Hq, int Hkv, int D, int W, int page, int N, Kv8 kv,
+                            void *ws, cudaStream_t s);
+cudaError_t take_kv8_tile_error_word(unsigned *value);
 
 // ---- the per-chunk gradients of the bf16 d = 128 chunk-64 backward on tcgen05
 // (gdr_bwd_tc.cu): Wt, Sb, dSb are the value-major bf16 tiles [BH][NC][128][64 / 128]

@@ -111,23 +111,9 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     const int P = 1 << a.page_log2;
 
     // ---- loads: lane i < 2 brings tokens 16 i .. 16 i + 15 of the slab, a page entry ahead
-    struct Cursor {
-        int s, h, b, t, nt, end; // item, unit, the item's units and keys
-        Request r;
-    } ld;
-    auto enter = [&](Cursor &c) {
-        c.end = block_end<RB>(a, c.r, c.b);
-        c.nt = units_of<UT>(c.end);
-    };
-    ld.s = s_place.s, ld.h = s_place.h, ld.b = s_place.b, ld.t = s_place.t;
-    ld.r = request_of(a, ld.s);
-    enter(ld);
-    auto advance = [&](Cursor &c) {
-        if (++c.t < c.nt) return;
-        c.t = 0;
-        next_item<RB>(a, c.s, c.h, c.b, c.r);
-        if (c.s < a.S) enter(c);
-    };
+    using Cur = Cursor<RB, UT>;
+    Cur ld;
+    ld.start(a, s_place);
     int left = units, fill = 0;          // units to load, stage to fill
     int page = -1, page_h = 0;           // of the slab to be loaded next
     int pend = -1;                       // stage whose scales are on their way
@@ -165,7 +151,7 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         pend = fill;
         fill = fill == ST - 1 ? 0 : fill + 1;
         --left;
-        advance(ld);
+        ld.next_unit(a);
         look_up();
     };
     look_up();
@@ -174,16 +160,14 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     __syncwarp();
 
     // ---- the items
-    Cursor c;
-    c.s = s_place.s, c.h = s_place.h, c.b = s_place.b, c.t = s_place.t;
-    c.r = request_of(a, c.s);
+    Cur c;
+    c.start(a, s_place);
     bool ok = true;
     int stage = 0;
     uint32_t phase = 0;
     int waited = 0;
 #pragma unroll 1
     for (int done = 0; done < units;) {
-        enter(c);
         const int t_first = c.t, t_last = min(c.nt, t_first + units - done);   // this CTA's units of the item
         const int rows = min(RB, c.r.n * a.G - c.b * RB);
         // query fragments: rows g and g + 8, values LD t4 .. LD t4 + LD - 1, word j of a key
@@ -212,8 +196,8 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             for (int v = 0; v < LD; ++v) amax = fmaxf(amax, fabsf(f[v]));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            const float fac = row_factor(amax);
-            cs[e] = a.scale_log2 * (1.f / fac);
+            const float fac = row_factor(amax) * a.sign;
+            cs[e] = a.scale_log2 * fabsf(1.f / fac);
 #pragma unroll
             for (int j = 0; j < NKS; ++j) {
                 const float x0 = f[4 * j] * fac, x1 = f[4 * j + 1] * fac, x2 = f[4 * j + 2] * fac, x3 = f[4 * j + 3] * fac;
@@ -301,18 +285,20 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const int tk = tok0 + 8 * i + 2 * t4 + (e & 1);
-                            // a factor of either sign: the masked score goes through the exponent below
                             if (tk >= lim[e >> 1] || vsc[i >> 1] < 0.f) x[i][e] = __int_as_float(0xff800000);
                         }
                 }
-                float mx[2] = {-INFINITY, -INFINITY};
+                float mx[2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int e = 0; e < 2; ++e) {
+                    float m[2];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float y = x[i][e] == -INFINITY ? -INFINITY : fmaf(x[i][e], kf[e >> 1][i >> 1], ev[i >> 1]);
-                        mx[e >> 1] = fmaxf(mx[e >> 1], y);
-                    }
+                    for (int i = 0; i < 2; ++i)
+                        m[i] = fmaxf(fmaxf(x[2 * i][2 * e], x[2 * i][2 * e + 1]),
+                                     fmaxf(x[2 * i + 1][2 * e], x[2 * i + 1][2 * e + 1]));
+                    mx[e] = fmaxf(m[0] == -INFINITY ? -INFINITY : fmaf(m[0], kf[e][0], ev[0]),
+                                  m[1] == -INFINITY ? -INFINITY : fmaf(m[1], kf[e][1], ev[1]));
+                }
                 if (__any_sync(0xffffffffu, mx[0] > M[0] + kv8::kTau || mx[1] > M[1] + kv8::kTau)) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
@@ -488,8 +474,7 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             __syncthreads();
         }
         done += t_last - t_first;
-        c.t = 0;
-        if (done < units) next_item<RB>(a, c.s, c.h, c.b, c.r);
+        c.next_of_item(a);
     }
     if (!ok) {   // leave no copy in flight
         entry.x = -1;
@@ -513,16 +498,6 @@ bool make_cache_map(CUtensorMap *m, const void *ptr, int64_t tokens, int D) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-int sm_count() {
-    int dev = 0, sms = 152;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        sms = 152;
-    }
-    return sms;
-}
-
 template <typename E, Kv8 KV, int D>
 cudaError_t launch_split(const AttnArgs &a, const void *kc, const void *vc, int ctas, int rows, cudaStream_t s) {
     CUtensorMap mk, mv;
@@ -533,29 +508,34 @@ cudaError_t launch_split(const AttnArgs &a, const void *kc, const void *vc, int 
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)ctas, sp::NT, sp::SMEM<D>, s>>>(mk, mv, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_merge<E, D, sp::RB>(a, ctas, rows, s);
-}
-
-size_t part_bytes(int ctas, int RB, int D) {   // entries, then {M, l}, then the sums
-    return (size_t)ctas * (sizeof(int4) + (size_t)2 * RB * (2 + D) * sizeof(float));
+    return launch_merge<E, D, sp::RB, 8>(a, ctas, rows, s);
 }
 
 }  // namespace
 
-size_t kv8_attn_workspace_bytes(int, int, int, int, int, int D, Elem) { return part_bytes(2 * sm_count(), sp::RB, D); }
+// Rows of a cached head that the split kernel takes; bf16 with more goes to the tile kernel.
+// At 16 rows the split kernel's MMAs are full; beyond, it reads the cache once for every 16 rows (5 drafted tokens x 8 heads at 16 k keys: 421 us against TILE_US).
+bool kv8_tiles(int max_q, int G, Elem e) { return e == Elem::BF16 && (int64_t)max_q * G > sp::RB; }
+
+size_t kv8_attn_workspace_bytes(int, int max_q, int, int Hq, int Hkv, int D, Elem e) {
+    return kv8_tiles(max_q, Hq / Hkv, e) ? part_bytes(sm_count(), kKv8TileRows, D)
+                                         : part_bytes(2 * sm_count(), sp::RB, D);
+}
 
 cudaError_t launch_kv8_attn(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
                             const float *k_scale, const float *v_scale, const int *table,
                             const int *kv_len, const int *cu_q, float scale, void *out, float *lse, int S,
                             int max_q, int total_q, int Hq, int Hkv, int D, int W, int page, int N, Elem e,
                             Kv8 kv, void *ws, cudaStream_t s) {
+    if (kv8_tiles(max_q, Hq / Hkv, e))
+        return launch_kv8_tile(q, q_stride, k_cache, v_cache, k_scale, v_scale, table, kv_len, cu_q, scale, out,
+                               lse, S, max_q, total_q, Hq, Hkv, D, W, page, N, kv, ws, s);
     const int ctas = 2 * sm_count();
     AttnArgs a{};
     a.q = q, a.q_stride = q_stride, a.ks = k_scale, a.vs = v_scale, a.table = table, a.kv_len = kv_len;
-    a.cu_q = cu_q, a.scale_log2 = scale * 1.4426950408889634f, a.out = out, a.lse = lse;
-    a.entry = static_cast<int4 *>(ws);
-    a.part_ml = reinterpret_cast<float *>(a.entry + ctas);
-    a.part_o = a.part_ml + (size_t)ctas * 2 * sp::RB * 2;
+    a.cu_q = cu_q, a.scale_log2 = fabsf(scale) * 1.4426950408889634f, a.sign = scale < 0.f ? -1.f : 1.f;
+    a.out = out, a.lse = lse;
+    place_parts(a, ws, ctas, sp::RB);
     a.S = S, a.total_q = total_q, a.Hq = Hq, a.Hkv = Hkv, a.G = Hq / Hkv, a.W = W, a.N = N;
     a.page_log2 = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
     a.limit_ns = wait_limit_ns();

@@ -32,7 +32,9 @@ struct AttnArgs {
     int64_t q_stride;
     const float *ks, *vs;
     const int *table, *kv_len, *cu_q;
-    float scale_log2;            // score scale / ln 2
+    float scale_log2;            // |score scale| / ln 2; its sign goes into the queries, so that
+    float sign;                  // a larger product is a larger score (cache scales are positive)
+    const uint8_t *kc, *vc;
     void *out;
     float *lse;
     float *part_o;               // [CTA][2][RB][D]
@@ -170,6 +172,30 @@ __device__ __forceinline__ void next_item(const AttnArgs &a, int &s, int &h, int
     } while (r.n == 0);
 }
 
+// A role's way through this CTA's units.
+template <int RB, int UT>
+struct Cursor {
+    int s, h, b, t, nt, end;     // item, unit, the item's units and keys
+    Request r;
+    __device__ __forceinline__ void enter(const AttnArgs &a) {
+        end = block_end<RB>(a, r, b);
+        nt = units_of<UT>(end);
+    }
+    __device__ __forceinline__ void start(const AttnArgs &a, const Place &p) {
+        s = p.s, h = p.h, b = p.b, t = p.t;
+        r = request_of(a, s);
+        enter(a);
+    }
+    __device__ __forceinline__ void next_of_item(const AttnArgs &a) {   // past the last item: s = S
+        t = 0;
+        next_item<RB>(a, s, h, b, r);
+        if (s < a.S) enter(a);
+    }
+    __device__ __forceinline__ void next_unit(const AttnArgs &a) {
+        if (++t == nt) next_of_item(a);
+    }
+};
+
 template <typename E> struct Vec16;   // 16 bytes of E as floats and back
 template <> struct Vec16<float> {
     static constexpr int N = 4;
@@ -225,70 +251,73 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
 }
 
 // ------------------------------------------------------------------ merge of divided items
-// One CTA per (entry, row): its warps take the parts in turn, lanes the D values.
-template <typename E, int D, int RB>
+// WPR warps take one row: each the parts in turn, lanes the D values.
+template <typename E, int D, int RB, int WPR>
 __global__ void __launch_bounds__(256) kv8_merge_kernel(const AttnArgs a) {
-    constexpr int NWM = 8, VL = D / 32;
-    __shared__ float s_o[NWM][D];
-    __shared__ float s_m[NWM], s_l[NWM];
+    constexpr int RPC = 8 / WPR, VL = D / 32;    // rows a CTA
+    __shared__ float s_o[8][D];
+    __shared__ float s_l[8];
     grid_dependency_wait();
-    const int c0 = blockIdx.x, row = blockIdx.y;
+    const int c0 = blockIdx.x;
     const int4 en = a.entry[c0];
     if (en.x < 0) return;
     const Request r = request_of(a, en.y);
-    const int at = en.w * RB + row;
-    if (at >= r.n * a.G) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int parts = en.x - c0 + 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w0 = warp / WPR * WPR;
+    const int row = blockIdx.y * RPC + warp / WPR, at = en.w * RB + row;
+    const bool live = row < RB && at < r.n * a.G;
+    const int parts = live ? en.x - c0 + 1 : 0;
     auto slot = [&](int p) { return ((int64_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * RB + row; };
     float M = -INFINITY;
-    for (int p = warp; p < parts; p += NWM) M = fmaxf(M, a.part_ml[2 * slot(p)]);
-    if (lane == 0) s_m[warp] = M;
-    __syncthreads();
+    for (int p = lane; p < parts; p += 32) M = fmaxf(M, a.part_ml[2 * slot(p)]);
 #pragma unroll
-    for (int w = 0; w < NWM; ++w) M = fmaxf(M, s_m[w]);
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
     const float ref = M == -INFINITY ? 0.f : M;
     float o[VL] = {}, l = 0.f;
-    for (int p = warp; p < parts; p += NWM) {
+#pragma unroll 4
+    for (int p = warp - w0; p < parts; p += WPR) {
         const int64_t k = slot(p);
         const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * k);
-        // a part whose scores are all NaN has no exponent but a NaN sum, which has to stay
-        const float w = ml.x == -INFINITY && ml.y == 0.f ? 0.f : ml.x == -INFINITY ? 1.f : ex2(ml.x - ref);
+        // a part without an exponent weighs 0; if its sums are NaN (all its scores are) they stay NaN
+        const float w = part_weight(ml.x, ref);
         l = fmaf(w, ml.y, l);
         const float *src = a.part_o + k * D + lane * VL;
 #pragma unroll
         for (int e = 0; e < VL; ++e) o[e] = fmaf(w, src[e], o[e]);
     }
-    if (lane == 0) s_l[warp] = l;
+    if constexpr (WPR > 1) {
+        if (lane == 0) s_l[warp] = l;
 #pragma unroll
-    for (int e = 0; e < VL; ++e) s_o[warp][lane * VL + e] = o[e];
-    __syncthreads();
-    if (warp != 0) return;
-    float L = 0.f;
+        for (int e = 0; e < VL; ++e) s_o[warp][lane * VL + e] = o[e];
+        __syncthreads();
+        if (warp != w0) return;
+        l = 0.f;
 #pragma unroll
-    for (int w = 0; w < NWM; ++w) L += s_l[w];
-    const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int hq = en.z * a.G + at % a.G;
-    const int64_t orow = (int64_t)(r.q0 + at / a.G) * a.Hq + hq;
+        for (int w = 0; w < WPR; ++w) l += s_l[w0 + w];
+#pragma unroll
+        for (int e = 0; e < VL; ++e) {
+            o[e] = 0.f;
+#pragma unroll
+            for (int w = 0; w < WPR; ++w) o[e] += s_o[w0 + w][lane * VL + e];
+        }
+    }
+    if (!live) return;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int64_t orow = (int64_t)(r.q0 + at / a.G) * a.Hq + en.z * a.G + at % a.G;
 #pragma unroll
     for (int e = 0; e < VL; ++e) {
-        float x = 0.f;
-#pragma unroll
-        for (int w = 0; w < NWM; ++w) x += s_o[w][lane * VL + e];
-        x *= inv;
         if constexpr (sizeof(E) == 4)
-            static_cast<float *>(a.out)[orow * D + lane * VL + e] = x;
+            static_cast<float *>(a.out)[orow * D + lane * VL + e] = o[e] * inv;
         else
-            static_cast<__nv_bfloat16 *>(a.out)[orow * D + lane * VL + e] = __float2bfloat16_rn(x);
+            static_cast<__nv_bfloat16 *>(a.out)[orow * D + lane * VL + e] = __float2bfloat16_rn(o[e] * inv);
     }
-    if (a.lse && lane == 0)
-        a.lse[orow] = L == 0.f ? -INFINITY : (ref - kv8::kOff + log2f(L)) * 0.693147180559945f;
+    if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : (ref - kv8::kOff + log2f(l)) * 0.693147180559945f;
 }
 
-template <typename E, int D, int RB>
+template <typename E, int D, int RB, int WPR>
 cudaError_t launch_merge(const AttnArgs &a, int ctas, int rows, cudaStream_t s) {
+    constexpr int RPC = 8 / WPR;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(rows < RB ? rows : RB));
+    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(((rows < RB ? rows : RB) + RPC - 1) / RPC));
     cfg.blockDim = dim3(256);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -296,7 +325,27 @@ cudaError_t launch_merge(const AttnArgs &a, int ctas, int rows, cudaStream_t s) 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv8_merge_kernel<E, D, RB>, a);
+    return cudaLaunchKernelEx(&cfg, kv8_merge_kernel<E, D, RB, WPR>, a);
+}
+
+// Entries, then {M, l}, then the sums.
+size_t part_bytes(int ctas, int RB, int D) {
+    return (size_t)ctas * (sizeof(int4) + (size_t)2 * RB * (2 + D) * sizeof(float));
+}
+void place_parts(AttnArgs &a, void *ws, int ctas, int RB) {
+    a.entry = static_cast<int4 *>(ws);
+    a.part_ml = reinterpret_cast<float *>(a.entry + ctas);
+    a.part_o = a.part_ml + (size_t)ctas * 2 * RB * 2;
+}
+
+int sm_count() {
+    int dev = 0, sms = 152;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        sms = 152;
+    }
+    return sms;
 }
 
 }  // namespace
