@@ -56,6 +56,24 @@ __device__ __forceinline__ uint32_t decode2_h(uint32_t c) {
     const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&b), __float2half2_rn(1152.f));
     return *reinterpret_cast<const uint32_t *>(&r);
 }
+// The halves of the four codes of a word.
+template <Kv8 KV>
+__device__ __forceinline__ void decode4_h(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if (KV == Kv8::E4M3) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
+    } else {
+        const uint32_t c = w ^ 0x80808080u;
+        const uint32_t b0 = __byte_perm(c, 0x64646464u, 0x4140), b1 = __byte_perm(c, 0x64646464u, 0x4342);
+        const __half2 off = __float2half2_rn(1152.f);
+        const __half2 r0 = __hsub2(*reinterpret_cast<const __half2 *>(&b0), off);
+        const __half2 r1 = __hsub2(*reinterpret_cast<const __half2 *>(&b1), off);
+        lo = *reinterpret_cast<const uint32_t *>(&r0);
+        hi = *reinterpret_cast<const uint32_t *>(&r1);
+    }
+}
 template <Kv8 KV>
 __device__ __forceinline__ float2 decode2(uint32_t c) {
     const uint32_t h = decode2_h<KV>(c);

@@ -514,7 +514,9 @@ cudaError_t launch_split(const AttnArgs &a, const void *kc, const void *vc, int 
 }  // namespace
 
 // Rows of a cached head that the split kernel takes; bf16 with more goes to the tile kernel.
-// At 16 rows the split kernel's MMAs are full; beyond, it reads the cache once for every 16 rows (5 drafted tokens x 8 heads at 16 k keys: 421 us against TILE_US).
+// At 16 rows the split kernel's MMAs are full; beyond, it reads the cache once for every 16
+// rows (5 drafted tokens x 8 heads on 16 k keys 0.42 ms against 0.33 ms here, a chunk of 1000
+// tokens on 65 k 7.3 ms against 1.5 ms).
 bool kv8_tiles(int max_q, int G, Elem e) { return e == Elem::BF16 && (int64_t)max_q * G > sp::RB; }
 
 size_t kv8_attn_workspace_bytes(int, int max_q, int, int Hq, int Hkv, int D, Elem e) {

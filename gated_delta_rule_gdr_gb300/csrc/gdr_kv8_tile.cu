@@ -9,15 +9,20 @@
 // is two tiles of 128 rows (row = query x group of heads) that share every key, a unit 128
 // keys.  A tile's scores S (128 x 128 fp32) and sums O live in TMEM; its weights go back over
 // S as halves and are the A operand of the second product from there, so that they never
-// touch shared memory.  While the softmax of one tile runs, the products of the other do.
+// touch shared memory.
 // The codes come by bulk copies (a page's block of a head is contiguous) and are widened to
 // halves in the tensor core's swizzled layout: keys K-major, values MN-major from the same
 // [token][64 values] rows, so values need no transpose.
 //
+// Two forms.  PAIR (items of 256 rows): two tiles of different rows share every key, the
+// softmax of one runs under the products of the other.  Otherwise (items of at most 128
+// rows, where the cache's bytes bound): one tile of rows, whose units alternate between the
+// two score and output buffers; the two halves of the sum are joined at the item's end.
+//
 // Warps: 0 loads (page entries and scales looked up one unit ahead), 1 issues the products
-// and owns the TMEM, 4-7 widen, 8-11 and 12-15 the softmax of tile 0 and 1, a thread a row:
-// maxima and sums never leave the thread.  Rings: 4 raw slots and 3 widened ones, each taking
-// keys and values in turn.  No barrier spans the CTA inside the loop; every wait is bounded.
+// and owns the TMEM, 4-7 widen, 8-11 and 12-15 the softmax of buffer 0 and 1, a thread a row:
+// maxima and sums never leave the thread.  No barrier spans the CTA inside the loop; every
+// wait is bounded.
 
 #include "gdr_kv8_attn.cuh"
 
@@ -28,24 +33,64 @@ namespace {
 
 namespace tl {
 constexpr int NT = 512;
-constexpr int RB = kKv8TileRows, TR = 128, UT = 128;   // rows of an item and a tile, keys of a unit
-constexpr int NRAW = 4, NCV = 3, NSC = 4;              // raw slots, widened slots, scale slots
-template <int D> constexpr uint32_t RAW = UT * D;                    // a raw slot
-template <int D> constexpr uint32_t CV = UT * D * 2;                 // a widened slot
-constexpr uint32_t SLAB = 128 * 128;                                 // 128 rows x 64 halves
-template <int D> constexpr uint32_t OFF_Q = 0;                       // two tiles
-template <int D> constexpr uint32_t OFF_CV = 2 * TR * D * 2;
-template <int D> constexpr uint32_t OFF_RAW = OFF_CV<D> + NCV * CV<D>;
-template <int D> constexpr uint32_t OFF_SC = OFF_RAW<D> + NRAW * RAW<D>;   // [NSC][8 groups]{ks, vs, log2 vs, 1/vs}
-template <int D> constexpr uint32_t SMEM = OFF_SC<D> + NSC * 8 * 16 + 1024;
-static_assert(SMEM<128> + 512 <= 232448, "exceeds 227 KB of shared memory per CTA");
-constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;              // tile t at + 128 t
+constexpr int TR = 128, UT = 128;                // rows of a tile, keys of a unit
+constexpr int NRAW = 4, NSC = 4;                 // raw slots (keys and values in turn), scale slots
+constexpr uint32_t SLAB = 128 * 128;             // 128 rows x 64 halves
+constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;   // buffer b at + 128 b
+constexpr int MAXCV = 4;
 enum : int {
-    B_RAWFULL = 0, B_RAWFREE = B_RAWFULL + NRAW, B_CVFULL = B_RAWFREE + NRAW, B_CVFREE = B_CVFULL + NCV,
-    B_SC = B_CVFREE + NCV, B_Q = B_SC + NSC, B_S = B_Q + 2, B_P = B_S + 2, B_O = B_P + 2, B_DRAIN = B_O + 2,
-    NUM_BARS = B_DRAIN + 1
+    B_RAWFULL = 0, B_RAWFREE = B_RAWFULL + NRAW, B_CVFULL = B_RAWFREE + NRAW, B_CVFREE = B_CVFULL + MAXCV,
+    B_SC = B_CVFREE + MAXCV, B_Q = B_SC + NSC, B_S = B_Q + 2, B_P = B_S + 2, B_O = B_P + 2, B_ML = B_O + 2,
+    B_OFREE = B_ML + 1, B_DRAIN = B_OFREE + 1, NUM_BARS = B_DRAIN + 1
+};
+template <int D, bool PAIR> struct Lay {
+    static constexpr int RB = PAIR ? kKv8TileRows : TR;   // rows of an item
+    static constexpr int NCV = PAIR ? 3 : 4;              // widened slots
+    static constexpr uint32_t RAW = UT * D, CV = UT * D * 2;
+    static constexpr uint32_t OFF_Q = 0;                  // one tile, or two
+    static constexpr uint32_t OFF_CV = (PAIR ? 2 : 1) * TR * D * 2;
+    static constexpr uint32_t OFF_RAW = OFF_CV + NCV * CV;
+    static constexpr uint32_t OFF_SC = OFF_RAW + NRAW * RAW;     // [NSC][8 groups]{ks, vs, log2 vs, 1/vs}
+    static constexpr uint32_t OFF_ML = OFF_SC + NSC * 8 * 16;    // [TR]{M, l} of buffer 1 (not PAIR)
+    static constexpr uint32_t SMEM = OFF_ML + (PAIR ? 0 : TR * 8);   // 1024-byte aligned by its declaration
+    static_assert(SMEM + 1024 <= 232448, "exceeds 227 KB of shared memory per CTA");
 };
 }  // namespace tl
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// One lane of a converged warp (always the same one).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 
 // Instruction descriptor of kind::f16 with half A and B and an fp32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_f16(int M, int N, bool b_mn) {
@@ -69,22 +114,200 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         : "memory");
 }
 
-template <Kv8 KV, int D>
+// A query row of the item that block b of RB rows is: its place in q and out, and how many
+// keys it sees.
+struct TileRow {
+    int qrow, hq, lim;
+    bool live;
+};
+template <int RB>
+__device__ __forceinline__ TileRow tile_row(const AttnArgs &a, const Cursor<RB, tl::UT> &c, int lr) {
+    TileRow t;
+    const int at = c.b * RB + lr;
+    t.live = lr < RB && at < c.r.n * a.G;
+    const int i = t.live ? at / a.G : 0;
+    t.qrow = c.r.q0 + i;
+    t.hq = c.h * a.G + (t.live ? at - i * a.G : 0);
+    t.lim = t.live ? seen_by(c.r, i) : 0;
+    return t;
+}
+
+// The row's query, normalised, as a row of the K-major tile at `dst` (nullptr: not stored).
+// Returns the row's score factor.
+template <int D>
+__device__ __forceinline__ float stage_query(const AttnArgs &a, const TileRow &t, int row, uint8_t *dst) {
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + (int64_t)t.qrow * a.q_stride + (int64_t)t.hq * D;
+    float amax = 0.f;
+    auto piece = [&](int i) { return t.live ? reinterpret_cast<const uint4 *>(q)[i] : make_uint4(0, 0, 0, 0); };
+#pragma unroll 4
+    for (int i = 0; i < D / 8; ++i) {
+        const uint4 u = piece(i);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+    }
+    const float fac = row_factor(amax) * a.sign;
+    if (dst) {
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+            const uint4 u = piece(i);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            uint32_t h[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                h[e] = pack_h2(__uint_as_float(w[e] << 16) * fac, __uint_as_float(w[e] & 0xffff0000u) * fac);
+            *reinterpret_cast<uint4 *>(dst + (uint32_t)(i >> 3) * tl::SLAB + (uint32_t)row * 128u +
+                                       (((uint32_t)(i & 7) ^ (uint32_t)(row & 7)) << 4)) =
+                make_uint4(h[0], h[1], h[2], h[3]);
+        }
+    }
+    return a.scale_log2 * fabsf(1.f / fac);
+}
+
+// One unit of one row: scores from TMEM, the weights as halves in their upper columns
+// (kP on), M and l moved on.  The maximum is taken half by half; the upper half stays in
+// registers, whose weights then go over it, and the lower half is read a second time: half
+// the registers of holding all 128 scores for one TMEM read more.
+// see: keys of the unit that the row sees; part: some row of the warp sees fewer than all, or
+// a page is gone; rescale: the output buffer holds sums of earlier units.
+constexpr uint32_t kP = 64;
+struct RowUnit {
+    const float4 *sc;
+    int see;
+    bool part;
+    float cs;
+};
+__device__ __forceinline__ void load_half(uint32_t ts, int h, const RowUnit &u, float (&v)[2][32]) {
+    tmem_ld32(ts + 64u * h, v[0]);
+    tmem_ld32(ts + 64u * h + 32u, v[1]);
+    tmem_wait_ld();
+    if (u.part) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int n = u.sc[4 * h + i].y < 0.f ? 0 : u.see - 64 * h - 16 * i;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (e >= n) v[i >> 1][16 * (i & 1) + e] = -INFINITY;
+        }
+    }
+}
+// A factor of at least 2^-126 keeps masked scores at -inf where a scale is zero.
+__device__ __forceinline__ float unit_factor(float cs, float ks) { return fmaxf(cs * ks, 1.2e-38f); }
+__device__ __forceinline__ float half_max(const float (&v)[2][32], int h, const RowUnit &u, float mx) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float *x = &v[i >> 1][16 * (i & 1)];
+        float m = fmaxf(fmaxf(x[0], x[1]), x[2]);
+#pragma unroll
+        for (int e = 3; e < 15; e += 2) m = fmaxf(fmaxf(m, x[e]), x[e + 1]);
+        m = fmaxf(m, x[15]);
+        const float4 s4 = u.sc[4 * h + i];
+        mx = fmaxf(mx, fmaf(m, unit_factor(u.cs, s4.x), s4.z));
+    }
+    return mx;
+}
+__device__ __forceinline__ float half_weights(uint32_t ts, int h, const RowUnit &u, const float (&v)[2][32], float ref,
+                                              float l) {
+#pragma unroll
+    for (int cb = 0; cb < 2; ++cb) {
+        uint32_t p[16];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float4 s4 = u.sc[4 * h + 2 * cb + i];
+            const float kf = unit_factor(u.cs, s4.x), add = s4.z + ref;
+            const uint64_t kf2 = f2_pack(kf, kf), add2 = f2_pack(add, add);
+            uint64_t sum = 0;
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+                float p0, p1;
+                f2_unpack(f2_fma(f2_pack(v[cb][16 * i + e], v[cb][16 * i + e + 1]), kf2, add2), p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                sum = f2_add(sum, f2_pack(p0, p1));
+                p[8 * i + (e >> 1)] = pack_h2(p0, p1);
+            }
+            float s0, s1;
+            f2_unpack(sum, s0, s1);
+            l = fmaf(s0 + s1, s4.w, l);
+        }
+        tmem_st16(ts + kP + 32u * h + 16u * cb, p);
+    }
+    return l;
+}
+template <int D>
+__device__ __forceinline__ void softmax_unit(uint32_t ts, uint32_t to, const RowUnit &u, bool rescale, float &M, float &l) {
+    float v[2][32];
+    load_half(ts, 0, u, v);
+    float mx = half_max(v, 0, u, -INFINITY);
+    load_half(ts, 1, u, v);
+    mx = half_max(v, 1, u, mx);
+    if (__any_sync(0xffffffffu, mx > M + kv8::kTau)) {
+        const float m = fmaxf(M, ceilf(mx)), w = part_weight(M, m);
+        M = m;
+        l *= w;
+        if (rescale) {      // their products have landed: the scores' barrier came after them
+#pragma unroll 1
+            for (int cb = 0; cb < D / 8; ++cb) {     // few registers: the upper scores are held too
+                uint32_t o[8];
+                tmem_ld8(to + 8u * cb, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w);
+                tmem_st8(to + 8u * cb, o);
+            }
+        }
+    }
+    const float ref = kv8::kOff - (M == -INFINITY ? 0.f : M);
+    l = half_weights(ts, 1, u, v, ref, l);
+    load_half(ts, 0, u, v);
+    l = half_weights(ts, 0, u, v, ref, l);
+    tmem_wait_st();
+}
+
+// A row's result: the output, or the part that the merge kernel joins.
+template <int D, int RB>
+__device__ __forceinline__ void write_chunk(const AttnArgs &a, const TileRow &t, bool whole, int64_t slot, int cb,
+                                            float inv, float (&o)[32]) {
+    if (!t.live) return;
+    if (whole) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] *= inv;
+        __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)t.qrow * a.Hq + t.hq) * D + 32 * cb;
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) Vec16<__nv_bfloat16>::store(dst + e, o + e);
+    } else {
+        float *dst = a.part_o + slot * D + 32 * cb;
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) Vec16<float>::store(dst + e, o + e);
+    }
+}
+__device__ __forceinline__ void write_stats(const AttnArgs &a, const TileRow &t, bool whole, int64_t slot, float M, float l) {
+    if (!t.live) return;
+    if (!whole)
+        *reinterpret_cast<float2 *>(a.part_ml + 2 * slot) = make_float2(M, l);
+    else if (a.lse)
+        a.lse[(int64_t)t.qrow * a.Hq + t.hq] =
+            l == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) - kv8::kOff + log2f(l)) * 0.693147180559945f;
+}
+
+template <Kv8 KV, int D, bool PAIR>
 __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
     using namespace tl;
+    using L = Lay<D, PAIR>;
+    constexpr int RB = L::RB, NCV = L::NCV, NSL = D / 64;
     using Cur = Cursor<RB, UT>;
-    constexpr int NSL = D / 64;            // slabs of 64 values
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     __shared__ __align__(8) uint64_t s_bar[NUM_BARS];
     __shared__ Place s_place;
     __shared__ int64_t s_scan[NT / 32];
     __shared__ uint32_t s_tmem;
+    __shared__ int s_gone[NSC];
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto bar = [&](int i) { return smem_u32(&s_bar[i]); };
-    float4 *s_sc = reinterpret_cast<float4 *>(sm + OFF_SC<D>);
+    float4 *s_sc = reinterpret_cast<float4 *>(sm + L::OFF_SC);
     const int P = 1 << a.page_log2;
 
     if (tid == 0) {
@@ -103,6 +326,8 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
             mbar_init(bar(B_P + i), 4);
             mbar_init(bar(B_O + i), 1);
         }
+        mbar_init(bar(B_ML), 4);
+        mbar_init(bar(B_OFREE), 4);
         mbar_init(bar(B_DRAIN), 1);
         s_abort = 0;
         fence_mbar_init();
@@ -126,374 +351,356 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
     const uint32_t tmem = s_tmem;
     auto wait = [&](int b, uint32_t parity) { return role_wait(bar(b), parity & 1u, a.limit_ns, &s_abort); };
     auto warp_wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
-    auto tiles_of = [&](const Cur &c) { return c.r.n * a.G - c.b * RB > TR ? 2 : 1; };
+    auto tiles_of = [&](const Cur &c) { return PAIR && c.r.n * a.G - c.b * RB > TR ? 2 : 1; };
 
-    if (warp == 0) {
-        // ================================================================ loads
-        // Lane i < 8 has keys 16 i .. 16 i + 15 of the unit; the first lane of a page copies it.
-        Cur c;
-        c.start(a, s_place);
-        int page = -1;
-        auto look_up = [&]() {
-            page = -1;
-            const int tok = c.t * UT + 16 * lane;
-            if (lane < 8 && tok < c.r.kv) page = a.table[(int64_t)c.s * a.W + (tok >> a.page_log2)];
-        };
-        look_up();
-        bool ok = true;
-        int x = 0, pend = -1;
-        float pk = 0.f, pv = 0.f;
-        auto publish = [&]() {     // the scales of a unit, once they are here
-            if (pend < 0) return;
-            if (lane < 8)
-                s_sc[(pend % NSC) * 8 + lane] = pv < 0.f ? make_float4(0.f, -1.f, 0.f, 0.f)
-                                                         : make_float4(pk, pv, log2f(pv), 1.f / pv);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_SC + pend % NSC));
-            pend = -1;
-        };
-#pragma unroll 1
-        for (int k = 0; k < units; ++k) {
-            const bool there = lane < 8 && page >= 0 && page < a.N;
-            const int tok = c.t * UT + 16 * lane;
-            const bool leader = there && (tok & (P - 1)) == 0;
-            const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, leader)) * (uint32_t)(P * D);
-            const int64_t ph = (int64_t)page * a.Hkv + c.h;
-            publish();
-#pragma unroll 1
-            for (int w = 0; w < 2; ++w, ++x) {      // keys, values
-                const int sl = x % NRAW;
-                if (x >= NRAW && !(ok = warp_wait(B_RAWFREE + sl, (uint32_t)(x / NRAW - 1)))) break;
-                if (lane == 0) mbar_arrive_expect_tx(bar(B_RAWFULL + sl), bytes);
-                __syncwarp();
-                if (leader)
-                    bulk_load(sb + OFF_RAW<D> + (uint32_t)sl * RAW<D> + (uint32_t)(16 * lane * D),
-                              (w ? a.vc : a.kc) + (ph << a.page_log2) * D, (uint32_t)(P * D), bar(B_RAWFULL + sl));
-            }
-            if (!ok) break;
-            pk = 0.f, pv = -1.f;     // a page that is gone
-            if (there) {
-                pk = a.ks[ph];
-                pv = fminf(fmaxf(a.vs[ph], kv8::kVsMin), kv8::kVsMax);
-            }
-            pend = k;
-            c.next_unit(a);
-            if (k + 1 < units) look_up();
-        }
-        if (ok) publish();
-        if (s_abort && lane == 0)    // leave no copy in flight
-            for (int y = max(0, x - NRAW); y < x; ++y)
-                mbar_wait(bar(B_RAWFULL + y % NRAW), (uint32_t)(y / NRAW) & 1u, kCleanupLimitNs);
-    } else if (warp == 1) {
-        // ================================================================ products
-        if (lane == 0) {
-            constexpr uint32_t id_s = idesc_f16(TR, UT, false), id_o = idesc_f16(TR, D, true);
-            Cur c, n;                // the unit whose second product is next, and the one after it
+    if (warp < 8) {
+        if (warp == 0) {
+            // ============================================================ loads
+            // Lane i < 8 has keys 16 i .. 16 i + 15 of the unit; the first lane of a page copies it.
+            Cur c;
             c.start(a, s_place);
-            n = c;
-            bool ok = true, issued = false;
-            uint32_t nq[2] = {0, 0}, np[2] = {0, 0};   // items and units that tile t has begun
-            auto cv = [&](int x) { return sb + OFF_CV<D> + (uint32_t)(x % NCV) * CV<D>; };
-            // scores of tile t for unit k (widened slot 2 k), n being its cursor
-            auto scores = [&](int t, int k, bool new_item) {
-                if (new_item) ok = ok && wait(B_Q + t, nq[t]++);
-                ok = ok && wait(B_CVFULL + (2 * k) % NCV, (uint32_t)(2 * k / NCV));
+            int page = -1;
+            auto look_up = [&]() {
+                page = -1;
+                const int tok = c.t * UT + 16 * lane;
+                if (lane < 8 && tok < c.r.kv) page = a.table[(int64_t)c.s * a.W + (tok >> a.page_log2)];
+            };
+            look_up();
+            bool ok = true;
+            int x = 0, pend = -1;
+            float pk = 0.f, pv = 0.f;
+            auto publish = [&]() {     // the scales of a unit, once they are here
+                if (pend < 0) return;
+                const unsigned gone = __ballot_sync(0xffffffffu, lane < 8 && pv < 0.f);
+                if (lane < 8)
+                    s_sc[(pend % NSC) * 8 + lane] = pv < 0.f ? make_float4(0.f, -1.f, 0.f, 0.f)
+                                                             : make_float4(pk, pv, log2f(pv), 1.f / pv);
+                if (lane == 0) s_gone[pend % NSC] = gone != 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_SC + pend % NSC));
+                pend = -1;
+            };
+#pragma unroll 1
+            for (int k = 0; k < units; ++k) {
+                const bool there = lane < 8 && page >= 0 && page < a.N;
+                const int tok = c.t * UT + 16 * lane;
+                const bool leader = there && (tok & (P - 1)) == 0;
+                const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, leader)) * (uint32_t)(P * D);
+                const int64_t ph = (int64_t)page * a.Hkv + c.h;
+                publish();
+#pragma unroll 1
+                for (int w = 0; w < 2; ++w, ++x) {      // keys, values
+                    const int sl = x % NRAW;
+                    if (x >= NRAW && !(ok = warp_wait(B_RAWFREE + sl, (uint32_t)(x / NRAW - 1)))) break;
+                    if (lane == 0) mbar_arrive_expect_tx(bar(B_RAWFULL + sl), bytes);
+                    __syncwarp();
+                    if (leader)
+                        bulk_load(sb + L::OFF_RAW + (uint32_t)sl * L::RAW + (uint32_t)(16 * lane * D),
+                                  (w ? a.vc : a.kc) + (ph << a.page_log2) * D, (uint32_t)(P * D), bar(B_RAWFULL + sl));
+                }
+                if (!ok) break;
+                pk = 0.f, pv = -1.f;     // a page that is gone
+                if (there) {
+                    pk = a.ks[ph];
+                    pv = fminf(fmaxf(a.vs[ph], kv8::kVsMin), kv8::kVsMax);
+                }
+                pend = k;
+                c.next_unit(a);
+                if (k + 1 < units) look_up();
+            }
+            if (ok) publish();
+            if (s_abort && lane == 0)    // leave no copy in flight
+                for (int y = max(0, x - NRAW); y < x; ++y)
+                    mbar_wait(bar(B_RAWFULL + y % NRAW), (uint32_t)(y / NRAW) & 1u, kCleanupLimitNs);
+        } else if (warp == 1) {
+            // ============================================================ products
+            // The whole warp walks the loop, so that the descriptors stay in uniform registers;
+            // one elected lane issues.
+            constexpr uint32_t id_s = idesc_f16(TR, UT, false), id_o = idesc_f16(TR, D, true);
+            bool ok = tmem == 0, issued = false;     // all of the TMEM is ours: its base is 0
+            if (!ok) s_abort = 1;
+            auto cv_wait = [&](int x) { ok = ok && warp_wait(B_CVFULL + x % NCV, (uint32_t)(x / NCV)); };
+            // scores of unit k into buffer b from query tile q; the key slot is given back after the last
+            auto scores = [&](int b, int q, int k, bool free) {
+                cv_wait(2 * k);
                 if (!ok) return;
                 tc_fence_after();
-                const uint64_t dq = sdesc_sw128(sb + OFF_Q<D> + (uint32_t)t * NSL * SLAB, 16, 1024);
-                const uint64_t dk = sdesc_sw128(cv(2 * k), 16, 1024);
+                const uint64_t dq = sdesc_sw128(sb + L::OFF_Q + (uint32_t)q * NSL * SLAB, 16, 1024);
+                const uint64_t dk = sdesc_sw128(sb + L::OFF_CV + (uint32_t)((2 * k) % NCV) * L::CV, 16, 1024);
+                if (elect_one()) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (uint32_t)(kk >> 2) * SLAB + (uint32_t)(kk & 3) * 32;
-                    mma_bf16(tmem + TM_S + 128u * t, sdesc_add(dq, off), sdesc_add(dk, off), id_s, kk > 0);
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (uint32_t)(kk >> 2) * SLAB + (uint32_t)(kk & 3) * 32;
+                        mma_bf16(TM_S + 128u * b, sdesc_add(dq, off), sdesc_add(dk, off), id_s, kk > 0);
+                    }
+                    mma_commit(bar(B_S + b));
+                    if (free) mma_commit(bar(B_CVFREE + (2 * k) % NCV));
                 }
-                mma_commit(bar(B_S + t));
+                __syncwarp();
                 issued = true;
             };
-            const int nt0 = tiles_of(n);
-            for (int t = 0; t < nt0; ++t) scores(t, 0, true);
-            if (ok) mma_commit(bar(B_CVFREE + 0));
-#pragma unroll 1
-            for (int k = 0; ok && k < units; ++k) {
-                const int ntc = tiles_of(c);
-                const bool last = c.t + 1 == c.nt || k + 1 == units, first = c.t == 0 || k == 0;
-                bool fresh = false;
-                int ntn = 0;
-                if (k + 1 < units) {
-                    n.next_unit(a);
-                    fresh = n.t == 0;
-                    ntn = tiles_of(n);
-                }
-#pragma unroll 1
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (t < ntc) {
-                        ok = wait(B_P + t, np[t]++) && wait(B_CVFULL + (2 * k + 1) % NCV, (uint32_t)((2 * k + 1) / NCV));
-                        if (!ok) break;
-                        tc_fence_after();
-                        const uint64_t dv = sdesc_sw128(cv(2 * k + 1), SLAB, 1024);
+            // the weights of buffer b with unit k's values onto its sums (last: the item's last
+            // here); the value slot is given back after the last
+            auto sums = [&](int b, int k, bool fresh, bool last, bool free) {
+                cv_wait(2 * k + 1);
+                if (!ok) return;
+                tc_fence_after();
+                const uint64_t dv = sdesc_sw128(sb + L::OFF_CV + (uint32_t)((2 * k + 1) % NCV) * L::CV, SLAB, 1024);
+                if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < UT / 16; ++kk)
-                            mma_f16_ts(tmem + TM_O + 128u * t, tmem + TM_S + 128u * t + 8u * kk, sdesc_add(dv, kk * 2048),
-                                       id_o, (!first || kk > 0) ? 1u : 0u);
-                        if (t + 1 == ntc) mma_commit(bar(B_CVFREE + (2 * k + 1) % NCV));
-                        if (last) mma_commit(bar(B_O + t));
-                    }
-                    if (t < ntn) {
-                        scores(t, k + 1, fresh);
-                        if (ok && t + 1 == ntn) mma_commit(bar(B_CVFREE + (2 * k + 2) % NCV));
-                    }
+                    for (int kk = 0; kk < UT / 16; ++kk)
+                        mma_f16_ts(TM_O + 128u * b, TM_S + 128u * b + kP + 8u * kk, sdesc_add(dv, kk * 2048), id_o,
+                                   (!fresh || kk > 0) ? 1u : 0u);
+                    if (free) mma_commit(bar(B_CVFREE + (2 * k + 1) % NCV));
+                    if (last) mma_commit(bar(B_O + b));
                 }
-                c = n;
-            }
-            if (s_abort && issued) {   // let this thread's products land before the TMEM goes away
-                mma_commit(bar(B_DRAIN));
-                mbar_wait(bar(B_DRAIN), 0u, kCleanupLimitNs);
-            }
-        }
-        __syncwarp();
-    } else if (warp >= 4 && warp < 8) {
-        // ================================================================ widening
-        Cur c;
-        c.start(a, s_place);
-        const int ct = tid - 128;
-        constexpr int CPT = D / 16;          // 16-byte chunks of a token
-        int x = 0;
-        bool ok = true;
+                __syncwarp();
+            };
+            if constexpr (PAIR) {
+                Cur c, n;                // the unit whose second product is next, and the one after it
+                c.start(a, s_place);
+                n = c;
+                uint32_t nq[2] = {0, 0}, np[2] = {0, 0};   // items and units that tile t has begun
+                const int nt0 = tiles_of(n);
+#pragma unroll
+                for (int t = 0; t < 2; ++t)
+                    if (t < nt0) {
+                        ok = ok && warp_wait(B_Q + t, nq[t]++);
+                        scores(t, t, 0, t + 1 == nt0);
+                    }
 #pragma unroll 1
-        for (int k = 0; k < units && ok; ++k) {
+                for (int k = 0; ok && k < units; ++k) {
+                    const int ntc = tiles_of(c);
+                    const bool last = c.t + 1 == c.nt || k + 1 == units, first = c.t == 0 || k == 0;
+                    int ntn = 0;
+                    if (k + 1 < units) {
+                        n.next_unit(a);
+                        ntn = tiles_of(n);
+                    }
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (t < ntc) {
+                            ok = ok && warp_wait(B_P + t, np[t]++);
+                            sums(t, k, first, last, t + 1 == ntc);
+                        }
+                        if (t < ntn) {
+                            if (n.t == 0) ok = ok && warp_wait(B_Q + t, nq[t]++);
+                            scores(t, t, k + 1, t + 1 == ntn);
+                        }
+                    }
+                    c = n;
+                }
+            } else {
+                Cur c, n;                // units k (second product) and k + 2 (first)
+                c.start(a, s_place);
+                n = c;
+                uint32_t nq = 0;
+                auto next_scores = [&](int k) {      // n is at unit k
+                    if (k == 0 || n.t == 0) ok = ok && warp_wait(B_Q, nq++);
+                    scores(k & 1, 0, k, true);
+                    n.next_unit(a);
+                };
+                next_scores(0);
+                if (units > 1) next_scores(1);
+                int k0 = 0;              // the item's first unit
 #pragma unroll 1
-            for (int w = 0; w < 2; ++w, ++x) {
-                const int rs = x % NRAW, cs = x % NCV;
-                ok = warp_wait(B_RAWFULL + rs, (uint32_t)(x / NRAW));
-                if (ok && x >= NCV) ok = warp_wait(B_CVFREE + cs, (uint32_t)(x / NCV - 1));
-                if (ok && w == 1) ok = warp_wait(B_SC + k % NSC, (uint32_t)(k / NSC));
-                if (!ok) break;
-                const uint32_t src = sb + OFF_RAW<D> + (uint32_t)rs * RAW<D>;
-                const uint32_t dst = sb + OFF_CV<D> + (uint32_t)cs * CV<D>;
-                const int left = c.r.kv - c.t * UT;      // cached keys from the unit's first on
-#pragma unroll 2
-                for (int i = ct; i < UT * CPT; i += 128) {
-                    const int row = i / CPT, ch = i % CPT;
-                    uint4 u;
-                    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-                                 : "r"(src + (uint32_t)i * 16));
+                for (int k = 0; ok && k < units; ++k) {
+                    const int b = k & 1, k1 = min(units, k + c.nt - c.t);   // the item's end here
+                    ok = warp_wait(B_P + b, (uint32_t)(k >> 1));
+                    sums(b, k, k - k0 < 2, k + 2 >= k1, true);
+                    if (ok && k + 2 < units) next_scores(k + 2);
+                    c.next_unit(a);
+                    if (c.t == 0) k0 = k + 1;
+                }
+            }
+            if (s_abort && issued) {   // let this warp's products land before the TMEM goes away
+                if (elect_one()) {
+                    mma_commit(bar(B_DRAIN));
+                    mbar_wait(bar(B_DRAIN), 0u, kCleanupLimitNs);
+                }
+                __syncwarp();
+            }
+        } else if (warp >= 4) {
+            // ============================================================ widening
+            // A thread takes 8 codes of a row to 16 bytes of halves: reads and swizzled writes
+            // both fall on distinct banks, and a thread's rows keep its place in the swizzle.
+            Cur c;
+            c.start(a, s_place);
+            const int ct = tid - 128;
+            constexpr int PPR = D / 8, RPI = 128 / PPR, IT = UT / RPI;   // pieces a row, rows a step, steps
+            const int row0 = ct / PPR, piece = ct % PPR;
+            const uint32_t src0 = sb + L::OFF_RAW + (uint32_t)ct * 8;
+            const uint32_t dst0 = sb + L::OFF_CV + (uint32_t)(piece >> 3) * SLAB + (uint32_t)row0 * 128u +
+                                  (((uint32_t)(piece & 7) ^ (uint32_t)(row0 & 7)) << 4);
+            int x = 0;
+            bool ok = true;
+#pragma unroll 1
+            for (int k = 0; k < units && ok; ++k) {
+#pragma unroll 1
+                for (int w = 0; w < 2; ++w, ++x) {
+                    const int rs = x % NRAW, cs = x % NCV;
+                    ok = warp_wait(B_RAWFULL + rs, (uint32_t)(x / NRAW));
+                    if (ok && x >= NCV) ok = warp_wait(B_CVFREE + cs, (uint32_t)(x / NCV - 1));
+                    if (ok && w == 1) ok = warp_wait(B_SC + k % NSC, (uint32_t)(k / NSC));
+                    if (!ok) break;
+                    const uint32_t src = src0 + (uint32_t)rs * L::RAW, dst = dst0 + (uint32_t)cs * L::CV;
                     // value codes of places without a cached token: zero, so that no stale NaN
                     // meets a zero weight (stale keys only reach scores that are masked)
-                    if (w == 1 && (row >= left || s_sc[(k % NSC) * 8 + (row >> 4)].y < 0.f)) u = make_uint4(0, 0, 0, 0);
-                    uint32_t h[8];
-                    const uint32_t cw[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        h[2 * e] = decode2_h<KV>(cw[e] & 0xffffu);
-                        h[2 * e + 1] = decode2_h<KV>(cw[e] >> 16);
-                    }
-                    // chunks 2 ch and 2 ch + 1 of the row; the second slab's lanes store the odd
-                    // one first, so that a quarter warp's stores fall on distinct banks
-                    const uint32_t base = dst + (uint32_t)(ch >> 2) * SLAB + (uint32_t)row * 128u;
-                    const uint32_t sw = (uint32_t)(ch >> 2);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t o = (uint32_t)e ^ sw;
-                        const uint32_t addr = base + ((((uint32_t)(ch & 3) * 2 + o) ^ (uint32_t)(row & 7)) << 4);
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(o ? h[4] : h[0]),
-                                     "r"(o ? h[5] : h[1]), "r"(o ? h[6] : h[2]), "r"(o ? h[7] : h[3])
+                    const int left = w == 0 ? UT : c.r.kv - c.t * UT;
+                    const bool holes = w == 1 && s_gone[k % NSC];
+                    const bool plain = left >= UT && !holes;
+#pragma unroll 4
+                    for (int i = 0; i < IT; ++i) {
+                        uint32_t u0, u1, h0, h1, h2, h3;
+                        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(u0), "=r"(u1) : "r"(src + (uint32_t)i * 1024u));
+                        if (!plain) {
+                            const int row = row0 + i * RPI;
+                            if (row >= left || (holes && s_sc[(k % NSC) * 8 + (row >> 4)].y < 0.f)) u0 = u1 = 0;
+                        }
+                        decode4_h<KV>(u0, h0, h1);
+                        decode4_h<KV>(u1, h2, h3);
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (uint32_t)(i * RPI) * 128u), "r"(h0),
+                                     "r"(h1), "r"(h2), "r"(h3)
                                      : "memory");
                     }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(bar(B_RAWFREE + rs));
+                        mbar_arrive(bar(B_CVFULL + cs));
+                    }
                 }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bar(B_RAWFREE + rs));
-                    mbar_arrive(bar(B_CVFULL + cs));
-                }
+                c.next_unit(a);
             }
-            c.next_unit(a);
         }
-    } else if (warp >= 8) {
-        // ================================================================ softmax of tile t
-        const int t = (warp - 8) >> 2, qd = warp & 3;
+    } else {
+        // ================================================================ softmax of buffer b
+        const int b = (warp - 8) >> 2, qd = warp & 3;
         const int row = 32 * qd + lane;                 // of the tile
         const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16);
-        const uint32_t ts = tl + TM_S + 128u * t, to = tl + TM_O + 128u * t;
+        const uint32_t ts = tl + TM_S + 128u * b, to = tl + TM_O + 128u * b;
+        float2 *s_ml = reinterpret_cast<float2 *>(sm + L::OFF_ML);
         Cur c;
         c.start(a, s_place);
         bool ok = true;
-        uint32_t ns = 0, no = 0;      // units and items of this tile so far
-        int k = 0;                    // unit of the CTA
+        uint32_t ns = 0, no = 0, no1 = 0, items = 0;   // units and items of this buffer (and of
+                                                       // the other's sums), items of the CTA
+        int k = 0;                            // unit of the CTA
+        TileRow r;
+        float cs = 0.f;
+        // this buffer's rows of the item at c: their place, and their queries for the products
+        auto enter_item = [&]() {
+            r = tile_row<RB>(a, c, (PAIR ? b * TR : 0) + row);
+            cs = stage_query<D>(a, r, row, PAIR || b == 0 ? sm + L::OFF_Q + (uint32_t)(PAIR ? b : 0) * NSL * SLAB : nullptr);
+            if (PAIR || b == 0) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_Q + (PAIR ? b : 0)));
+            }
+        };
+        bool mine_item = !PAIR || b < tiles_of(c);
+        if (mine_item) enter_item();
 #pragma unroll 1
         while (k < units && ok) {
             const int mine = min(c.nt - c.t, units - k);      // the CTA's units of this item
-            const int rows = min(RB, c.r.n * a.G - c.b * RB);
-            const bool first = c.t == 0, last = c.t + mine == c.nt;
-            if (t == 0 && tid == 256) {
+            const bool first = c.t == 0, last = c.t + mine == c.nt, whole = first && last;
+            const int t0 = c.t;
+            if (tid == 256) {
                 // the CTA's entry: an item that begins here and ends elsewhere (its last)
                 if (first && !last)
                     a.entry[blockIdx.x] = make_int4(cta_of(u0 + k + c.nt - 1, s_place.total, s_place.ctas), c.s, c.h, c.b);
                 else if (k + mine == units)
                     a.entry[blockIdx.x] = make_int4(-1, 0, 0, 0);
             }
-            if (t < (rows > TR ? 2 : 1)) {
-                const int lr = t * TR + row, at = c.b * RB + lr;
-                const bool live = lr < rows;
-                const int qi = live ? at / a.G : 0;
-                const int64_t qrow = c.r.q0 + qi, hq = c.h * a.G + (at - qi * a.G);
-                // ---- the row's query, normalised, to shared memory
-                float cs;
-                {
-                    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + qrow * a.q_stride + hq * D;
-                    uint4 u[D / 8];
-                    float amax = 0.f;
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i)
-                        u[i] = live ? reinterpret_cast<const uint4 *>(q)[i] : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)),
-                                                     fabsf(__uint_as_float(w[e] & 0xffff0000u))));
-                    }
-                    const float fac = row_factor(amax) * a.sign;
-                    cs = a.scale_log2 * fabsf(1.f / fac);
-                    uint8_t *dst = sm + OFF_Q<D> + (uint32_t)t * NSL * SLAB + (uint32_t)row * 128u;
-#pragma unroll
-                    for (int i = 0; i < D / 8; ++i) {
-                        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-                        uint32_t h[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            h[e] = pack_h2(__uint_as_float(w[e] << 16) * fac, __uint_as_float(w[e] & 0xffff0000u) * fac);
-                        *reinterpret_cast<uint4 *>(dst + (i >> 3) * SLAB + (((uint32_t)(i & 7) ^ (uint32_t)(row & 7)) << 4)) =
-                            make_uint4(h[0], h[1], h[2], h[3]);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_Q + t));
-                }
-                const int lim = live ? seen_by(c.r, qi) : 0;
-                float M = -INFINITY, l = 0.f;
+            float M = -INFINITY, l = 0.f;
+            if (mine_item) {
+                const int j0 = PAIR ? 0 : (k ^ b) & 1, dj = PAIR ? 1 : 2;   // not PAIR: units of this parity
 #pragma unroll 1
-                for (int j = 0; j < mine && ok; ++j) {
-                    const int kk = k + j, sc = (kk % NSC) * 8, tok0 = (c.t + j) * UT;
+                for (int j = j0; j < mine && ok; j += dj) {
+                    const int kk = k + j, see = r.lim - (t0 + j) * UT;
                     // the scores first: a tile that sat out items is then at this unit, and the
                     // scale slot's phase is the one before or after its publication
-                    ok = warp_wait(B_S + t, ns++) && warp_wait(B_SC + kk % NSC, (uint32_t)(kk / NSC));
+                    ok = warp_wait(B_S + b, ns++) && warp_wait(B_SC + kk % NSC, (uint32_t)(kk / NSC));
                     if (!ok) break;
                     tc_fence_after();
-                    // which of the unit's keys this row sees; all of them in most units
-                    bool part = tok0 + UT > lim;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) part |= s_sc[sc + i].y < 0.f;
-                    part = __any_sync(0xffffffffu, part);
-                    // pass 1: the row's maximum
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int cb = 0; cb < 4; ++cb) {
-                        float v[32];
-                        tmem_ld32(ts + 32u * cb, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float4 s4 = s_sc[sc + 2 * cb + i];
-                            float m = -INFINITY;
-                            if (part) {
-                                const int see = s4.y < 0.f ? 0 : lim - (tok0 + 32 * cb + 16 * i);
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) m = fmaxf(m, e < see ? v[16 * i + e] : -INFINITY);
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) m = fmaxf(m, v[16 * i + e]);
-                            }
-                            if (m != -INFINITY) mx = fmaxf(mx, fmaf(m, cs * s4.x, s4.z));
-                        }
-                    }
-                    if (__any_sync(0xffffffffu, mx > M + kv8::kTau)) {
-                        const float m = fmaxf(M, ceilf(mx)), w = part_weight(M, m);
-                        M = m;
-                        l *= w;
-                        if (j > 0) {      // the sums of the units before (their products have landed)
-#pragma unroll 1
-                            for (int cb = 0; cb < D / 32; ++cb) {
-                                float o[32];
-                                tmem_ld32(to + 32u * cb, o);
-                                tmem_wait_ld();
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] *= w;
-                                tmem_st32(to + 32u * cb, o);
-                            }
-                        }
-                    }
-                    // pass 2: the weights, over the scores
-                    const float ref = kv8::kOff - (M == -INFINITY ? 0.f : M);
-#pragma unroll
-                    for (int cb = 0; cb < 4; ++cb) {
-                        float v[32];
-                        uint32_t p[16];
-                        tmem_ld32(ts + 32u * cb, v);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const float4 s4 = s_sc[sc + 2 * cb + i];
-                            const float kf = cs * s4.x, add = s4.z + ref;
-                            const int see = !part ? 16 : s4.y < 0.f ? 0 : lim - (tok0 + 32 * cb + 16 * i);
-                            float sum = 0.f;
-#pragma unroll
-                            for (int e = 0; e < 16; e += 2) {
-                                float p0 = ex2(fmaf(v[16 * i + e], kf, add));
-                                float p1 = ex2(fmaf(v[16 * i + e + 1], kf, add));
-                                if (part) {
-                                    p0 = e < see ? p0 : 0.f;
-                                    p1 = e + 1 < see ? p1 : 0.f;
-                                }
-                                sum += p0 + p1;
-                                p[8 * i + (e >> 1)] = pack_h2(p0, p1);
-                            }
-                            l = fmaf(sum, s4.w, l);
-                        }
-                        tmem_st16(ts + 16u * cb, p);
-                    }
-                    tmem_wait_st();
+                    const bool part = __any_sync(0xffffffffu, see < UT) || s_gone[kk % NSC];
+                    softmax_unit<D>(ts, to, RowUnit{s_sc + (kk % NSC) * 8, see, part, cs}, j > j0, M, l);
+                    // the weights let buffer 1's sums be written again: not before buffer 0's warps
+                    // have read those of the item before
+                    if (!PAIR && b == 1 && j == j0 && items > 0 && !(ok = warp_wait(B_OFREE, items - 1))) break;
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_P + t));
+                    if (lane == 0) mbar_arrive(bar(B_P + b));
                 }
-                // ---- the item's sums
-                if (ok) ok = warp_wait(B_O + t, no++);
-                if (ok) {
+            }
+            // ---- the item's sums, after the next item's queries are on their way
+            const TileRow done = r;
+            const int64_t slot = ((int64_t)blockIdx.x * 2 + (first ? 1 : 0)) * RB + (PAIR ? b * TR : 0) + row;
+            const bool had = mine_item;
+            const int had0 = PAIR ? mine : (mine + 1 - (k & 1)) >> 1, had1 = PAIR ? mine : (mine + (k & 1)) >> 1;
+            k += mine;
+            c.next_of_item(a);
+            auto next_item_queries = [&]() {
+                mine_item = k < units && (!PAIR || b < tiles_of(c));
+                if (ok && mine_item) enter_item();
+            };
+            if constexpr (PAIR) {
+                next_item_queries();
+                if (had) {
+                    ok = ok && warp_wait(B_O + b, no++);
+                    if (!ok) break;
                     tc_fence_after();
-                    const bool whole = first && last;
-                    const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
-                    const int64_t slot = ((int64_t)blockIdx.x * 2 + (first ? 1 : 0)) * RB + lr;
-                    const int64_t orow = qrow * a.Hq + hq;
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
                     for (int cb = 0; cb < D / 32; ++cb) {
                         float o[32];
                         tmem_ld32(to + 32u * cb, o);
                         tmem_wait_ld();
-                        if (!live) continue;
-                        if (whole) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) o[e] *= inv;
-                            __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + orow * D + 32 * cb;
-#pragma unroll
-                            for (int e = 0; e < 32; e += 8) Vec16<__nv_bfloat16>::store(dst + e, o + e);
-                        } else {
-                            float *dst = a.part_o + slot * D + 32 * cb;
-#pragma unroll
-                            for (int e = 0; e < 32; e += 4) Vec16<float>::store(dst + e, o + e);
-                        }
+                        write_chunk<D, RB>(a, done, whole, slot, cb, inv, o);
                     }
-                    if (live && whole && a.lse)
-                        a.lse[orow] = l == 0.f ? -INFINITY
-                                               : ((M == -INFINITY ? 0.f : M) - kv8::kOff + log2f(l)) * 0.693147180559945f;
-                    if (live && !whole) *reinterpret_cast<float2 *>(a.part_ml + 2 * slot) = make_float2(M, l);
+                    write_stats(a, done, whole, slot, M, l);
                     tc_fence_before();
                 }
+            } else if (b == 1) {
+                // hand M and l over (the item before's have been read); buffer 0's warps join the sums
+                if (had1 == 0 && items > 0) ok = ok && warp_wait(B_OFREE, items - 1);
+                if (ok) {
+                    s_ml[row] = make_float2(M, l);
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_ML));
+                }
+                next_item_queries();
+            } else {
+                // the other buffer's scores are done once its M and l are here (or it had none), so
+                // the query tile may be written again
+                ok = ok && warp_wait(B_ML, items);
+                if (!ok) break;
+                const float2 ml = s_ml[row];
+                next_item_queries();
+                if (had0 > 0) ok = ok && warp_wait(B_O + 0, no++);
+                if (had1 > 0) ok = ok && warp_wait(B_O + 1, no1++);
+                if (!ok) break;
+                tc_fence_after();
+                const float Mt = fmaxf(M, ml.x);
+                const float w0 = M == Mt ? 1.f : part_weight(M, Mt), w1 = ml.x == Mt ? 1.f : part_weight(ml.x, Mt);
+                const float lt = l * w0 + ml.y * w1, inv = lt == 0.f ? 0.f : 1.f / lt;
+#pragma unroll 1
+                for (int cb = 0; cb < D / 32; ++cb) {
+                    float o[32], o1[32];
+                    tmem_ld32(to + 32u * cb, o);          // a buffer without sums is read, not used
+                    tmem_ld32(to + 128u + 32u * cb, o1);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = (had0 > 0 ? o[e] * w0 : 0.f) + (had1 > 0 ? o1[e] * w1 : 0.f);
+                    write_chunk<D, RB>(a, done, whole, slot, cb, inv, o);
+                }
+                write_stats(a, done, whole, slot, Mt, lt);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_OFREE));
             }
-            k += mine;
-            c.next_of_item(a);
+            ++items;
         }
     }
     tc_fence_before();
@@ -504,14 +711,23 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
     grid_launch_dependents();
 }
 
-template <Kv8 KV, int D>
-cudaError_t launch_tile_d(const AttnArgs &a, int ctas, int rows, cudaStream_t s) {
-    auto kernel = kv8_tile_kernel<KV, D>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)tl::SMEM<D>);
+template <Kv8 KV, int D, bool PAIR>
+cudaError_t launch_tile_f(AttnArgs &a, void *ws, int ctas, int64_t rows, cudaStream_t s) {
+    using L = tl::Lay<D, PAIR>;
+    place_parts(a, ws, ctas, L::RB);
+    auto kernel = kv8_tile_kernel<KV, D, PAIR>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::SMEM);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)ctas, tl::NT, tl::SMEM<D>, s>>>(a);
+    kernel<<<(unsigned)ctas, tl::NT, L::SMEM, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_merge<__nv_bfloat16, D, tl::RB, 1>(a, ctas, rows, s);
+    return launch_merge<__nv_bfloat16, D, L::RB, 1>(a, ctas, (int)(rows < L::RB ? rows : L::RB), s);
+}
+
+// Pairs of tiles where a request may have more rows than one tile.
+template <Kv8 KV, int D>
+cudaError_t launch_tile_d(AttnArgs &a, void *ws, int ctas, int64_t rows, cudaStream_t s) {
+    return rows > tl::TR ? launch_tile_f<KV, D, true>(a, ws, ctas, rows, s)
+                         : launch_tile_f<KV, D, false>(a, ws, ctas, rows, s);
 }
 
 }  // namespace
@@ -528,17 +744,15 @@ cudaError_t launch_kv8_tile(const void *q, int64_t q_stride, const void *k_cache
     a.ks = k_scale, a.vs = v_scale, a.table = table, a.kv_len = kv_len;
     a.cu_q = cu_q, a.scale_log2 = fabsf(scale) * 1.4426950408889634f, a.sign = scale < 0.f ? -1.f : 1.f;
     a.out = out, a.lse = lse;
-    place_parts(a, ws, ctas, tl::RB);
     a.S = S, a.total_q = total_q, a.Hq = Hq, a.Hkv = Hkv, a.G = Hq / Hkv, a.W = W, a.N = N;
     a.page_log2 = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
     a.limit_ns = wait_limit_ns();
-    const int64_t rows64 = (int64_t)max_q * a.G;
-    const int rows = rows64 > tl::RB ? tl::RB : (int)rows64;
+    const int64_t rows = (int64_t)max_q * a.G;
     if (D == 128)
-        return kv == Kv8::E4M3 ? launch_tile_d<Kv8::E4M3, 128>(a, ctas, rows, s)
-                               : launch_tile_d<Kv8::INT8, 128>(a, ctas, rows, s);
-    return kv == Kv8::E4M3 ? launch_tile_d<Kv8::E4M3, 64>(a, ctas, rows, s)
-                           : launch_tile_d<Kv8::INT8, 64>(a, ctas, rows, s);
+        return kv == Kv8::E4M3 ? launch_tile_d<Kv8::E4M3, 128>(a, ws, ctas, rows, s)
+                               : launch_tile_d<Kv8::INT8, 128>(a, ws, ctas, rows, s);
+    return kv == Kv8::E4M3 ? launch_tile_d<Kv8::E4M3, 64>(a, ws, ctas, rows, s)
+                           : launch_tile_d<Kv8::INT8, 64>(a, ws, ctas, rows, s);
 }
 
 cudaError_t take_kv8_tile_error_word(unsigned *value) { return take_error_word(value); }
