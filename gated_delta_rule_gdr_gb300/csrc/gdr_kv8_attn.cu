@@ -10,17 +10,21 @@
 //
 // Bound: the cache's bytes.  At group size 8 a byte of keys or values meets 16 flops, far
 // below what the tensor cores need, so the kernel's job is to keep enough loads in flight
-// and to stay within the issue slots: 8 warps an SM, each with three 8 KB slabs (32 tokens
-// of keys and values) of its own coming by TMA, no barrier between warps inside an item.
-// Both products are warp MMAs m16n8k16 on halves: codes of both types and normalised bf16
-// queries are exact in a half, weights keep 11 bits.  The 16 rows of the MMA are the rows of
-// one item; the codes go from the swizzled slab straight to B fragments:
-//   keys    a lane reads 32 consecutive bytes of one key; which of the row's values a lane
+// and to stay within the issue slots: 12 warps an SM, each with two 8 KB slabs (32 tokens of
+// keys and values) of its own coming by TMA, no barrier between warps inside an item.
+// Both products are warp MMAs m16n8k16 on halves, transposed: S^T = K q^T and O^T = V^T P^T,
+// so that the 16-row side of the MMA holds keys or value columns and the 8-column side the
+// query rows: one token of up to 8 heads a cached head wastes nothing (with the rows on the
+// 16-row side half of every product, exponential and register would be).  Codes of both
+// types and normalised bf16 queries are exact in a half, weights keep 11 bits.  The codes go
+// from the swizzled slab straight to A fragments:
+//   keys    a lane reads D / 4 consecutive bytes of one key; which of the row's values a lane
 //           holds is free as long as the query fragment is laid out alike
-//   values  a lane reads 16 bytes of four tokens and interleaves them pairwise (PRMT); which
-//           column of which MMA a value is, is free, and chosen so that a lane's outputs are
-//           D / 4 consecutive values
+//   values  a lane reads D / 8 bytes of four tokens and interleaves them pairwise (PRMT); which
+//           row of which MMA a value is, is free, and chosen so that a lane's outputs are
+//           D / 8 consecutive values
 // with every 16-byte load of a quarter warp on distinct banks under the 128-byte swizzle.
+// The weights turn from accumulator to B layout by one 8 x 8 transpose (MOVM) per 8 keys.
 // fp32 queries and their weights are split in two halves each (22 bits), two MMAs for one.
 
 #include "gdr_kv8_attn.cuh"
@@ -31,16 +35,18 @@ namespace gdr {
 namespace {
 
 namespace sp {
-constexpr int NW = 4, NT = 32 * NW;    // warps a CTA; two CTAs an SM
+constexpr int NW = 4, NT = 32 * NW;    // warps a CTA
 constexpr int SLAB = 32;               // tokens a warp takes at a time
 constexpr int UT = SLAB * NW;          // a unit: one slab for each warp
-constexpr int ST = 3;                  // slabs a warp has in flight
-constexpr int RB = 16;                 // rows of an item
+// Slabs a warp has in flight and CTAs an SM; an item is R blocks of 8 rows, and two blocks'
+// fragments need the registers of two CTAs.
+template <int R> constexpr int ST = R == 2 ? 3 : 2;
+template <int R> constexpr int CPS = R == 2 ? 2 : 3;
 template <int D> constexpr uint32_t SLAB_BYTES = SLAB * D;
 template <int D> constexpr uint32_t STAGE = 2 * SLAB_BYTES<D>;     // keys, then values
-template <int D> constexpr uint32_t OFF_RED = NW * ST * STAGE<D>;  // [4 warps][4 rows][D] floats
-template <int D> constexpr uint32_t OFF_SCAL = OFF_RED<D> + NW * 4 * D * 4;   // [NW][ST][2 groups][2]
-template <int D> constexpr uint32_t SMEM = OFF_SCAL<D> + NW * ST * 4 * 4 + 1024;
+template <int R, int D> constexpr uint32_t OFF_RED = NW * ST<R> * STAGE<D>;   // [4 warps][4 rows][D]
+template <int R, int D> constexpr uint32_t OFF_SCAL = OFF_RED<R, D> + NW * 4 * D * 4;   // [NW][ST][2 groups][2]
+template <int R, int D> constexpr uint32_t SMEM = OFF_SCAL<R, D> + NW * ST<R> * 4 * 4;
 }  // namespace sp
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -48,6 +54,12 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The transpose of an 8 x 8 matrix of halves, a row's pair a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 v;
@@ -68,24 +80,24 @@ __device__ __forceinline__ uint32_t slab_offset(uint32_t t, uint32_t c) {
     return row * 128u + ((ch ^ (row & 7u)) << 4);
 }
 
-template <typename E, Kv8 KV, int D>
-__global__ void __launch_bounds__(sp::NT, 2)
+template <typename E, Kv8 KV, int D, int R>
+__global__ void __launch_bounds__(sp::NT, sp::CPS<R>)
 kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const AttnArgs a) {
     using namespace sp;
+    constexpr int ST = sp::ST<R>, RB = 8 * R;
     constexpr bool HL = sizeof(E) == 4;          // two halves for queries and weights
-    constexpr int NKS = D / 16, NVT = D / 8;     // k steps of q.k, column tiles of the output
-    constexpr int LD = D / 4;                    // values of a row that a lane holds
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    constexpr int NKS = D / 16, NVT = D / 16;    // k steps of K q^T, row tiles of O^T
+    constexpr int LD = D / 4, LO = D / 8;        // values of a query, of an output row that a lane holds
+    extern __shared__ __align__(1024) uint8_t sm[];
     __shared__ __align__(8) uint64_t s_bar[NW * ST];
     __shared__ Place s_place;
     __shared__ int64_t s_scan[NW];
-    __shared__ float s_stat[2][NW][RB];          // M, l of each warp at an item's end
+    __shared__ float s_stat[2][NW][8 * R];       // M, l of each warp at an item's end
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-    float *s_red = reinterpret_cast<float *>(sm + OFF_RED<D>);
-    float *s_scal = reinterpret_cast<float *>(sm + OFF_SCAL<D>) + warp * ST * 4;
+    float *s_red = reinterpret_cast<float *>(sm + OFF_RED<R, D>);
+    float *s_scal = reinterpret_cast<float *>(sm + OFF_SCAL<R, D>) + warp * ST * 4;
     const uint32_t stage0 = smem_u32(sm) + (uint32_t)warp * ST * STAGE<D>;
     auto bar = [&](int i) { return smem_u32(&s_bar[warp * ST + i]); };
 
@@ -131,6 +143,7 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             s_scal[pend * 4 + lane * 2] = pend_k;
             s_scal[pend * 4 + lane * 2 + 1] = pend_v;
         }
+        __syncwarp();
         pend = -1;
         if (left == 0) return;
         const bool there = lane < 2 && page >= 0 && page < a.N;
@@ -170,23 +183,22 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     for (int done = 0; done < units;) {
         const int t_first = c.t, t_last = min(c.nt, t_first + units - done);   // this CTA's units of the item
         const int rows = min(RB, c.r.n * a.G - c.b * RB);
-        // query fragments: rows g and g + 8, values LD t4 .. LD t4 + LD - 1, word j of a key
-        // holding values 4 j .. 4 j + 3 of them
-        uint32_t qf[HL ? 2 : 1][NKS][4];
-        float cs[2];                       // score factor of the row, in units of ln 2
-        int lim[2];                        // keys it sees
+        // query fragments: row 8 n + g, values LD t4 .. LD t4 + LD - 1, word j of a key holding
+        // values 4 j .. 4 j + 3 of them
+        uint32_t qf[HL ? 2 : 1][R][NKS][2];
+        // of rows 8 n + 2 t4 + e: the score factor in units of ln 2, the keys seen, M and l
+        float cs[R][2], M[R][2], l[R][2];
+        int lim[R][2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int lr = g + 8 * e, at = c.b * RB + lr;
+        for (int n = 0; n < R; ++n) {
+            const int lr = 8 * n + g, at = c.b * RB + lr;
             float f[LD];
-            lim[e] = 0;
             if (lr < rows) {
                 const int i = at / a.G;
                 const E *q = static_cast<const E *>(a.q) + (int64_t)(c.r.q0 + i) * a.q_stride +
                              (int64_t)(c.h * a.G + at - i * a.G) * D + t4 * LD;
 #pragma unroll
                 for (int v = 0; v < LD; v += Vec16<E>::N) Vec16<E>::load(q + v, f + v);
-                lim[e] = seen_by(c.r, i);
             } else {
 #pragma unroll
                 for (int v = 0; v < LD; ++v) f[v] = 0.f;
@@ -196,29 +208,36 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             for (int v = 0; v < LD; ++v) amax = fmaxf(amax, fabsf(f[v]));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            const float fac = row_factor(amax) * a.sign;
-            cs[e] = a.scale_log2 * fabsf(1.f / fac);
+            const float fac = row_factor(amax) * a.sign, csg = a.scale_log2 * fabsf(1.f / fac);
 #pragma unroll
-            for (int j = 0; j < NKS; ++j) {
-                const float x0 = f[4 * j] * fac, x1 = f[4 * j + 1] * fac, x2 = f[4 * j + 2] * fac, x3 = f[4 * j + 3] * fac;
-                qf[0][j][e] = pack_h2(x0, x1);
-                qf[0][j][2 + e] = pack_h2(x2, x3);
-                if constexpr (HL) {
-                    const float2 h0 = __half22float2(*reinterpret_cast<__half2 *>(&qf[0][j][e]));
-                    const float2 h1 = __half22float2(*reinterpret_cast<__half2 *>(&qf[0][j][2 + e]));
-                    qf[HL ? 1 : 0][j][e] = pack_h2(x0 - h0.x, x1 - h0.y);
-                    qf[HL ? 1 : 0][j][2 + e] = pack_h2(x2 - h1.x, x3 - h1.y);
+            for (int j = 0; j < NKS; ++j)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const float x0 = f[4 * j + 2 * k] * fac, x1 = f[4 * j + 2 * k + 1] * fac;
+                    qf[0][n][j][k] = pack_h2(x0, x1);
+                    if constexpr (HL) {
+                        const float2 h = __half22float2(*reinterpret_cast<__half2 *>(&qf[0][n][j][k]));
+                        qf[HL ? 1 : 0][n][j][k] = pack_h2(x0 - h.x, x1 - h.y);
+                    }
                 }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r2 = 8 * n + 2 * t4 + e;
+                cs[n][e] = __shfl_sync(0xffffffffu, csg, 4 * (2 * t4 + e));
+                lim[n][e] = r2 < rows ? seen_by(c.r, (c.b * RB + r2) / a.G) : 0;
+                M[n][e] = -INFINITY;
+                l[n][e] = 0.f;
             }
         }
         // the fewest keys that a row of the item sees: below them no mask is needed
         const int lim_all = seen_by(c.r, c.b * RB / a.G);
-        float o[NVT][4];
+        float o[R][NVT][4];     // value LO g + 2 j + (k >> 1) of row 8 n + 2 t4 + (k & 1)
 #pragma unroll
-        for (int j = 0; j < NVT; ++j)
+        for (int n = 0; n < R; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
-        float M[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+            for (int j = 0; j < NVT; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[n][j][k] = 0.f;
 
 #pragma unroll 1
         for (int t = t_first; t < t_last; ++t) {
@@ -230,15 +249,14 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
             const uint32_t kb = stage0 + (uint32_t)stage * STAGE<D>, vb = kb + SLAB_BYTES<D>;
             const int tok0 = t * UT + warp * SLAB;
-            float ksc[2], vsc[2];
-            bool gone = false;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                ksc[i] = s_scal[stage * 4 + 2 * i];
-                vsc[i] = s_scal[stage * 4 + 2 * i + 1];
-                gone |= vsc[i] < 0.f;
-            }
             if (ok && tok0 < c.end) {
+                float ksc[2], vsc[2];      // of the slab's two groups of 16 tokens
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    ksc[i] = s_scal[stage * 4 + 2 * i];
+                    vsc[i] = s_scal[stage * 4 + 2 * i + 1];
+                }
+                const bool gone = vsc[0] < 0.f || vsc[1] < 0.f;
                 // value codes of places without a cached token: zero, so that no stale NaN
                 // meets a zero weight
                 if (gone || tok0 + SLAB > c.r.kv) {
@@ -252,103 +270,120 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                // scores of 32 keys: column n of tile i is key 8 i + n
-                float x[4][4];
+                // scores of 32 keys: x[i][n][k] is key 16 i + g + 8 (k >> 1), row 8 n + 2 t4 + (k & 1)
+                float x[2][R][4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                for (int i = 0; i < 2; ++i)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[i][e] = 0.f;
-                    uint32_t w[NKS];
+                    for (int n = 0; n < R; ++n)
 #pragma unroll
-                    for (int v = 0; v < NKS / 4; ++v) {
-                        const uint4 u = lds128(kb + slab_offset<D>(8 * i + g, t4 * (NKS / 4) + v));
-                        w[4 * v] = u.x, w[4 * v + 1] = u.y, w[4 * v + 2] = u.z, w[4 * v + 3] = u.w;
-                    }
+                        for (int k = 0; k < 4; ++k) x[i][n][k] = 0.f;
 #pragma unroll
-                    for (int j = 0; j < NKS; ++j) {
-                        const uint32_t b0 = decode2_h<KV>(w[j] & 0xffffu), b1 = decode2_h<KV>(w[j] >> 16);
-                        mma_f16(x[i], qf[0][j], b0, b1);
-                        if constexpr (HL) mma_f16(x[i], qf[HL ? 1 : 0][j], b0, b1);
-                    }
-                }
-                // exponents y = x cs ks + log2 vs of both rows, masked where needed
-                float kf[2][2], ev[2];
+                for (int v = 0; v < NKS / 4; ++v) {
+                    uint32_t w[2][2][4];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    ev[i] = vsc[i] < 0.f ? 0.f : __log2f(vsc[i]);
-                    kf[0][i] = cs[0] * ksc[i];
-                    kf[1][i] = cs[1] * ksc[i];
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const uint4 u = lds128(kb + slab_offset<D>(16 * i + 8 * e + g, t4 * (NKS / 4) + v));
+                            w[i][e][0] = u.x, w[i][e][1] = u.y, w[i][e][2] = u.z, w[i][e][3] = u.w;
+                        }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            uint32_t f[4];
+                            decode4_h<KV>(w[i][0][j], f[0], f[2]);
+                            decode4_h<KV>(w[i][1][j], f[1], f[3]);
+#pragma unroll
+                            for (int n = 0; n < R; ++n) {
+                                mma_f16(x[i][n], f, qf[0][n][4 * v + j][0], qf[0][n][4 * v + j][1]);
+                                if constexpr (HL)
+                                    mma_f16(x[i][n], f, qf[HL ? 1 : 0][n][4 * v + j][0], qf[HL ? 1 : 0][n][4 * v + j][1]);
+                            }
+                        }
                 }
                 if (gone || tok0 + SLAB > lim_all) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int tk = tok0 + 8 * i + 2 * t4 + (e & 1);
-                            if (tk >= lim[e >> 1] || vsc[i >> 1] < 0.f) x[i][e] = __int_as_float(0xff800000);
-                        }
-                }
-                float mx[2];
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float m[2];
-#pragma unroll
                     for (int i = 0; i < 2; ++i)
-                        m[i] = fmaxf(fmaxf(x[2 * i][2 * e], x[2 * i][2 * e + 1]),
-                                     fmaxf(x[2 * i + 1][2 * e], x[2 * i + 1][2 * e + 1]));
-                    mx[e] = fmaxf(m[0] == -INFINITY ? -INFINITY : fmaf(m[0], kf[e][0], ev[0]),
-                                  m[1] == -INFINITY ? -INFINITY : fmaf(m[1], kf[e][1], ev[1]));
+#pragma unroll
+                        for (int n = 0; n < R; ++n)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (tok0 + 16 * i + g + 8 * (k >> 1) >= lim[n][k & 1] || vsc[i] < 0.f) x[i][n][k] = -INFINITY;
                 }
-                if (__any_sync(0xffffffffu, mx[0] > M[0] + kv8::kTau || mx[1] > M[1] + kv8::kTau)) {
+                // exponents are x cs ks + log2 vs; a factor of at least 2^-126 keeps masked scores
+                // at -inf where a scale is zero
+                float ev[2], iv[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    ev[i] = vsc[i] < 0.f ? 0.f : __log2f(vsc[i]);
+                    iv[i] = vsc[i] < 0.f ? 0.f : __frcp_rn(vsc[i]);
+                }
+                float kf[2][R][2], mx[R][2];
+                bool grow = false;
+#pragma unroll
+                for (int n = 0; n < R; ++n)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float m = mx[e];
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                        m = fmaxf(M[e], ceilf(m));
-                        const float w = part_weight(M[e], m);
-                        M[e] = m;
-                        l[e] *= w;
+                        mx[n][e] = -INFINITY;
 #pragma unroll
-                        for (int j = 0; j < NVT; ++j) {
-                            o[j][2 * e] *= w;
-                            o[j][2 * e + 1] *= w;
+                        for (int i = 0; i < 2; ++i) {
+                            kf[i][n][e] = fmaxf(cs[n][e] * ksc[i], 1.2e-38f);
+                            mx[n][e] = fmaxf(mx[n][e], fmaf(fmaxf(x[i][n][e], x[i][n][2 + e]), kf[i][n][e], ev[i]));
                         }
+                        grow |= mx[n][e] > M[n][e] + kv8::kTau;
                     }
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int n = 0; n < R; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            float m = mx[n][e];
+#pragma unroll
+                            for (int off = 4; off < 32; off <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                            m = fmaxf(M[n][e], ceilf(m));
+                            const float w = part_weight(M[n][e], m);
+                            M[n][e] = m;
+                            l[n][e] *= w;
+#pragma unroll
+                            for (int j = 0; j < NVT; ++j) {
+                                o[n][j][e] *= w;
+                                o[n][j][2 + e] *= w;
+                            }
+                        }
                 }
-                uint32_t pf[HL ? 2 : 1][2][4];     // weights of 16 keys as the A operand
+                uint32_t pf[HL ? 2 : 1][2][R][2];     // weights of 16 keys as the B operand
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const float ref = M[e] == -INFINITY ? 0.f : M[e];
+                for (int n = 0; n < R; ++n)
 #pragma unroll
-                    for (int kk = 0; kk < 2; ++kk) {
-                        const float add = ev[kk] - ref + kv8::kOff;
+                    for (int i = 0; i < 2; ++i) {
                         float p[4];
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float s = x[2 * kk + (k >> 1)][2 * e + (k & 1)];
-                            p[k] = s == -INFINITY ? 0.f : ex2(fmaf(s, kf[e][kk], add));
+                        for (int e = 0; e < 2; ++e) {
+                            const float add = ev[i] - (M[n][e] == -INFINITY ? 0.f : M[n][e]) + kv8::kOff;
+                            p[e] = ex2(fmaf(x[i][n][e], kf[i][n][e], add));
+                            p[2 + e] = ex2(fmaf(x[i][n][2 + e], kf[i][n][e], add));
+                            l[n][e] = fmaf(p[e] + p[2 + e], iv[i], l[n][e]);
                         }
-                        l[e] = fmaf((p[0] + p[1]) + (p[2] + p[3]), vsc[kk] < 0.f ? 0.f : 1.f / vsc[kk], l[e]);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const uint32_t hi = pack_h2(p[2 * k], p[2 * k + 1]);
-                            pf[0][kk][2 * k + e] = hi;
+                            pf[0][i][n][k] = transpose8(hi);
                             if constexpr (HL) {
                                 const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                                pf[HL ? 1 : 0][kk][2 * k + e] = pack_h2(p[2 * k] - h.x, p[2 * k + 1] - h.y);
+                                pf[HL ? 1 : 0][i][n][k] = transpose8(pack_h2(p[2 * k] - h.x, p[2 * k + 1] - h.y));
                             }
                         }
                     }
-                }
-                // outputs: column n of tile j is value (D / 8) n + j
+                // outputs: rows g and g + 8 of tile j are values LO g + 2 j and the next
 #pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
+                for (int i = 0; i < 2; ++i) {
                     constexpr int WPT = D / 32;    // words of a token that a lane reads
                     uint32_t w[4][WPT];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const uint32_t tk = 16 * kk + 2 * t4 + (k & 1) + 8 * (k >> 1);
+                        const uint32_t tk = 16 * i + 2 * t4 + (k & 1) + 8 * (k >> 1);
                         if constexpr (D == 128) {
                             const uint4 u = lds128(vb + slab_offset<D>(tk, g));
                             w[k][0] = u.x, w[k][1] = u.y, w[k][WPT - 2] = u.z, w[k][WPT - 1] = u.w;
@@ -361,15 +396,14 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     for (int v = 0; v < WPT; ++v)
 #pragma unroll
                         for (int hf = 0; hf < 2; ++hf) {
-                            const uint32_t lo = __byte_perm(w[0][v], w[1][v], hf ? 0x7362 : 0x5140);
-                            const uint32_t hi = __byte_perm(w[2][v], w[3][v], hf ? 0x7362 : 0x5140);
+                            uint32_t f[4];
+                            decode4_h<KV>(__byte_perm(w[0][v], w[1][v], hf ? 0x7362 : 0x5140), f[0], f[1]);
+                            decode4_h<KV>(__byte_perm(w[2][v], w[3][v], hf ? 0x7362 : 0x5140), f[2], f[3]);
 #pragma unroll
-                            for (int z = 0; z < 2; ++z) {
-                                const int j = 4 * v + 2 * hf + z;
-                                const uint32_t b0 = decode2_h<KV>(z ? lo >> 16 : lo & 0xffffu);
-                                const uint32_t b1 = decode2_h<KV>(z ? hi >> 16 : hi & 0xffffu);
-                                mma_f16(o[j], pf[0][kk], b0, b1);
-                                if constexpr (HL) mma_f16(o[j], pf[HL ? 1 : 0][kk], b0, b1);
+                            for (int n = 0; n < R; ++n) {
+                                mma_f16(o[n][2 * v + hf], f, pf[0][i][n][0], pf[0][i][n][1]);
+                                if constexpr (HL)
+                                    mma_f16(o[n][2 * v + hf], f, pf[HL ? 1 : 0][i][n][0], pf[HL ? 1 : 0][i][n][1]);
                             }
                         }
                 }
@@ -381,14 +415,16 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 
         // ---- the item's end: the four warps' sums joined
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 1);
-            l[e] += __shfl_xor_sync(0xffffffffu, l[e], 2);
-            if (t4 == 0) {
-                s_stat[0][warp][g + 8 * e] = M[e];
-                s_stat[1][warp][g + 8 * e] = l[e];
+        for (int n = 0; n < R; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], off);
+                if (g == 0) {
+                    s_stat[0][warp][8 * n + 2 * t4 + e] = M[n][e];
+                    s_stat[1][warp][8 * n + 2 * t4 + e] = l[n][e];
+                }
             }
-        }
         if (!__syncthreads_and(ok)) {
             ok = false;
             break;
@@ -397,28 +433,26 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         const int64_t slot = ((int64_t)blockIdx.x * 2 + (first ? 1 : 0)) * RB;
         if (first && !last)
             entry = make_int4(cta_of(u0 + done + c.nt - 1, total, s_place.ctas), c.s, c.h, c.b);
-#pragma unroll 1
-        for (int pass = 0; pass < 4; ++pass) {       // rows 4 pass .. 4 pass + 3
+#pragma unroll
+        for (int pass = 0; pass < 2 * R; ++pass) {       // rows 4 pass .. 4 pass + 3
             if (4 * pass >= rows) break;
-            const int e = pass >> 1;
-            if ((g >> 2) == (pass & 1)) {
-                const int lr = g + 8 * e;
-                float Mt = -INFINITY;
+            if ((t4 >> 1) == (pass & 1)) {
+                const int n = pass >> 1;
 #pragma unroll
-                for (int w = 0; w < NW; ++w) Mt = fmaxf(Mt, s_stat[0][w][lr]);
-                const float f = M[e] == Mt ? 1.f : part_weight(M[e], Mt);
-                float *dst = s_red + (warp * 4 + (g & 3)) * D;
+                for (int e = 0; e < 2; ++e) {
+                    const int lr = 8 * n + 2 * t4 + e;
+                    float Mt = -INFINITY;
 #pragma unroll
-                for (int m = 0; m < LD / 4; ++m) {   // a lane's LD consecutive values, banks spread
-                    float4 u;
-                    float *uf = reinterpret_cast<float *>(&u);
+                    for (int w = 0; w < NW; ++w) Mt = fmaxf(Mt, s_stat[0][w][lr]);
+                    const float f = M[n][e] == Mt ? 1.f : part_weight(M[n][e], Mt);
+                    float *dst = s_red + (warp * 4 + (lr & 3)) * D;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int d = 4 * m + k, n2 = d / NVT, j = d % NVT;   // column 2 t4 + n2 of tile j
-                        uf[k] = (e ? o[j][2 + n2] : o[j][n2]) * f;
+                    for (int m = 0; m < LO / 4; ++m) {   // a lane's LO consecutive values, banks spread
+                        const int ch = (LO / 4) * g + (m ^ ((g >> 1) & (LO / 4 - 1)));
+                        *reinterpret_cast<float4 *>(dst + 4 * ch) =
+                            make_float4(o[n][2 * m][e] * f, o[n][2 * m][2 + e] * f, o[n][2 * m + 1][e] * f,
+                                        o[n][2 * m + 1][2 + e] * f);
                     }
-                    const int ch = (LD / 4) * t4 + (m ^ ((2 * t4 + g) & (LD / 4 - 1)));
-                    *reinterpret_cast<float4 *>(dst + 4 * ch) = u;
                 }
             }
             __syncthreads();
@@ -436,8 +470,8 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                     }
                     constexpr int VL = D / 32;       // consecutive values a lane writes
                     float y[VL];
-                    const int ch4 = lane * VL / 4, tt = ch4 / (LD / 4), m = ch4 % (LD / 4);
-                    const int ch = (LD / 4) * tt + (m ^ ((2 * tt + lr) & (LD / 4 - 1)));
+                    const int ch4 = lane * VL / 4, gg = ch4 / (LO / 4), m = ch4 % (LO / 4);
+                    const int ch = (LO / 4) * gg + (m ^ ((gg >> 1) & (LO / 4 - 1)));
 #pragma unroll
                     for (int v = 0; v < VL; ++v) y[v] = 0.f;
 #pragma unroll
@@ -498,17 +532,25 @@ bool make_cache_map(CUtensorMap *m, const void *ptr, int64_t tokens, int D) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename E, Kv8 KV, int D>
-cudaError_t launch_split(const AttnArgs &a, const void *kc, const void *vc, int ctas, int rows, cudaStream_t s) {
+template <typename E, Kv8 KV, int D, int R>
+cudaError_t launch_split_r(AttnArgs &a, const void *kc, const void *vc, void *ws, int rows, cudaStream_t s) {
+    const int ctas = sp::CPS<R> * sm_count();
+    place_parts(a, ws, ctas, 8 * R);
     CUtensorMap mk, mv;
     const int64_t tokens = ((int64_t)a.N * a.Hkv) << a.page_log2;
     if (!make_cache_map(&mk, kc, tokens, D) || !make_cache_map(&mv, vc, tokens, D)) return cudaErrorInvalidValue;
-    auto kernel = kv8_split_kernel<E, KV, D>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sp::SMEM<D>);
+    auto kernel = kv8_split_kernel<E, KV, D, R>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sp::SMEM<R, D>);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)ctas, sp::NT, sp::SMEM<D>, s>>>(mk, mv, a);
+    kernel<<<(unsigned)ctas, sp::NT, sp::SMEM<R, D>, s>>>(mk, mv, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return launch_merge<E, D, sp::RB, 8>(a, ctas, rows, s);
+    return launch_merge<E, D, 8 * R, 8>(a, ctas, rows, s);
+}
+// One block of 8 rows where no request has more, else two.
+template <typename E, Kv8 KV, int D>
+cudaError_t launch_split(AttnArgs &a, const void *kc, const void *vc, void *ws, int64_t rows, cudaStream_t s) {
+    return rows <= 8 ? launch_split_r<E, KV, D, 1>(a, kc, vc, ws, (int)rows, s)
+                     : launch_split_r<E, KV, D, 2>(a, kc, vc, ws, rows > 16 ? 16 : (int)rows, s);
 }
 
 }  // namespace
@@ -517,11 +559,12 @@ cudaError_t launch_split(const AttnArgs &a, const void *kc, const void *vc, int 
 // At 16 rows the split kernel's MMAs are full; beyond, it reads the cache once for every 16
 // rows (5 drafted tokens x 8 heads on 16 k keys 0.42 ms against 0.33 ms here, a chunk of 1000
 // tokens on 65 k 7.3 ms against 1.5 ms).
-bool kv8_tiles(int max_q, int G, Elem e) { return e == Elem::BF16 && (int64_t)max_q * G > sp::RB; }
+bool kv8_tiles(int max_q, int G, Elem e) { return e == Elem::BF16 && (int64_t)max_q * G > 16; }
 
 size_t kv8_attn_workspace_bytes(int, int max_q, int, int Hq, int Hkv, int D, Elem e) {
-    return kv8_tiles(max_q, Hq / Hkv, e) ? part_bytes(sm_count(), kKv8TileRows, D)
-                                         : part_bytes(2 * sm_count(), sp::RB, D);
+    if (kv8_tiles(max_q, Hq / Hkv, e)) return part_bytes(sm_count(), kKv8TileRows, D);
+    const bool one = (int64_t)max_q * (Hq / Hkv) <= 8;
+    return one ? part_bytes(sp::CPS<1> * sm_count(), 8, D) : part_bytes(sp::CPS<2> * sm_count(), 16, D);
 }
 
 cudaError_t launch_kv8_attn(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
@@ -532,28 +575,25 @@ cudaError_t launch_kv8_attn(const void *q, int64_t q_stride, const void *k_cache
     if (kv8_tiles(max_q, Hq / Hkv, e))
         return launch_kv8_tile(q, q_stride, k_cache, v_cache, k_scale, v_scale, table, kv_len, cu_q, scale, out,
                                lse, S, max_q, total_q, Hq, Hkv, D, W, page, N, kv, ws, s);
-    const int ctas = 2 * sm_count();
     AttnArgs a{};
     a.q = q, a.q_stride = q_stride, a.ks = k_scale, a.vs = v_scale, a.table = table, a.kv_len = kv_len;
     a.cu_q = cu_q, a.scale_log2 = fabsf(scale) * 1.4426950408889634f, a.sign = scale < 0.f ? -1.f : 1.f;
     a.out = out, a.lse = lse;
-    place_parts(a, ws, ctas, sp::RB);
     a.S = S, a.total_q = total_q, a.Hq = Hq, a.Hkv = Hkv, a.G = Hq / Hkv, a.W = W, a.N = N;
     a.page_log2 = page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7;
     a.limit_ns = wait_limit_ns();
-    const int64_t rows64 = (int64_t)max_q * a.G;
-    const int rows = rows64 > sp::RB ? sp::RB : (int)rows64;
+    const int64_t rows = (int64_t)max_q * a.G;
     const bool bf = e == Elem::BF16, f8 = kv == Kv8::E4M3;
     if (D == 128) {
-        if (bf) return f8 ? launch_split<__nv_bfloat16, Kv8::E4M3, 128>(a, k_cache, v_cache, ctas, rows, s)
-                          : launch_split<__nv_bfloat16, Kv8::INT8, 128>(a, k_cache, v_cache, ctas, rows, s);
-        return f8 ? launch_split<float, Kv8::E4M3, 128>(a, k_cache, v_cache, ctas, rows, s)
-                  : launch_split<float, Kv8::INT8, 128>(a, k_cache, v_cache, ctas, rows, s);
+        if (bf) return f8 ? launch_split<__nv_bfloat16, Kv8::E4M3, 128>(a, k_cache, v_cache, ws, rows, s)
+                          : launch_split<__nv_bfloat16, Kv8::INT8, 128>(a, k_cache, v_cache, ws, rows, s);
+        return f8 ? launch_split<float, Kv8::E4M3, 128>(a, k_cache, v_cache, ws, rows, s)
+                  : launch_split<float, Kv8::INT8, 128>(a, k_cache, v_cache, ws, rows, s);
     }
-    if (bf) return f8 ? launch_split<__nv_bfloat16, Kv8::E4M3, 64>(a, k_cache, v_cache, ctas, rows, s)
-                      : launch_split<__nv_bfloat16, Kv8::INT8, 64>(a, k_cache, v_cache, ctas, rows, s);
-    return f8 ? launch_split<float, Kv8::E4M3, 64>(a, k_cache, v_cache, ctas, rows, s)
-              : launch_split<float, Kv8::INT8, 64>(a, k_cache, v_cache, ctas, rows, s);
+    if (bf) return f8 ? launch_split<__nv_bfloat16, Kv8::E4M3, 64>(a, k_cache, v_cache, ws, rows, s)
+                      : launch_split<__nv_bfloat16, Kv8::INT8, 64>(a, k_cache, v_cache, ws, rows, s);
+    return f8 ? launch_split<float, Kv8::E4M3, 64>(a, k_cache, v_cache, ws, rows, s)
+              : launch_split<float, Kv8::INT8, 64>(a, k_cache, v_cache, ws, rows, s);
 }
 
 cudaError_t take_kv8_split_error_word(unsigned *value) { return take_error_word(value); }
