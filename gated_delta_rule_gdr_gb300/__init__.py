@@ -569,10 +569,17 @@ def last_device_error(device=None) -> int:
 
 
 # ---- the paged 8-bit cache of the exact-attention layers
+#
+# These run once a layer for every token served, and their small calls take a few
+# microseconds on the device: the checks below read each property of a tensor once, and the
+# stream's handle is taken without building a Stream object.
+
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
 
 def _int(t, name, shape=None):
     """Device pointer of a contiguous int32 CUDA tensor."""
-    if t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+    if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous int32 CUDA tensor")
     if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}")
@@ -587,6 +594,8 @@ def _rows(t, name):
     if not t.is_cuda or t.dim() != 3:
         raise ValueError(f"{name} must be a [tokens, heads, D] CUDA tensor")
     n, h, d = t.shape
+    if t.is_contiguous():
+        return t.data_ptr(), h * d
     st = t.stride()
     if (st[2] != 1 and d > 1) or (st[1] != d and h > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
@@ -594,19 +603,21 @@ def _rows(t, name):
 
 
 def _kv8_cache(k_cache, v_cache, k_scale, v_scale):
-    if k_cache.dtype not in KV8 or v_cache.dtype != k_cache.dtype:
+    code = KV8.get(k_cache.dtype)
+    if code is None or v_cache.dtype is not k_cache.dtype:
         raise TypeError("k_cache, v_cache must share one dtype, float8_e4m3fn or int8")
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache, v_cache must be [num_pages, Hkv, page, D]")
-    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32:
+    if k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32:
         raise TypeError("k_scale, v_scale must be float32")
     if k_scale.shape != shape[:2] or v_scale.shape != shape[:2]:
         raise ValueError("k_scale, v_scale must be [num_pages, Hkv]")
-    for t in (k_cache, v_cache, k_scale, v_scale):
-        if not t.is_cuda or not t.is_contiguous():
-            raise ValueError("libgdr takes contiguous CUDA tensors")
-    return shape
+    if not (k_cache.is_cuda and v_cache.is_cuda and k_scale.is_cuda and v_scale.is_cuda
+            and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and k_scale.is_contiguous() and v_scale.is_contiguous()):
+        raise ValueError("libgdr takes contiguous CUDA tensors")
+    return code, shape
 
 
 def page_plan(kv_len, q_len, block_table, free_ring, free_state, page: int, max_tokens: int):
@@ -614,17 +625,20 @@ def page_plan(kv_len, q_len, block_table, free_ring, free_state, page: int, max_
     finished), block_table [S,W], free_ring [num_pages], free_state [2] = (head, count), all
     int32; block_table and free_ring are updated in place.  Returns int32 (kv_len_out [S],
     cu_q [S+1], slots [max_tokens], positions [max_tokens], granted [S], free_state_out [2])."""
-    lib = load()
+    lib = _lib or load()
     S, W = block_table.shape
-    n = int(max_tokens)
-    slots, positions, cu, kv, granted, st, _ = torch.empty(
-        2 * n + 3 * S + 4, dtype=torch.int32, device=block_table.device).split((n, n, S + 1, S, S, 2, 1))
-    _check(lib.gdr_page_plan(_int(kv_len, "kv_len", (S,)), _int(q_len, "q_len", (S,)),
+    n, dev = int(max_tokens), block_table.device
+    i32, empty = torch.int32, torch.empty
+    kv, granted = empty(S, dtype=i32, device=dev), empty(S, dtype=i32, device=dev)
+    slots, positions = empty(n, dtype=i32, device=dev), empty(n, dtype=i32, device=dev)
+    cu, st = empty(S + 1, dtype=i32, device=dev), empty(2, dtype=i32, device=dev)
+    code = lib.gdr_page_plan(_int(kv_len, "kv_len", (S,)), _int(q_len, "q_len", (S,)),
                              _int(block_table, "block_table"), _int(free_ring, "free_ring"),
                              _int(free_state, "free_state", (2,)), kv.data_ptr(), cu.data_ptr(),
                              slots.data_ptr(), positions.data_ptr(), granted.data_ptr(),
-                             st.data_ptr(), S, W, int(page), free_ring.numel(), n,
-                             _stream(block_table.device)), "gdr_page_plan")
+                             st.data_ptr(), S, W, page, free_ring.numel(), n, _raw_stream(dev.index))
+    if code:
+        raise GdrError(code, "gdr_page_plan")
     return kv, cu, slots, positions, granted, st
 
 
@@ -632,18 +646,19 @@ def kv8_append(k, v, slots, k_cache, v_cache, k_scale, v_scale) -> None:
     """Quantise the new tokens' k, v [T,Hkv,D] (fp32 or bf16; tokens may be strided) into the
     paged cache at slots [T] int32 (negative: dropped).  k_cache, v_cache [num_pages,Hkv,page,D]
     float8_e4m3fn or int8, k_scale, v_scale [num_pages,Hkv] fp32, all updated in place."""
-    lib = load()
-    N, H, P, D = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    lib = _lib or load()
+    kv, (N, H, P, D) = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
     (kp, kst), (vp, vst) = _rows(k, "k"), _rows(v, "v")
     T = k.shape[0]
-    if k.dtype != v.dtype:
+    if k.dtype is not v.dtype:
         raise TypeError("k, v must share one dtype, float32 or bfloat16")
     if k.shape != (T, H, D) or v.shape != (T, H, D):
         raise ValueError(f"k, v must be [T, {H}, {D}]")
-    _check(lib.gdr_kv8_append(kp, vp, kst, vst, _int(slots, "slots", (T,)), k_cache.data_ptr(),
+    code = lib.gdr_kv8_append(kp, vp, kst, vst, _int(slots, "slots", (T,)), k_cache.data_ptr(),
                               v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), T, H, D,
-                              P, N, DTYPE[k.dtype], KV8[k_cache.dtype], _stream(k.device)),
-           "gdr_kv8_append")
+                              P, N, DTYPE[k.dtype], kv, _raw_stream(k_cache.device.index))
+    if code:
+        raise GdrError(code, "gdr_kv8_append")
 
 
 def kv8_attn_workspace_size(S, max_q, total_q, Hq, Hkv, D, dtype=torch.bfloat16) -> int:
@@ -659,29 +674,32 @@ def kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, scale: 
     sees the first kv_len - n + 1 + i keys.  workspace: None (allocated here) or a uint8 CUDA
     tensor of kv8_attn_workspace_size bytes.  Returns out [total_q,Hq,D], or (out, lse
     [total_q,Hq] fp32) if want_lse."""
-    lib = load()
-    N, Hkv, P, D = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    lib = _lib or load()
+    kv, (N, Hkv, P, D) = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
     qp, qst = _rows(q, "q")
     T, Hq, dq = q.shape
     S, W = block_table.shape
+    dtype, dev = q.dtype, k_cache.device
     if dq != D:
         raise ValueError(f"q must be [total_q, Hq, {D}]")
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
-    elif out.dtype != q.dtype or out.shape != q.shape or not out.is_cuda or not out.is_contiguous():
+        out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
+    elif out.dtype is not dtype or out.shape != q.shape or not out.is_cuda or not out.is_contiguous():
         raise ValueError("out must be a contiguous CUDA tensor of q's shape and dtype")
-    lse = torch.empty((T, Hq), dtype=torch.float32, device=q.device) if want_lse else None
-    need = lib.gdr_kv8_attn_workspace_size(S, int(max_q), T, Hq, Hkv, D, DTYPE[q.dtype])
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if want_lse else None
+    el = DTYPE[dtype]
+    need = lib.gdr_kv8_attn_workspace_size(S, max_q, T, Hq, Hkv, D, el)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
-    elif workspace.dtype != torch.uint8 or not workspace.is_cuda or workspace.numel() < need:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    elif workspace.dtype is not torch.uint8 or not workspace.is_cuda or workspace.numel() < need:
         raise ValueError(f"workspace must be a uint8 CUDA tensor of at least {need} bytes")
-    _check(lib.gdr_kv8_attn(qp, qst, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+    code = lib.gdr_kv8_attn(qp, qst, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                             v_scale.data_ptr(), _int(block_table, "block_table"),
                             _int(kv_len, "kv_len", (S,)),
-                            None if cu_q is None else _int(cu_q, "cu_q", (S + 1,)), float(scale),
-                            out.data_ptr(), None if lse is None else lse.data_ptr(), S, int(max_q),
-                            T, Hq, Hkv, D, W, P, N, DTYPE[q.dtype], KV8[k_cache.dtype],
-                            workspace.data_ptr(), workspace.numel(), _stream(q.device)),
-           "gdr_kv8_attn")
+                            None if cu_q is None else _int(cu_q, "cu_q", (S + 1,)), scale,
+                            out.data_ptr(), None if lse is None else lse.data_ptr(), S, max_q,
+                            T, Hq, Hkv, D, W, P, N, el, kv, workspace.data_ptr(), need,
+                            _raw_stream(dev.index))
+    if code:
+        raise GdrError(code, "gdr_kv8_attn")
     return (out, lse) if want_lse else out

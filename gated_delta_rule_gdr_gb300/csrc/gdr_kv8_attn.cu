@@ -540,7 +540,8 @@ cudaError_t launch_split_r(AttnArgs &a, const void *kc, const void *vc, void *ws
     const int64_t tokens = ((int64_t)a.N * a.Hkv) << a.page_log2;
     if (!make_cache_map(&mk, kc, tokens, D) || !make_cache_map(&mv, vc, tokens, D)) return cudaErrorInvalidValue;
     auto kernel = kv8_split_kernel<E, KV, D, R>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sp::SMEM<R, D>);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_smem(kernel, sp::SMEM<R, D>, allowed);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)ctas, sp::NT, sp::SMEM<R, D>, s>>>(mk, mv, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

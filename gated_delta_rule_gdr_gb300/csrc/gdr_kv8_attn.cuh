@@ -18,6 +18,8 @@
 #include "gdr_fused_common.cuh"
 #include "gdr_kv8.cuh"
 
+#include <atomic>
+
 namespace gdr {
 namespace {
 
@@ -338,14 +340,34 @@ void place_parts(AttnArgs &a, void *ws, int ctas, int RB) {
     a.part_o = a.part_ml + (size_t)ctas * 2 * RB * 2;
 }
 
+// SMs of the current device, asked once a device.
 int sm_count() {
-    int dev = 0, sms = 152;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    static std::atomic<int> known[64];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
         cudaGetLastError();
-        sms = 152;
+        return 152;
     }
+    const bool in = dev >= 0 && dev < 64;
+    if (in && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 152;
+    }
+    if (in) known[dev].store(sms, std::memory_order_relaxed);
     return sms;
+}
+// The kernel's shared-memory limit, raised once a device (`done`: one flag a kernel).
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
+    if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 }  // namespace

@@ -716,7 +716,8 @@ cudaError_t launch_tile_f(AttnArgs &a, void *ws, int ctas, int64_t rows, cudaStr
     using L = tl::Lay<D, PAIR>;
     place_parts(a, ws, ctas, L::RB);
     auto kernel = kv8_tile_kernel<KV, D, PAIR>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::SMEM);
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_smem(kernel, L::SMEM, allowed);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)ctas, tl::NT, L::SMEM, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
