@@ -20,7 +20,7 @@
 // two score and output buffers; the two halves of the sum are joined at the item's end.
 //
 // Warps: 0 loads (page entries and scales looked up one unit ahead), 1 issues the products
-// and owns the TMEM, 4-7 widen, 8-11 and 12-15 the softmax of buffer 0 and 1, a thread a row:
+// and owns the TMEM, 4-7 widen (two the keys, two the values), 8-11 and 12-15 the softmax of buffer 0 and 1, a thread a row:
 // maxima and sums never leave the thread.  No barrier spans the CTA inside the loop; every
 // wait is bounded.
 
@@ -74,6 +74,37 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
 }
+// A warp's wait for up to 32 barriers at once, a lane's own each (need: this lane has one):
+// a barrier is a trip to shared memory, which the products keep busy, and one trip serves
+// them all.  Bounded as role_wait; true once every lane's phase has completed.
+__device__ __noinline__ bool warp_wait_slow(uint32_t bar, uint32_t parity, bool need, uint64_t limit_ns,
+                                            volatile int *abort) {
+    const uint64_t t0 = global_timer_ns();
+    bool give_up = limit_ns == 0;
+    while (true) {
+        if (!give_up) {
+            const bool done = !need || mbar_try_wait_hint(bar, parity, kWaitSliceNs);
+            if (__all_sync(0xffffffffu, done)) return true;
+            if (*abort) give_up = true;
+            if (global_timer_ns() - t0 > limit_ns) give_up = true;
+        }
+        if (__any_sync(0xffffffffu, give_up)) {
+            if (give_up && !*abort) {
+                *abort = 1;
+                atomicOr(&g_device_error_word, kDevErrTimeout);
+            }
+            __syncwarp();
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool warp_wait_all(uint32_t bar, uint32_t parity, bool need, uint64_t limit_ns,
+                                              volatile int *abort) {
+    const bool done = !need || mbar_test_wait(bar, parity);
+    if (__all_sync(0xffffffffu, done)) return true;
+    return warp_wait_slow(bar, parity, need, limit_ns, abort);
+}
+
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t f2_pack(float a, float b) {
     uint64_t r;
@@ -169,16 +200,21 @@ __device__ __forceinline__ float stage_query(const AttnArgs &a, const TileRow &t
 // (kP on), M and l moved on.  The maximum is taken half by half; the upper half stays in
 // registers, whose weights then go over it, and the lower half is read a second time: half
 // the registers of holding all 128 scores for one TMEM read more.
+// GR: groups of a half (64 keys) with a scale of their own: one where pages hold 64 tokens or
+// more, else four.
 // see: keys of the unit that the row sees; part: some row of the warp sees fewer than all, or
 // a page is gone; rescale: the output buffer holds sums of earlier units.
 constexpr uint32_t kP = 64;
-struct RowUnit {
-    const float4 *sc;
+template <int GR> struct RowUnit {
+    const float4 *sc;              // the unit's scales: {ks, vs, log2 vs, 1 / vs} a group of 16
+    float4 held[GR == 1 ? 2 : 1];  // GR 1: those of the halves
     int see;
     bool part;
     float cs;
+    __device__ __forceinline__ float4 scales(int h, int i) const { return GR == 1 ? held[GR == 1 ? h : 0] : sc[4 * h + i]; }
 };
-__device__ __forceinline__ void load_half(uint32_t ts, int h, const RowUnit &u, float (&v)[2][32]) {
+template <int GR>
+__device__ __forceinline__ void load_half(uint32_t ts, int h, const RowUnit<GR> &u, float (&v)[2][32]) {
     tmem_ld32(ts + 64u * h, v[0]);
     tmem_ld32(ts + 64u * h + 32u, v[1]);
     tmem_wait_ld();
@@ -194,54 +230,62 @@ __device__ __forceinline__ void load_half(uint32_t ts, int h, const RowUnit &u, 
 }
 // A factor of at least 2^-126 keeps masked scores at -inf where a scale is zero.
 __device__ __forceinline__ float unit_factor(float cs, float ks) { return fmaxf(cs * ks, 1.2e-38f); }
-__device__ __forceinline__ float half_max(const float (&v)[2][32], int h, const RowUnit &u, float mx) {
+template <int GR>
+__device__ __forceinline__ float half_max(const float (&v)[2][32], int h, const RowUnit<GR> &u, float mx) {
+    constexpr int N = 64 / GR;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float *x = &v[i >> 1][16 * (i & 1)];
-        float m = fmaxf(fmaxf(x[0], x[1]), x[2]);
+    for (int i = 0; i < GR; ++i) {
+        auto x = [&](int e) { return v[(N * i + e) >> 5][(N * i + e) & 31]; };
+        float m = fmaxf(fmaxf(x(0), x(1)), x(2));
 #pragma unroll
-        for (int e = 3; e < 15; e += 2) m = fmaxf(fmaxf(m, x[e]), x[e + 1]);
-        m = fmaxf(m, x[15]);
-        const float4 s4 = u.sc[4 * h + i];
+        for (int e = 3; e + 1 < N; e += 2) m = fmaxf(fmaxf(m, x(e)), x(e + 1));
+        m = fmaxf(m, x(N - 1));
+        const float4 s4 = u.scales(h, i);
         mx = fmaxf(mx, fmaf(m, unit_factor(u.cs, s4.x), s4.z));
     }
     return mx;
 }
-__device__ __forceinline__ float half_weights(uint32_t ts, int h, const RowUnit &u, const float (&v)[2][32], float ref,
+template <int GR>
+__device__ __forceinline__ float half_weights(uint32_t ts, int h, const RowUnit<GR> &u, const float (&v)[2][32], float ref,
                                               float l) {
+    constexpr int N = 64 / GR;
 #pragma unroll
     for (int cb = 0; cb < 2; ++cb) {
         uint32_t p[16];
+        uint64_t kf2 = 0, add2 = 0, sum = 0;
+        float iv = 0.f;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 s4 = u.sc[4 * h + 2 * cb + i];
-            const float kf = unit_factor(u.cs, s4.x), add = s4.z + ref;
-            const uint64_t kf2 = f2_pack(kf, kf), add2 = f2_pack(add, add);
-            uint64_t sum = 0;
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-                float p0, p1;
-                f2_unpack(f2_fma(f2_pack(v[cb][16 * i + e], v[cb][16 * i + e + 1]), kf2, add2), p0, p1);
-                p0 = ex2(p0);
-                p1 = ex2(p1);
-                sum = f2_add(sum, f2_pack(p0, p1));
-                p[8 * i + (e >> 1)] = pack_h2(p0, p1);
+        for (int e = 0; e < 32; e += 2) {
+            if (e % N == 0) {
+                const float4 s4 = u.scales(h, (32 * cb + e) / 16);
+                const float kf = unit_factor(u.cs, s4.x), add = s4.z + ref;
+                kf2 = f2_pack(kf, kf), add2 = f2_pack(add, add);
+                iv = s4.w;
+                sum = 0;
             }
-            float s0, s1;
-            f2_unpack(sum, s0, s1);
-            l = fmaf(s0 + s1, s4.w, l);
+            float p0, p1;
+            f2_unpack(f2_fma(f2_pack(v[cb][e], v[cb][e + 1]), kf2, add2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            sum = f2_add(sum, f2_pack(p0, p1));
+            p[e >> 1] = pack_h2(p0, p1);
+            if ((e + 2) % N == 0 || e == 30) {
+                float s0, s1;
+                f2_unpack(sum, s0, s1);
+                l = fmaf(s0 + s1, iv, l);
+            }
         }
         tmem_st16(ts + kP + 32u * h + 16u * cb, p);
     }
     return l;
 }
-template <int D>
-__device__ __forceinline__ void softmax_unit(uint32_t ts, uint32_t to, const RowUnit &u, bool rescale, float &M, float &l) {
+template <int D, int GR>
+__device__ __forceinline__ void softmax_unit(uint32_t ts, uint32_t to, const RowUnit<GR> &u, bool rescale, float &M, float &l) {
     float v[2][32];
-    load_half(ts, 0, u, v);
-    float mx = half_max(v, 0, u, -INFINITY);
-    load_half(ts, 1, u, v);
-    mx = half_max(v, 1, u, mx);
+    load_half<GR>(ts, 0, u, v);
+    float mx = half_max<GR>(v, 0, u, -INFINITY);
+    load_half<GR>(ts, 1, u, v);
+    mx = half_max<GR>(v, 1, u, mx);
     if (__any_sync(0xffffffffu, mx > M + kv8::kTau)) {
         const float m = fmaxf(M, ceilf(mx)), w = part_weight(M, m);
         M = m;
@@ -259,9 +303,9 @@ __device__ __forceinline__ void softmax_unit(uint32_t ts, uint32_t to, const Row
         }
     }
     const float ref = kv8::kOff - (M == -INFINITY ? 0.f : M);
-    l = half_weights(ts, 1, u, v, ref, l);
-    load_half(ts, 0, u, v);
-    l = half_weights(ts, 0, u, v, ref, l);
+    l = half_weights<GR>(ts, 1, u, v, ref, l);
+    load_half<GR>(ts, 0, u, v);
+    l = half_weights<GR>(ts, 0, u, v, ref, l);
     tmem_wait_st();
 }
 
@@ -291,7 +335,7 @@ __device__ __forceinline__ void write_stats(const AttnArgs &a, const TileRow &t,
             l == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) - kv8::kOff + log2f(l)) * 0.693147180559945f;
 }
 
-template <Kv8 KV, int D, bool PAIR>
+template <Kv8 KV, int D, bool PAIR, int GR>
 __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
     using namespace tl;
     using L = Lay<D, PAIR>;
@@ -313,10 +357,10 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
     if (tid == 0) {
         for (int i = 0; i < NRAW; ++i) {
             mbar_init(bar(B_RAWFULL + i), 1);
-            mbar_init(bar(B_RAWFREE + i), 4);
+            mbar_init(bar(B_RAWFREE + i), 2);
         }
         for (int i = 0; i < NCV; ++i) {
-            mbar_init(bar(B_CVFULL + i), 4);
+            mbar_init(bar(B_CVFULL + i), 2);
             mbar_init(bar(B_CVFREE + i), 1);
         }
         for (int i = 0; i < NSC; ++i) mbar_init(bar(B_SC + i), 1);
@@ -349,8 +393,13 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s_tmem;
-    auto wait = [&](int b, uint32_t parity) { return role_wait(bar(b), parity & 1u, a.limit_ns, &s_abort); };
-    auto warp_wait = [&](int b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+    // one barrier (b0), or several: lane i has b_i, of phase n_i; a negative b_i is none
+    auto warp_wait = [&](int b, uint32_t n) { return warp_wait_all(bar(b), n & 1u, true, a.limit_ns, &s_abort); };
+    auto warp_wait3 = [&](int b0, uint32_t n0, int b1, uint32_t n1, int b2, uint32_t n2) {
+        const int b = lane == 0 ? b0 : lane == 1 ? b1 : lane == 2 ? b2 : -1;
+        const uint32_t n = lane == 0 ? n0 : lane == 1 ? n1 : n2;
+        return warp_wait_all(bar(max(b, 0)), n & 1u, b >= 0, a.limit_ns, &s_abort);
+    };
     auto tiles_of = [&](const Cur &c) { return PAIR && c.r.n * a.G - c.b * RB > TR ? 2 : 1; };
 
     if (warp < 8) {
@@ -419,10 +468,8 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
             constexpr uint32_t id_s = idesc_f16(TR, UT, false), id_o = idesc_f16(TR, D, true);
             bool ok = tmem == 0, issued = false;     // all of the TMEM is ours: its base is 0
             if (!ok) s_abort = 1;
-            auto cv_wait = [&](int x) { ok = ok && warp_wait(B_CVFULL + x % NCV, (uint32_t)(x / NCV)); };
             // scores of unit k into buffer b from query tile q; the key slot is given back after the last
             auto scores = [&](int b, int q, int k, bool free) {
-                cv_wait(2 * k);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t dq = sdesc_sw128(sb + L::OFF_Q + (uint32_t)q * NSL * SLAB, 16, 1024);
@@ -442,7 +489,6 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
             // the weights of buffer b with unit k's values onto its sums (last: the item's last
             // here); the value slot is given back after the last
             auto sums = [&](int b, int k, bool fresh, bool last, bool free) {
-                cv_wait(2 * k + 1);
                 if (!ok) return;
                 tc_fence_after();
                 const uint64_t dv = sdesc_sw128(sb + L::OFF_CV + (uint32_t)((2 * k + 1) % NCV) * L::CV, SLAB, 1024);
@@ -465,7 +511,7 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
                     if (t < nt0) {
-                        ok = ok && warp_wait(B_Q + t, nq[t]++);
+                        ok = ok && warp_wait3(B_Q + t, nq[t]++, t == 0 ? B_CVFULL : -1, 0, -1, 0);
                         scores(t, t, 0, t + 1 == nt0);
                     }
 #pragma unroll 1
@@ -477,14 +523,21 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                         n.next_unit(a);
                         ntn = tiles_of(n);
                     }
+                    const int xv = 2 * k + 1, xk = 2 * k + 2;
+                    bool keys = false;       // the next unit's are known to be there
 #pragma unroll
                     for (int t = 0; t < 2; ++t) {
                         if (t < ntc) {
-                            ok = ok && warp_wait(B_P + t, np[t]++);
+                            ok = ok && warp_wait3(B_P + t, np[t]++, t == 0 ? B_CVFULL + xv % NCV : -1, (uint32_t)(xv / NCV),
+                                                  -1, 0);
                             sums(t, k, first, last, t + 1 == ntc);
                         }
                         if (t < ntn) {
-                            if (n.t == 0) ok = ok && warp_wait(B_Q + t, nq[t]++);
+                            if (n.t == 0 || !keys)
+                                ok = ok && warp_wait3(n.t == 0 ? B_Q + t : -1, nq[t], keys ? -1 : B_CVFULL + xk % NCV,
+                                                      (uint32_t)(xk / NCV), -1, 0);
+                            nq[t] += n.t == 0;
+                            keys = true;
                             scores(t, t, k + 1, t + 1 == ntn);
                         }
                     }
@@ -496,7 +549,9 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                 n = c;
                 uint32_t nq = 0;
                 auto next_scores = [&](int k) {      // n is at unit k
-                    if (k == 0 || n.t == 0) ok = ok && warp_wait(B_Q, nq++);
+                    const bool fresh = k == 0 || n.t == 0;
+                    ok = ok && warp_wait3(B_CVFULL + (2 * k) % NCV, (uint32_t)(2 * k / NCV), fresh ? B_Q : -1, nq, -1, 0);
+                    nq += fresh;
                     scores(k & 1, 0, k, true);
                     n.next_unit(a);
                 };
@@ -506,7 +561,7 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
 #pragma unroll 1
                 for (int k = 0; ok && k < units; ++k) {
                     const int b = k & 1, k1 = min(units, k + c.nt - c.t);   // the item's end here
-                    ok = warp_wait(B_P + b, (uint32_t)(k >> 1));
+                    ok = warp_wait3(B_P + b, (uint32_t)(k >> 1), B_CVFULL + (2 * k + 1) % NCV, (uint32_t)((2 * k + 1) / NCV), -1, 0);
                     sums(b, k, k - k0 < 2, k + 2 >= k1, true);
                     if (ok && k + 2 < units) next_scores(k + 2);
                     c.next_unit(a);
@@ -522,53 +577,62 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
             }
         } else if (warp >= 4) {
             // ============================================================ widening
-            // A thread takes 8 codes of a row to 16 bytes of halves: reads and swizzled writes
-            // both fall on distinct banks, and a thread's rows keep its place in the swizzle.
+            // Two warps widen the keys, two the values, so that one pair's waits lie under the
+            // other's work.  A thread takes 8 codes of a row to 16 bytes of halves: reads and
+            // swizzled writes both fall on distinct banks, a thread's rows keep its place in the
+            // swizzle, and all of a thread's reads are in flight at once.
             Cur c;
             c.start(a, s_place);
-            const int ct = tid - 128;
-            constexpr int PPR = D / 8, RPI = 128 / PPR, IT = UT / RPI;   // pieces a row, rows a step, steps
+            const int w = (warp - 4) >> 1, ct = tid & 63;                // keys or values
+            constexpr int PPR = D / 8, RPI = 64 / PPR, IT = UT / RPI, NB = IT;   // pieces a row, rows a step, steps, batch
             const int row0 = ct / PPR, piece = ct % PPR;
             const uint32_t src0 = sb + L::OFF_RAW + (uint32_t)ct * 8;
-            const uint32_t dst0 = sb + L::OFF_CV + (uint32_t)(piece >> 3) * SLAB + (uint32_t)row0 * 128u +
-                                  (((uint32_t)(piece & 7) ^ (uint32_t)(row0 & 7)) << 4);
-            int x = 0;
+            const uint32_t dst0 = sb + L::OFF_CV + (uint32_t)(piece >> 3) * SLAB + (uint32_t)row0 * 128u;
+            const uint32_t sw0 = ((uint32_t)(piece & 7) ^ (uint32_t)(row0 & 7)) << 4;
             bool ok = true;
 #pragma unroll 1
-            for (int k = 0; k < units && ok; ++k) {
-#pragma unroll 1
-                for (int w = 0; w < 2; ++w, ++x) {
-                    const int rs = x % NRAW, cs = x % NCV;
-                    ok = warp_wait(B_RAWFULL + rs, (uint32_t)(x / NRAW));
-                    if (ok && x >= NCV) ok = warp_wait(B_CVFREE + cs, (uint32_t)(x / NCV - 1));
-                    if (ok && w == 1) ok = warp_wait(B_SC + k % NSC, (uint32_t)(k / NSC));
-                    if (!ok) break;
-                    const uint32_t src = src0 + (uint32_t)rs * L::RAW, dst = dst0 + (uint32_t)cs * L::CV;
-                    // value codes of places without a cached token: zero, so that no stale NaN
-                    // meets a zero weight (stale keys only reach scores that are masked)
-                    const int left = w == 0 ? UT : c.r.kv - c.t * UT;
-                    const bool holes = w == 1 && s_gone[k % NSC];
-                    const bool plain = left >= UT && !holes;
-#pragma unroll 4
-                    for (int i = 0; i < IT; ++i) {
-                        uint32_t u0, u1, h0, h1, h2, h3;
-                        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(u0), "=r"(u1) : "r"(src + (uint32_t)i * 1024u));
-                        if (!plain) {
-                            const int row = row0 + i * RPI;
-                            if (row >= left || (holes && s_sc[(k % NSC) * 8 + (row >> 4)].y < 0.f)) u0 = u1 = 0;
+            for (int k = 0, x = w; k < units; ++k, x += 2) {
+                const int rs = x % NRAW, cs = x % NCV;
+                ok = warp_wait3(B_RAWFULL + rs, (uint32_t)(x / NRAW), x >= NCV ? B_CVFREE + cs : -1, (uint32_t)(x / NCV - 1),
+                                w == 1 ? B_SC + k % NSC : -1, (uint32_t)(k / NSC));
+                if (!ok) break;
+                const uint32_t src = src0 + (uint32_t)rs * L::RAW, dst = dst0 + (uint32_t)cs * L::CV;
+                // value codes of places without a cached token: zero, so that no stale NaN
+                // meets a zero weight (stale keys only reach scores that are masked)
+                const int left = w == 0 ? UT : c.r.kv - c.t * UT;
+                const bool holes = w == 1 && s_gone[k % NSC];
+                const bool plain = left >= UT && !holes;
+#pragma unroll
+                for (int i0 = 0; i0 < IT; i0 += NB) {
+                    uint32_t u[NB][2];
+#pragma unroll
+                    for (int i = 0; i < NB; ++i)
+                        asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(u[i][0]), "=r"(u[i][1])
+                                     : "r"(src + (uint32_t)(i0 + i) * 512u));
+                    if (!plain) {
+#pragma unroll
+                        for (int i = 0; i < NB; ++i) {
+                            const int row = row0 + (i0 + i) * RPI;
+                            if (row >= left || (holes && s_sc[(k % NSC) * 8 + (row >> 4)].y < 0.f)) u[i][0] = u[i][1] = 0;
                         }
-                        decode4_h<KV>(u0, h0, h1);
-                        decode4_h<KV>(u1, h2, h3);
-                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (uint32_t)(i * RPI) * 128u), "r"(h0),
-                                     "r"(h1), "r"(h2), "r"(h3)
+                    }
+#pragma unroll
+                    for (int i = 0; i < NB; ++i) {
+                        uint32_t h0, h1, h2, h3;
+                        decode4_h<KV>(u[i][0], h0, h1);
+                        decode4_h<KV>(u[i][1], h2, h3);
+                        // the row's place in the swizzle moves with a step's rows (4 or 8)
+                        const uint32_t sw = sw0 ^ (uint32_t)((((i0 + i) * RPI) & 7) << 4);
+                        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(dst + (uint32_t)((i0 + i) * RPI) * 128u + sw),
+                                     "r"(h0), "r"(h1), "r"(h2), "r"(h3)
                                      : "memory");
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) {
-                        mbar_arrive(bar(B_RAWFREE + rs));
-                        mbar_arrive(bar(B_CVFULL + cs));
-                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bar(B_RAWFREE + rs));
+                    mbar_arrive(bar(B_CVFULL + cs));
                 }
                 c.next_unit(a);
             }
@@ -615,22 +679,40 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
             float M = -INFINITY, l = 0.f;
             if (mine_item) {
                 const int j0 = PAIR ? 0 : (k ^ b) & 1, dj = PAIR ? 1 : 2;   // not PAIR: units of this parity
+                RowUnit<GR> u;
+                u.cs = cs;
+                bool gone = false;
+                auto scales_of = [&](int kk) {     // of unit kk, whose scale slot has been waited for
+                    u.sc = s_sc + (kk % NSC) * 8;
+                    if constexpr (GR == 1) u.held[0] = u.sc[0], u.held[1] = u.sc[4];
+                    gone = s_gone[kk % NSC];
+                };
 #pragma unroll 1
                 for (int j = j0; j < mine && ok; j += dj) {
-                    const int kk = k + j, see = r.lim - (t0 + j) * UT;
-                    // the scores first: a tile that sat out items is then at this unit, and the
-                    // scale slot's phase is the one before or after its publication
-                    ok = warp_wait(B_S + b, ns++) && warp_wait(B_SC + kk % NSC, (uint32_t)(kk / NSC));
+                    const int kk = k + j;
+                    ok = warp_wait(B_S + b, ns++);
+                    // An item's first unit: the scores came first, so a tile that sat out items is now
+                    // at this unit and the scale slot's phase is the one before or after its publication.
+                    if (ok && j == j0) {
+                        ok = warp_wait(B_SC + kk % NSC, (uint32_t)(kk / NSC));
+                        scales_of(kk);
+                    }
                     if (!ok) break;
                     tc_fence_after();
-                    const bool part = __any_sync(0xffffffffu, see < UT) || s_gone[kk % NSC];
-                    softmax_unit<D>(ts, to, RowUnit{s_sc + (kk % NSC) * 8, see, part, cs}, j > j0, M, l);
+                    u.see = r.lim - (t0 + j) * UT;
+                    u.part = __any_sync(0xffffffffu, u.see < UT) || gone;
+                    softmax_unit<D, GR>(ts, to, u, j > j0, M, l);
                     // the weights let buffer 1's sums be written again: not before buffer 0's warps
                     // have read those of the item before
                     if (!PAIR && b == 1 && j == j0 && items > 0 && !(ok = warp_wait(B_OFREE, items - 1))) break;
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_P + b));
+                    // the next unit's scales, while its scores are made
+                    if (j + dj < mine) {
+                        ok = warp_wait(B_SC + (kk + dj) % NSC, (uint32_t)((kk + dj) / NSC));
+                        scales_of(kk + dj);
+                    }
                 }
             }
             // ---- the item's sums, after the next item's queries are on their way
@@ -711,17 +793,22 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
     grid_launch_dependents();
 }
 
-template <Kv8 KV, int D, bool PAIR>
-cudaError_t launch_tile_f(AttnArgs &a, void *ws, int ctas, int64_t rows, cudaStream_t s) {
+template <Kv8 KV, int D, bool PAIR, int GR>
+cudaError_t launch_tile_g(AttnArgs &a, void *ws, int ctas, int64_t rows, cudaStream_t s) {
     using L = tl::Lay<D, PAIR>;
     place_parts(a, ws, ctas, L::RB);
-    auto kernel = kv8_tile_kernel<KV, D, PAIR>;
+    auto kernel = kv8_tile_kernel<KV, D, PAIR, GR>;
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(kernel, L::SMEM, allowed);
     if (e != cudaSuccess) return e;
     kernel<<<(unsigned)ctas, tl::NT, L::SMEM, s>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     return launch_merge<__nv_bfloat16, D, L::RB, 1>(a, ctas, (int)(rows < L::RB ? rows : L::RB), s);
+}
+template <Kv8 KV, int D, bool PAIR>
+cudaError_t launch_tile_f(AttnArgs &a, void *ws, int ctas, int64_t rows, cudaStream_t s) {
+    return a.page_log2 >= 6 ? launch_tile_g<KV, D, PAIR, 1>(a, ws, ctas, rows, s)
+                            : launch_tile_g<KV, D, PAIR, 4>(a, ws, ctas, rows, s);
 }
 
 // Pairs of tiles where a request may have more rows than one tile.
