@@ -19,8 +19,8 @@
 // rows, where the cache's bytes bound): one tile of rows, whose units alternate between the
 // two score and output buffers; the two halves of the sum are joined at the item's end.
 //
-// Warps: 0 loads (page entries and scales looked up one unit ahead), 1 issues the products
-// and owns the TMEM, 4-7 widen (two the keys, two the values), 8-11 and 12-15 the softmax of buffer 0 and 1, a thread a row:
+// Warps: 0 loads (page entries and scales looked up one unit ahead), 1 and 2 issue the products
+// (1 owns the TMEM), 4-7 widen (two the keys, two the values), 8-11 and 12-15 the softmax of buffer 0 and 1, a thread a row:
 // maxima and sums never leave the thread.  No barrier spans the CTA inside the loop; every
 // wait is bounded.
 
@@ -40,8 +40,9 @@ constexpr uint32_t TM_S = 0, TM_O = 256, TM_COLS = 512;   // buffer b at + 128 b
 constexpr int MAXCV = 4;
 enum : int {
     B_RAWFULL = 0, B_RAWFREE = B_RAWFULL + NRAW, B_CVFULL = B_RAWFREE + NRAW, B_CVFREE = B_CVFULL + MAXCV,
-    B_SC = B_CVFREE + MAXCV, B_Q = B_SC + NSC, B_S = B_Q + 2, B_P = B_S + 2, B_O = B_P + 2, B_ML = B_O + 2,
-    B_OFREE = B_ML + 1, B_DRAIN = B_OFREE + 1, NUM_BARS = B_DRAIN + 1
+    B_SC = B_CVFREE + MAXCV, B_Q = B_SC + NSC, B_S = B_Q + 2, B_PU = B_S + 2, B_P = B_PU + 2, B_O = B_P + 2,
+    B_ML = B_O + 2, B_OFREE = B_ML + 1, B_DRAIN = B_OFREE + 1, B_U = B_DRAIN + 2,
+    NUM_BARS = B_U + 2
 };
 template <int D, bool PAIR> struct Lay {
     static constexpr int RB = PAIR ? kKv8TileRows : TR;   // rows of an item
@@ -196,10 +197,10 @@ __device__ __forceinline__ float stage_query(const AttnArgs &a, const TileRow &t
     return a.scale_log2 * fabsf(1.f / fac);
 }
 
-// One unit of one row: scores from TMEM, the weights as halves in their upper columns
-// (kP on), M and l moved on.  The maximum is taken half by half; the upper half stays in
-// registers, whose weights then go over it, and the lower half is read a second time: half
-// the registers of holding all 128 scores for one TMEM read more.
+// One unit of one row, in two halves of 64 keys, the upper first: scores from TMEM, M moved on
+// where a score exceeds it by much, the weights as halves to the upper columns (kP on; the
+// upper half's go over its own scores, the lower half's over the upper scores, which have been
+// read by then), l.  A half's sums can begin while the other half is worked on.
 // GR: groups of a half (64 keys) with a scale of their own: one where pages hold 64 tokens or
 // more, else four.
 // see: keys of the unit that the row sees; part: some row of the warp sees fewer than all, or
@@ -279,34 +280,54 @@ __device__ __forceinline__ float half_weights(uint32_t ts, int h, const RowUnit<
     }
     return l;
 }
-template <int D, int GR>
-__device__ __forceinline__ void softmax_unit(uint32_t ts, uint32_t to, const RowUnit<GR> &u, bool rescale, float &M, float &l) {
-    float v[2][32];
-    load_half<GR>(ts, 0, u, v);
-    float mx = half_max<GR>(v, 0, u, -INFINITY);
-    load_half<GR>(ts, 1, u, v);
-    mx = half_max<GR>(v, 1, u, mx);
-    if (__any_sync(0xffffffffu, mx > M + kv8::kTau)) {
-        const float m = fmaxf(M, ceilf(mx)), w = part_weight(M, m);
-        M = m;
-        l *= w;
-        if (rescale) {      // their products have landed: the scores' barrier came after them
+// Moves M to hold a half whose largest exponent is mx, and the sums so far with it: rare, since
+// M holds what exceeds it by up to kTau.  settled() waits until no product writes the sums.
+template <int D, typename Settled>
+__device__ __forceinline__ bool move_reference(uint32_t to, float mx, bool rescale, float &M, float &l, Settled settled) {
+    if (!__any_sync(0xffffffffu, mx > M + kv8::kTau)) return true;
+    const float m = fmaxf(M, ceilf(mx)), w = part_weight(M, m);
+    M = m;
+    l *= w;
+    if (!rescale) return true;
+    if (!settled()) return false;
 #pragma unroll 1
-            for (int cb = 0; cb < D / 8; ++cb) {     // few registers: the upper scores are held too
-                uint32_t o[8];
-                tmem_ld8(to + 8u * cb, o);
-                tmem_wait_ld();
+    for (int cb = 0; cb < D / 8; ++cb) {     // few registers: the scores are held too
+        uint32_t o[8];
+        tmem_ld8(to + 8u * cb, o);
+        tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w);
-                tmem_st8(to + 8u * cb, o);
-            }
-        }
+        for (int e = 0; e < 8; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * w);
+        tmem_st8(to + 8u * cb, o);
     }
-    const float ref = kv8::kOff - (M == -INFINITY ? 0.f : M);
-    l = half_weights<GR>(ts, 1, u, v, ref, l);
-    load_half<GR>(ts, 0, u, v);
-    l = half_weights<GR>(ts, 0, u, v, ref, l);
     tmem_wait_st();
+    return true;
+}
+// upper(): called when the weights of the upper half are in place; upper_done(): waits for their
+// products (false from either: give up).  BY_HALVES: the lower half's maximum is taken after the
+// upper half's weights are out, and waits for their products if it moves M; else both maxima
+// come first (the lower half is read twice) and nothing here waits for a product: with one
+// warp issuing for both buffers, in order, such a wait could meet one for the next item's
+// queries, which in turn wait for this unit.
+template <int D, int GR, bool BY_HALVES, typename Upper, typename UpperDone>
+__device__ __forceinline__ bool softmax_unit(uint32_t ts, uint32_t to, const RowUnit<GR> &u, bool rescale, float &M, float &l,
+                                             Upper upper, UpperDone upper_done) {
+    float v[2][32], mx = -INFINITY;
+    if constexpr (!BY_HALVES) {
+        load_half<GR>(ts, 0, u, v);
+        mx = half_max<GR>(v, 0, u, mx);
+    }
+    load_half<GR>(ts, 1, u, v);
+    // the earlier units' products have landed: the scores' barrier came after them
+    move_reference<D>(to, half_max<GR>(v, 1, u, mx), rescale, M, l, []() { return true; });
+    l = half_weights<GR>(ts, 1, u, v, kv8::kOff - (M == -INFINITY ? 0.f : M), l);
+    tmem_wait_st();
+    if (!upper()) return false;
+    load_half<GR>(ts, 0, u, v);
+    if constexpr (BY_HALVES)
+        if (!move_reference<D>(to, half_max<GR>(v, 0, u, -INFINITY), true, M, l, upper_done)) return false;
+    l = half_weights<GR>(ts, 0, u, v, kv8::kOff - (M == -INFINITY ? 0.f : M), l);
+    tmem_wait_st();
+    return true;
 }
 
 // A row's result: the output, or the part that the merge kernel joins.
@@ -361,18 +382,20 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
         }
         for (int i = 0; i < NCV; ++i) {
             mbar_init(bar(B_CVFULL + i), 2);
-            mbar_init(bar(B_CVFREE + i), 1);
+            mbar_init(bar(B_CVFREE + i), PAIR ? 2 : 1);
         }
         for (int i = 0; i < NSC; ++i) mbar_init(bar(B_SC + i), 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(bar(B_Q + i), 4);
             mbar_init(bar(B_S + i), 1);
+            mbar_init(bar(B_PU + i), 4);
             mbar_init(bar(B_P + i), 4);
+            mbar_init(bar(B_DRAIN + i), 1);
+            mbar_init(bar(B_U + i), 1);
             mbar_init(bar(B_O + i), 1);
         }
         mbar_init(bar(B_ML), 4);
         mbar_init(bar(B_OFREE), 4);
-        mbar_init(bar(B_DRAIN), 1);
         s_abort = 0;
         fence_mbar_init();
     }
@@ -461,16 +484,19 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
             if (s_abort && lane == 0)    // leave no copy in flight
                 for (int y = max(0, x - NRAW); y < x; ++y)
                     mbar_wait(bar(B_RAWFULL + y % NRAW), (uint32_t)(y / NRAW) & 1u, kCleanupLimitNs);
-        } else if (warp == 1) {
+        } else if (warp <= (PAIR ? 2 : 1)) {
             // ============================================================ products
-            // The whole warp walks the loop, so that the descriptors stay in uniform registers;
-            // one elected lane issues.
+            // PAIR: warp 1 + t issues tile t's, so that a tile waits for its own softmax only; else
+            // warp 1 both buffers'.  The whole warp walks the loop, so that the descriptors stay in
+            // uniform registers; one elected lane issues.
             constexpr uint32_t id_s = idesc_f16(TR, UT, false), id_o = idesc_f16(TR, D, true);
             bool ok = tmem == 0, issued = false;     // all of the TMEM is ours: its base is 0
-            if (!ok) s_abort = 1;
-            // scores of unit k into buffer b from query tile q; the key slot is given back after the last
-            auto scores = [&](int b, int q, int k, bool free) {
-                if (!ok) return;
+            if (!ok) {
+                s_abort = 1;
+                atomicOr(&g_device_error_word, kDevErrTimeout);
+            }
+            // scores of unit k into buffer b from query tile q; gives the key slot back
+            auto scores = [&](int b, int q, int k) {
                 tc_fence_after();
                 const uint64_t dq = sdesc_sw128(sb + L::OFF_Q + (uint32_t)q * NSL * SLAB, 16, 1024);
                 const uint64_t dk = sdesc_sw128(sb + L::OFF_CV + (uint32_t)((2 * k) % NCV) * L::CV, 16, 1024);
@@ -481,66 +507,78 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                         mma_bf16(TM_S + 128u * b, sdesc_add(dq, off), sdesc_add(dk, off), id_s, kk > 0);
                     }
                     mma_commit(bar(B_S + b));
-                    if (free) mma_commit(bar(B_CVFREE + (2 * k) % NCV));
+                    mma_commit(bar(B_CVFREE + (2 * k) % NCV));
                 }
                 __syncwarp();
                 issued = true;
             };
-            // the weights of buffer b with unit k's values onto its sums (last: the item's last
-            // here); the value slot is given back after the last
-            auto sums = [&](int b, int k, bool fresh, bool last, bool free) {
-                if (!ok) return;
+            // the weights of a half (h = 1: keys 64 on, which come first) of buffer b with unit k's
+            // values onto its sums
+            auto sums = [&](int b, int k, int h, bool fresh) {
                 tc_fence_after();
                 const uint64_t dv = sdesc_sw128(sb + L::OFF_CV + (uint32_t)((2 * k + 1) % NCV) * L::CV, SLAB, 1024);
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < UT / 16; ++kk)
-                        mma_f16_ts(TM_O + 128u * b, TM_S + 128u * b + kP + 8u * kk, sdesc_add(dv, kk * 2048), id_o,
-                                   (!fresh || kk > 0) ? 1u : 0u);
-                    if (free) mma_commit(bar(B_CVFREE + (2 * k + 1) % NCV));
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_f16_ts(TM_O + 128u * b, TM_S + 128u * b + kP + 32u * h + 8u * kk,
+                                   sdesc_add(dv, (4 * h + kk) * 2048), id_o, (!fresh || h == 0 || kk > 0) ? 1u : 0u);
+                    if (h == 1) mma_commit(bar(B_U + b));
+                }
+                __syncwarp();
+            };
+            // after the second half: gives the value slot back; last: the item's last sums here
+            auto sums_done = [&](int b, int k, bool last) {
+                if (elect_one()) {
+                    mma_commit(bar(B_CVFREE + (2 * k + 1) % NCV));
                     if (last) mma_commit(bar(B_O + b));
                 }
                 __syncwarp();
             };
+            auto just_free = [&](int x) {      // a unit without rows in this tile
+                ok = ok && warp_wait(B_CVFULL + x % NCV, (uint32_t)(x / NCV));
+                if (ok && lane == 0) mbar_arrive(bar(B_CVFREE + x % NCV));
+                __syncwarp();
+            };
             if constexpr (PAIR) {
+                const int t = warp - 1;
                 Cur c, n;                // the unit whose second product is next, and the one after it
                 c.start(a, s_place);
                 n = c;
-                uint32_t nq[2] = {0, 0}, np[2] = {0, 0};   // items and units that tile t has begun
-                const int nt0 = tiles_of(n);
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    if (t < nt0) {
-                        ok = ok && warp_wait3(B_Q + t, nq[t]++, t == 0 ? B_CVFULL : -1, 0, -1, 0);
-                        scores(t, t, 0, t + 1 == nt0);
+                uint32_t nq = 0, np = 0;         // items and units of this tile so far
+                // unit k, at n; keys: known to be widened
+                auto next_scores = [&](int k, bool fresh, bool keys) {
+                    if (t < tiles_of(n)) {
+                        if (fresh || !keys)
+                            ok = ok && warp_wait3(B_CVFULL + (2 * k) % NCV, (uint32_t)(2 * k / NCV), fresh ? B_Q + t : -1, nq, -1, 0);
+                        nq += fresh;
+                        if (ok) scores(t, t, k);
+                    } else {
+                        just_free(2 * k);
                     }
+                };
+                next_scores(0, true, false);
 #pragma unroll 1
                 for (int k = 0; ok && k < units; ++k) {
-                    const int ntc = tiles_of(c);
                     const bool last = c.t + 1 == c.nt || k + 1 == units, first = c.t == 0 || k == 0;
-                    int ntn = 0;
-                    if (k + 1 < units) {
-                        n.next_unit(a);
-                        ntn = tiles_of(n);
+                    const int xv = 2 * k + 1;
+                    const bool mine = t < tiles_of(c);
+                    bool keys = false;
+                    if (k + 1 < units) n.next_unit(a);
+                    if (mine) {
+                        ok = warp_wait3(B_PU + t, np, B_CVFULL + xv % NCV, (uint32_t)(xv / NCV), -1, 0);
+                        if (ok) sums(t, k, 1, first);
+                        // one look at the next keys on the way
+                        const int xk = 2 * k + 2;
+                        const bool look = lane == 1 && mbar_test_wait(bar(B_CVFULL + xk % NCV), (uint32_t)(xk / NCV) & 1u);
+                        ok = ok && warp_wait(B_P + t, np++);
+                        if (!ok) break;
+                        sums(t, k, 0, first);
+                        sums_done(t, k, last);
+                        keys = __any_sync(0xffffffffu, look);
+                    } else {
+                        just_free(xv);
                     }
-                    const int xv = 2 * k + 1, xk = 2 * k + 2;
-                    bool keys = false;       // the next unit's are known to be there
-#pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (t < ntc) {
-                            ok = ok && warp_wait3(B_P + t, np[t]++, t == 0 ? B_CVFULL + xv % NCV : -1, (uint32_t)(xv / NCV),
-                                                  -1, 0);
-                            sums(t, k, first, last, t + 1 == ntc);
-                        }
-                        if (t < ntn) {
-                            if (n.t == 0 || !keys)
-                                ok = ok && warp_wait3(n.t == 0 ? B_Q + t : -1, nq[t], keys ? -1 : B_CVFULL + xk % NCV,
-                                                      (uint32_t)(xk / NCV), -1, 0);
-                            nq[t] += n.t == 0;
-                            keys = true;
-                            scores(t, t, k + 1, t + 1 == ntn);
-                        }
-                    }
+                    if (k + 1 < units) next_scores(k + 1, n.t == 0, keys);
                     c = n;
                 }
             } else {
@@ -552,7 +590,7 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                     const bool fresh = k == 0 || n.t == 0;
                     ok = ok && warp_wait3(B_CVFULL + (2 * k) % NCV, (uint32_t)(2 * k / NCV), fresh ? B_Q : -1, nq, -1, 0);
                     nq += fresh;
-                    scores(k & 1, 0, k, true);
+                    if (ok) scores(k & 1, 0, k);
                     n.next_unit(a);
                 };
                 next_scores(0);
@@ -560,18 +598,22 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                 int k0 = 0;              // the item's first unit
 #pragma unroll 1
                 for (int k = 0; ok && k < units; ++k) {
-                    const int b = k & 1, k1 = min(units, k + c.nt - c.t);   // the item's end here
-                    ok = warp_wait3(B_P + b, (uint32_t)(k >> 1), B_CVFULL + (2 * k + 1) % NCV, (uint32_t)((2 * k + 1) / NCV), -1, 0);
-                    sums(b, k, k - k0 < 2, k + 2 >= k1, true);
-                    if (ok && k + 2 < units) next_scores(k + 2);
+                    const int b = k & 1, xv = 2 * k + 1, k1 = min(units, k + c.nt - c.t);   // the item's end here
+                    ok = warp_wait3(B_PU + b, (uint32_t)(k >> 1), B_CVFULL + xv % NCV, (uint32_t)(xv / NCV), -1, 0);
+                    if (ok) sums(b, k, 1, k - k0 < 2);
+                    ok = ok && warp_wait(B_P + b, (uint32_t)(k >> 1));
+                    if (!ok) break;
+                    sums(b, k, 0, k - k0 < 2);
+                    sums_done(b, k, k + 2 >= k1);
+                    if (k + 2 < units) next_scores(k + 2);
                     c.next_unit(a);
                     if (c.t == 0) k0 = k + 1;
                 }
             }
             if (s_abort && issued) {   // let this warp's products land before the TMEM goes away
                 if (elect_one()) {
-                    mma_commit(bar(B_DRAIN));
-                    mbar_wait(bar(B_DRAIN), 0u, kCleanupLimitNs);
+                    mma_commit(bar(B_DRAIN + warp - 1));
+                    mbar_wait(bar(B_DRAIN + warp - 1), 0u, kCleanupLimitNs);
                 }
                 __syncwarp();
             }
@@ -701,10 +743,20 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                     tc_fence_after();
                     u.see = r.lim - (t0 + j) * UT;
                     u.part = __any_sync(0xffffffffu, u.see < UT) || gone;
-                    softmax_unit<D, GR>(ts, to, u, j > j0, M, l);
-                    // the weights let buffer 1's sums be written again: not before buffer 0's warps
-                    // have read those of the item before
-                    if (!PAIR && b == 1 && j == j0 && items > 0 && !(ok = warp_wait(B_OFREE, items - 1))) break;
+                    ok = softmax_unit<D, GR, PAIR>(ts, to, u, j > j0, M, l, [&]() {
+                        // the weights let buffer 1's sums be written again: not before buffer 0's
+                        // warps have read those of the item before
+                        if (!PAIR && b == 1 && j == j0 && items > 0 && !warp_wait(B_OFREE, items - 1)) return false;
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(B_PU + b));
+                        return true;
+                    }, [&]() {
+                        const bool there = warp_wait(B_U + b, ns - 1);
+                        tc_fence_after();
+                        return there;
+                    });
+                    if (!ok) break;
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_P + b));

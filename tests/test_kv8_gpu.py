@@ -293,14 +293,16 @@ def test_pages_gone(dtype, qs):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
-@pytest.mark.parametrize("qs", [[1, 1], [4, 3], [140, 80]])
-def test_growing_scores(dtype, qs):
-    """Key scales that grow along the cache: every page raises the running maximum."""
-    x = attn_case([900, 640], qs, 8, 2, 128, 16, dtype, "int8", seed=6)
+@pytest.mark.parametrize("qs", [[1, 1], [4, 3], [20, 9], [31, 5], [140, 80]])
+@pytest.mark.parametrize("lens,page,every", [([900, 640], 16, 8), ([900, 640], 16, 1), ([1100, 129], 64, 1), ([128, 257], 32, 2)])
+def test_growing_scores(dtype, qs, lens, page, every):
+    """Key scales that grow along the cache: the running maximum moves inside and between
+    tiles, to the last one of a request."""
+    x = attn_case(lens, qs, 8, 2, 128, page, dtype, "int8", seed=6)
     for s in range(2):
         for i, p in enumerate(x["table"][s].tolist()):
             if p >= 0:
-                x["ks"][p] = 2.0 ** (i // 8 - 9)
+                x["ks"][p] = 2.0 ** (min(i // every, 18) / (2 if every == 1 else 1) - 9)
     check(x)
 
 
