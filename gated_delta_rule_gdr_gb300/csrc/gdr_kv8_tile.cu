@@ -171,27 +171,39 @@ __device__ __forceinline__ float stage_query(const AttnArgs &a, const TileRow &t
     const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + (int64_t)t.qrow * a.q_stride + (int64_t)t.hq * D;
     float amax = 0.f;
     auto piece = [&](int i) { return t.live ? reinterpret_cast<const uint4 *>(q)[i] : make_uint4(0, 0, 0, 0); };
-#pragma unroll 4
-    for (int i = 0; i < D / 8; ++i) {
-        const uint4 u = piece(i);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    // two reads of the row (the second from L1) rather than 64 registers held; eight loads in
+    // flight, since each is a trip to L2
+#pragma unroll 1
+    for (int i0 = 0; i0 < D / 8; i0 += 8) {
+        uint4 u[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+        for (int i = 0; i < 8; ++i) u[i] = piece(i0 + i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+        }
     }
     const float fac = row_factor(amax) * a.sign;
     if (dst) {
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-            const uint4 u = piece(i);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-            uint32_t h[4];
+#pragma unroll 1
+        for (int i0 = 0; i0 < D / 8; i0 += 8) {      // a slab of 64 values
+            uint4 u[8];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                h[e] = pack_h2(__uint_as_float(w[e] << 16) * fac, __uint_as_float(w[e] & 0xffff0000u) * fac);
-            *reinterpret_cast<uint4 *>(dst + (uint32_t)(i >> 3) * tl::SLAB + (uint32_t)row * 128u +
-                                       (((uint32_t)(i & 7) ^ (uint32_t)(row & 7)) << 4)) =
-                make_uint4(h[0], h[1], h[2], h[3]);
+            for (int i = 0; i < 8; ++i) u[i] = piece(i0 + i);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+                uint32_t h[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    h[e] = pack_h2(__uint_as_float(w[e] << 16) * fac, __uint_as_float(w[e] & 0xffff0000u) * fac);
+                *reinterpret_cast<uint4 *>(dst + (uint32_t)(i0 >> 3) * tl::SLAB + (uint32_t)row * 128u +
+                                           (((uint32_t)i ^ (uint32_t)(row & 7)) << 4)) =
+                    make_uint4(h[0], h[1], h[2], h[3]);
+            }
         }
     }
     return a.scale_log2 * fabsf(1.f / fac);
@@ -706,11 +718,24 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
         };
         bool mine_item = !PAIR || b < tiles_of(c);
         if (mine_item) enter_item();
+        // the next item's rows start on their way to L2 while this one is worked on
+        auto prefetch_next = [&]() {
+            Cur n = c;
+            if (k + (c.nt - c.t) >= units) return;
+            n.next_of_item(a);
+            const TileRow x = tile_row<RB>(a, n, (PAIR ? b * TR : 0) + row);
+            if (!x.live) return;
+            const char *p = reinterpret_cast<const char *>(static_cast<const __nv_bfloat16 *>(a.q) + (int64_t)x.qrow * a.q_stride +
+                                                           (int64_t)x.hq * D);
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p + D * 2 - 16));
+        };
 #pragma unroll 1
         while (k < units && ok) {
             const int mine = min(c.nt - c.t, units - k);      // the CTA's units of this item
             const bool first = c.t == 0, last = c.t + mine == c.nt, whole = first && last;
             const int t0 = c.t;
+            prefetch_next();
             if (tid == 256) {
                 // the CTA's entry: an item that begins here and ends elsewhere (its last)
                 if (first && !last)
