@@ -543,8 +543,7 @@ cudaError_t launch_split_r(AttnArgs &a, const void *kc, const void *vc, void *ws
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(kernel, sp::SMEM<R, D>, allowed);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)ctas, sp::NT, sp::SMEM<R, D>, s>>>(mk, mv, a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_after(kernel, dim3((unsigned)ctas), sp::NT, sp::SMEM<R, D>, s, mk, mv, a)) != cudaSuccess) return e;
     return launch_merge<E, D, 8 * R, 8>(a, ctas, rows, s);
 }
 // One block of 8 rows where no request has more, else two.

@@ -253,81 +253,96 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
 }
 
 // ------------------------------------------------------------------ merge of divided items
-// WPR warps take one row: each the parts in turn, lanes the D values.
-template <typename E, int D, int RB, int WPR>
+// WPR warps take one row, the parts in turn (few rows, many parts), or one warp takes RPW rows
+// one after another (many rows, few parts: fewer CTAs, each of which first waits for its
+// entry); lanes the D values.
+template <typename E, int D, int RB, int WPR, int RPW>
 __global__ void __launch_bounds__(256) kv8_merge_kernel(const AttnArgs a) {
-    constexpr int RPC = 8 / WPR, VL = D / 32;    // rows a CTA
-    __shared__ float s_o[8][D];
+    static_assert(WPR == 1 || RPW == 1, "");
+    constexpr int VL = D / 32;
+    __shared__ float s_o[WPR > 1 ? 8 : 1][D];
     __shared__ float s_l[8];
     grid_dependency_wait();
+    grid_launch_dependents();
     const int c0 = blockIdx.x;
     const int4 en = a.entry[c0];
     if (en.x < 0) return;
     const Request r = request_of(a, en.y);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w0 = warp / WPR * WPR;
-    const int row = blockIdx.y * RPC + warp / WPR, at = en.w * RB + row;
-    const bool live = row < RB && at < r.n * a.G;
-    const int parts = live ? en.x - c0 + 1 : 0;
-    auto slot = [&](int p) { return ((int64_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * RB + row; };
-    float M = -INFINITY;
-    for (int p = lane; p < parts; p += 32) M = fmaxf(M, a.part_ml[2 * slot(p)]);
+    const int row0 = (blockIdx.y * (8 / WPR) + warp / WPR) * RPW, parts = en.x - c0 + 1;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    const float ref = M == -INFINITY ? 0.f : M;
-    float o[VL] = {}, l = 0.f;
+    for (int rr = 0; rr < RPW; ++rr) {
+        const int row = row0 + rr, at = en.w * RB + row;
+        const bool live = row < RB && at < r.n * a.G;
+        auto slot = [&](int p) { return ((int64_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * RB + row; };
+        float M = -INFINITY;
+        for (int p = lane; p < parts && live; p += 32) M = fmaxf(M, a.part_ml[2 * slot(p)]);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        const float ref = M == -INFINITY ? 0.f : M;
+        float o[VL] = {}, l = 0.f;
 #pragma unroll 4
-    for (int p = warp - w0; p < parts; p += WPR) {
-        const int64_t k = slot(p);
-        const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * k);
-        // a part without an exponent weighs 0; if its sums are NaN (all its scores are) they stay NaN
-        const float w = part_weight(ml.x, ref);
-        l = fmaf(w, ml.y, l);
-        const float *src = a.part_o + k * D + lane * VL;
+        for (int p = warp - w0; p < parts && live; p += WPR) {
+            const int64_t k = slot(p);
+            const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * k);
+            // a part without an exponent weighs 0; if its sums are NaN (all its scores are) they stay NaN
+            const float w = part_weight(ml.x, ref);
+            l = fmaf(w, ml.y, l);
+            const float *src = a.part_o + k * D + lane * VL;
 #pragma unroll
-        for (int e = 0; e < VL; ++e) o[e] = fmaf(w, src[e], o[e]);
-    }
-    if constexpr (WPR > 1) {
-        if (lane == 0) s_l[warp] = l;
+            for (int e = 0; e < VL; ++e) o[e] = fmaf(w, src[e], o[e]);
+        }
+        if constexpr (WPR > 1) {
+            if (lane == 0) s_l[warp] = l;
 #pragma unroll
-        for (int e = 0; e < VL; ++e) s_o[warp][lane * VL + e] = o[e];
-        __syncthreads();
-        if (warp != w0) return;
-        l = 0.f;
+            for (int e = 0; e < VL; ++e) s_o[warp][lane * VL + e] = o[e];
+            __syncthreads();
+            if (warp != w0) return;
+            l = 0.f;
 #pragma unroll
-        for (int w = 0; w < WPR; ++w) l += s_l[w0 + w];
+            for (int w = 0; w < WPR; ++w) l += s_l[w0 + w];
+#pragma unroll
+            for (int e = 0; e < VL; ++e) {
+                o[e] = 0.f;
+#pragma unroll
+                for (int w = 0; w < WPR; ++w) o[e] += s_o[w0 + w][lane * VL + e];
+            }
+        }
+        if (!live) continue;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const int64_t orow = (int64_t)(r.q0 + at / a.G) * a.Hq + en.z * a.G + at % a.G;
 #pragma unroll
         for (int e = 0; e < VL; ++e) {
-            o[e] = 0.f;
-#pragma unroll
-            for (int w = 0; w < WPR; ++w) o[e] += s_o[w0 + w][lane * VL + e];
+            if constexpr (sizeof(E) == 4)
+                static_cast<float *>(a.out)[orow * D + lane * VL + e] = o[e] * inv;
+            else
+                static_cast<__nv_bfloat16 *>(a.out)[orow * D + lane * VL + e] = __float2bfloat16_rn(o[e] * inv);
         }
+        if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : (ref - kv8::kOff + log2f(l)) * 0.693147180559945f;
     }
-    if (!live) return;
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const int64_t orow = (int64_t)(r.q0 + at / a.G) * a.Hq + en.z * a.G + at % a.G;
-#pragma unroll
-    for (int e = 0; e < VL; ++e) {
-        if constexpr (sizeof(E) == 4)
-            static_cast<float *>(a.out)[orow * D + lane * VL + e] = o[e] * inv;
-        else
-            static_cast<__nv_bfloat16 *>(a.out)[orow * D + lane * VL + e] = __float2bfloat16_rn(o[e] * inv);
-    }
-    if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : (ref - kv8::kOff + log2f(l)) * 0.693147180559945f;
 }
 
-template <typename E, int D, int RB, int WPR>
-cudaError_t launch_merge(const AttnArgs &a, int ctas, int rows, cudaStream_t s) {
-    constexpr int RPC = 8 / WPR;
+// A launch that may start while the kernel before it in the stream ends (both wait before they
+// read what another kernel writes).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A &...args) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ctas, (unsigned)(((rows < RB ? rows : RB) + RPC - 1) / RPC));
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv8_merge_kernel<E, D, RB, WPR>, a);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+template <typename E, int D, int RB, int WPR>
+cudaError_t launch_merge(const AttnArgs &a, int ctas, int rows, cudaStream_t s) {
+    constexpr int RPW = WPR == 1 ? 4 : 1, RPC = 8 / WPR * RPW;
+    return launch_after(kv8_merge_kernel<E, D, RB, WPR, RPW>, dim3((unsigned)ctas, (unsigned)(((rows < RB ? rows : RB) + RPC - 1) / RPC)),
+                        256, 0, s, a);
 }
 
 // Entries, then {M, l}, then the sums.

@@ -878,8 +878,7 @@ cudaError_t launch_tile_g(AttnArgs &a, void *ws, int ctas, int64_t rows, cudaStr
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(kernel, L::SMEM, allowed);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)ctas, tl::NT, L::SMEM, s>>>(a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    if ((e = launch_after(kernel, dim3((unsigned)ctas), tl::NT, L::SMEM, s, a)) != cudaSuccess) return e;
     return launch_merge<__nv_bfloat16, D, L::RB, 1>(a, ctas, (int)(rows < L::RB ? rows : L::RB), s);
 }
 template <Kv8 KV, int D, bool PAIR>
