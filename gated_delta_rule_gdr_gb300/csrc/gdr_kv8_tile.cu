@@ -160,7 +160,7 @@ __device__ __forceinline__ TileRow tile_row(const AttnArgs &a, const Cursor<RB, 
     const int i = t.live ? at / a.G : 0;
     t.qrow = c.r.q0 + i;
     t.hq = c.h * a.G + (t.live ? at - i * a.G : 0);
-    t.lim = t.live ? seen_by(c.r, i) : 0;
+    t.lim = t.live ? seen_by(c.r, i) : 0x3fffffff;   // a row that is not there needs no mask
     return t;
 }
 
@@ -209,23 +209,81 @@ __device__ __forceinline__ float stage_query(const AttnArgs &a, const TileRow &t
     return a.scale_log2 * fabsf(1.f / fac);
 }
 
-// One unit of one row, in two halves of 64 keys, the upper first: scores from TMEM, M moved on
-// where a score exceeds it by much, the weights as halves to the upper columns (kP on; the
-// upper half's go over its own scores, the lower half's over the upper scores, which have been
-// read by then), l.  A half's sums can begin while the other half is worked on.
+// One unit of one row, the upper half's keys (64 on) first: scores from TMEM, M moved on where a
+// score exceeds it by much, the weights as halves to the upper columns (kP on; they go over
+// scores that have been read by then), l.  By halves, or in a loop over chunks of 32 keys
+// whose scores are read twice: the chunked code is a quarter of the size, and where many
+// warps with little to do share the instruction caches their misses were the largest stall
+// (3.7 of 10 warps waiting for instructions).
 // GR: groups of a half (64 keys) with a scale of their own: one where pages hold 64 tokens or
 // more, else four.
-// see: keys of the unit that the row sees; part: some row of the warp sees fewer than all, or
-// a page is gone; rescale: the output buffer holds sums of earlier units.
 constexpr uint32_t kP = 64;
 template <int GR> struct RowUnit {
     const float4 *sc;              // the unit's scales: {ks, vs, log2 vs, 1 / vs} a group of 16
-    float4 held[GR == 1 ? 2 : 1];  // GR 1: those of the halves
-    int see;
-    bool part;
+    int see;                       // keys of the unit that the row sees
+    bool part;                     // some row of the warp sees fewer than all, or a page is gone
     float cs;
-    __device__ __forceinline__ float4 scales(int h, int i) const { return GR == 1 ? held[GR == 1 ? h : 0] : sc[4 * h + i]; }
 };
+// A factor of at least 2^-126 keeps masked scores at -inf where a scale is zero.
+__device__ __forceinline__ float unit_factor(float cs, float ks) { return fmaxf(cs * ks, 1.2e-38f); }
+template <int GR>
+__device__ __forceinline__ void load_chunk(uint32_t ts, int ch, const RowUnit<GR> &u, float (&v)[32]) {
+    tmem_ld32(ts + 32u * ch, v);
+    tmem_wait_ld();
+    if (u.part) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int n = u.sc[2 * ch + i].y < 0.f ? 0 : u.see - 32 * ch - 16 * i;
+#pragma unroll
+            for (int e = 0; e < 16; ++e)
+                if (e >= n) v[16 * i + e] = -INFINITY;
+        }
+    }
+}
+template <int GR>
+__device__ __forceinline__ float chunk_max(uint32_t ts, int ch, const RowUnit<GR> &u, float mx) {
+    constexpr int N = GR == 1 ? 32 : 16;
+    float v[32];
+    load_chunk<GR>(ts, ch, u, v);
+#pragma unroll
+    for (int i = 0; i < 32 / N; ++i) {
+        const float4 s4 = u.sc[GR == 1 ? 4 * (ch >> 1) : 2 * ch + i];
+        float m[2] = {fmaxf(v[N * i], v[N * i + 1]), fmaxf(v[N * i + 2], v[N * i + 3])};
+#pragma unroll
+        for (int e = 4; e < N; e += 2) m[(e / 2) & 1] = fmaxf(fmaxf(m[(e / 2) & 1], v[N * i + e]), v[N * i + e + 1]);
+        mx = fmaxf(mx, fmaf(fmaxf(m[0], m[1]), unit_factor(u.cs, s4.x), s4.z));
+    }
+    return mx;
+}
+template <int GR>
+__device__ __forceinline__ float chunk_weights(uint32_t ts, int ch, const RowUnit<GR> &u, float ref, float l) {
+    constexpr int N = GR == 1 ? 32 : 16;
+    float v[32];
+    uint32_t p[16];
+    load_chunk<GR>(ts, ch, u, v);
+#pragma unroll
+    for (int i = 0; i < 32 / N; ++i) {
+        const float4 s4 = u.sc[GR == 1 ? 4 * (ch >> 1) : 2 * ch + i];
+        const float kf = unit_factor(u.cs, s4.x), add = s4.z + ref;
+        const uint64_t kf2 = f2_pack(kf, kf), add2 = f2_pack(add, add);
+        uint64_t sum = 0;
+#pragma unroll
+        for (int e = N * i; e < N * i + N; e += 2) {
+            float p0, p1;
+            f2_unpack(f2_fma(f2_pack(v[e], v[e + 1]), kf2, add2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            sum = f2_add(sum, f2_pack(p0, p1));
+            p[e >> 1] = pack_h2(p0, p1);
+        }
+        float s0, s1;
+        f2_unpack(sum, s0, s1);
+        l = fmaf(s0 + s1, s4.w, l);
+    }
+    tmem_st16(ts + kP + 16u * ch, p);
+    return l;
+}
+// By halves: 64 scores in registers, read once.
 template <int GR>
 __device__ __forceinline__ void load_half(uint32_t ts, int h, const RowUnit<GR> &u, float (&v)[2][32]) {
     tmem_ld32(ts + 64u * h, v[0]);
@@ -241,8 +299,6 @@ __device__ __forceinline__ void load_half(uint32_t ts, int h, const RowUnit<GR> 
         }
     }
 }
-// A factor of at least 2^-126 keeps masked scores at -inf where a scale is zero.
-__device__ __forceinline__ float unit_factor(float cs, float ks) { return fmaxf(cs * ks, 1.2e-38f); }
 template <int GR>
 __device__ __forceinline__ float half_max(const float (&v)[2][32], int h, const RowUnit<GR> &u, float mx) {
     constexpr int N = 64 / GR;
@@ -253,7 +309,7 @@ __device__ __forceinline__ float half_max(const float (&v)[2][32], int h, const 
 #pragma unroll
         for (int e = 3; e + 1 < N; e += 2) m = fmaxf(fmaxf(m, x(e)), x(e + 1));
         m = fmaxf(m, x(N - 1));
-        const float4 s4 = u.scales(h, i);
+        const float4 s4 = u.sc[GR == 1 ? 4 * h : 4 * h + i];
         mx = fmaxf(mx, fmaf(m, unit_factor(u.cs, s4.x), s4.z));
     }
     return mx;
@@ -270,7 +326,7 @@ __device__ __forceinline__ float half_weights(uint32_t ts, int h, const RowUnit<
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
             if (e % N == 0) {
-                const float4 s4 = u.scales(h, (32 * cb + e) / 16);
+                const float4 s4 = u.sc[GR == 1 ? 4 * h : 4 * h + (32 * cb + e) / 16];
                 const float kf = unit_factor(u.cs, s4.x), add = s4.z + ref;
                 kf2 = f2_pack(kf, kf), add2 = f2_pack(add, add);
                 iv = s4.w;
@@ -292,7 +348,7 @@ __device__ __forceinline__ float half_weights(uint32_t ts, int h, const RowUnit<
     }
     return l;
 }
-// Moves M to hold a half whose largest exponent is mx, and the sums so far with it: rare, since
+// Moves M to hold scores whose largest exponent is mx, and the sums so far with it: rare, since
 // M holds what exceeds it by up to kTau.  settled() waits until no product writes the sums.
 template <int D, typename Settled>
 __device__ __forceinline__ bool move_reference(uint32_t to, float mx, bool rescale, float &M, float &l, Settled settled) {
@@ -303,7 +359,7 @@ __device__ __forceinline__ bool move_reference(uint32_t to, float mx, bool resca
     if (!rescale) return true;
     if (!settled()) return false;
 #pragma unroll 1
-    for (int cb = 0; cb < D / 8; ++cb) {     // few registers: the scores are held too
+    for (int cb = 0; cb < D / 8; ++cb) {
         uint32_t o[8];
         tmem_ld8(to + 8u * cb, o);
         tmem_wait_ld();
@@ -314,32 +370,46 @@ __device__ __forceinline__ bool move_reference(uint32_t to, float mx, bool resca
     tmem_wait_st();
     return true;
 }
-// upper(): called when the weights of the upper half are in place; upper_done(): waits for their
-// products (false from either: give up).  BY_HALVES: the lower half's maximum is taken after the
-// upper half's weights are out, and waits for their products if it moves M; else both maxima
-// come first (the lower half is read twice) and nothing here waits for a product: with one
-// warp issuing for both buffers, in order, such a wait could meet one for the next item's
-// queries, which in turn wait for this unit.
-template <int D, int GR, bool BY_HALVES, typename Upper, typename UpperDone>
+// publish(h): called when the weights of half h (1, then 0) are in place; upper_done(): waits
+// for the products of the upper half (false from either: give up).  BY_HALVES (the tensor
+// cores bound): a half's scores stay in registers between the maximum and the weights; the
+// lower half's maximum is taken after the upper half's weights are out, and waits for their
+// products if it moves M.  Else (the cache's bytes bound): chunk by chunk, all maxima first, and
+// nothing here waits for a product: with one warp issuing for both buffers, in order, such a
+// wait could meet one for the next item's queries, which in turn wait for this unit.
+// Measured: chunks against halves 0.274 / 0.352 ms at 32 x 5 rows of 8 heads on 16 k keys, 1.48
+// / 1.16 ms at 1000 tokens on 65 k.
+template <int D, int GR, bool BY_HALVES, typename Publish, typename UpperDone>
 __device__ __forceinline__ bool softmax_unit(uint32_t ts, uint32_t to, const RowUnit<GR> &u, bool rescale, float &M, float &l,
-                                             Upper upper, UpperDone upper_done) {
-    float v[2][32], mx = -INFINITY;
-    if constexpr (!BY_HALVES) {
+                                             Publish publish, UpperDone upper_done) {
+    auto ref = [&]() { return kv8::kOff - (M == -INFINITY ? 0.f : M); };
+    if constexpr (BY_HALVES) {
+        float v[2][32];
+        load_half<GR>(ts, 1, u, v);
+        // the earlier units' products have landed: the scores' barrier came after them
+        move_reference<D>(to, half_max<GR>(v, 1, u, -INFINITY), rescale, M, l, []() { return true; });
+        l = half_weights<GR>(ts, 1, u, v, ref(), l);
+        tmem_wait_st();
+        if (!publish(1)) return false;
         load_half<GR>(ts, 0, u, v);
-        mx = half_max<GR>(v, 0, u, mx);
-    }
-    load_half<GR>(ts, 1, u, v);
-    // the earlier units' products have landed: the scores' barrier came after them
-    move_reference<D>(to, half_max<GR>(v, 1, u, mx), rescale, M, l, []() { return true; });
-    l = half_weights<GR>(ts, 1, u, v, kv8::kOff - (M == -INFINITY ? 0.f : M), l);
-    tmem_wait_st();
-    if (!upper()) return false;
-    load_half<GR>(ts, 0, u, v);
-    if constexpr (BY_HALVES)
         if (!move_reference<D>(to, half_max<GR>(v, 0, u, -INFINITY), true, M, l, upper_done)) return false;
-    l = half_weights<GR>(ts, 0, u, v, kv8::kOff - (M == -INFINITY ? 0.f : M), l);
-    tmem_wait_st();
-    return true;
+        l = half_weights<GR>(ts, 0, u, v, ref(), l);
+        tmem_wait_st();
+        return publish(0);
+    } else {
+        float mx = -INFINITY;
+#pragma unroll 1
+        for (int ch = 3; ch >= 0; --ch) mx = chunk_max<GR>(ts, ch, u, mx);
+        move_reference<D>(to, mx, rescale, M, l, []() { return true; });
+#pragma unroll 1
+        for (int ch = 3; ch >= 0; --ch) {
+            l = chunk_weights<GR>(ts, ch, u, ref(), l);
+            if (ch & 1) continue;
+            tmem_wait_st();
+            if (!publish(ch >> 1)) return false;
+        }
+        return true;
+    }
 }
 
 // A row's result: the output, or the part that the merge kernel joins.
@@ -634,11 +704,11 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
             // Two warps widen the keys, two the values, so that one pair's waits lie under the
             // other's work.  A thread takes 8 codes of a row to 16 bytes of halves: reads and
             // swizzled writes both fall on distinct banks, a thread's rows keep its place in the
-            // swizzle, and all of a thread's reads are in flight at once.
+            // swizzle, and eight reads are in flight at once.
             Cur c;
             c.start(a, s_place);
             const int w = (warp - 4) >> 1, ct = tid & 63;                // keys or values
-            constexpr int PPR = D / 8, RPI = 64 / PPR, IT = UT / RPI, NB = IT;   // pieces a row, rows a step, steps, batch
+            constexpr int PPR = D / 8, RPI = 64 / PPR, IT = UT / RPI, NB = 8;   // pieces a row, rows a step, steps, batch
             const int row0 = ct / PPR, piece = ct % PPR;
             const uint32_t src0 = sb + L::OFF_RAW + (uint32_t)ct * 8;
             const uint32_t dst0 = sb + L::OFF_CV + (uint32_t)(piece >> 3) * SLAB + (uint32_t)row0 * 128u;
@@ -656,7 +726,7 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                 const int left = w == 0 ? UT : c.r.kv - c.t * UT;
                 const bool holes = w == 1 && s_gone[k % NSC];
                 const bool plain = left >= UT && !holes;
-#pragma unroll
+#pragma unroll 1
                 for (int i0 = 0; i0 < IT; i0 += NB) {
                     uint32_t u[NB][2];
 #pragma unroll
@@ -748,10 +818,10 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                 const int j0 = PAIR ? 0 : (k ^ b) & 1, dj = PAIR ? 1 : 2;   // not PAIR: units of this parity
                 RowUnit<GR> u;
                 u.cs = cs;
+                const bool any_live = __any_sync(0xffffffffu, r.live);
                 bool gone = false;
                 auto scales_of = [&](int kk) {     // of unit kk, whose scale slot has been waited for
                     u.sc = s_sc + (kk % NSC) * 8;
-                    if constexpr (GR == 1) u.held[0] = u.sc[0], u.held[1] = u.sc[4];
                     gone = s_gone[kk % NSC];
                 };
 #pragma unroll 1
@@ -760,21 +830,30 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                     ok = warp_wait(B_S + b, ns++);
                     // An item's first unit: the scores came first, so a tile that sat out items is now
                     // at this unit and the scale slot's phase is the one before or after its publication.
-                    if (ok && j == j0) {
+                    if (ok && j == j0 && any_live) {
                         ok = warp_wait(B_SC + kk % NSC, (uint32_t)(kk / NSC));
                         scales_of(kk);
                     }
                     if (!ok) break;
+                    if (!any_live) {      // a warp without rows: its weights are never looked at
+                        if (!PAIR && b == 1 && j == j0 && items > 0 && !(ok = warp_wait(B_OFREE, items - 1))) break;
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(bar(B_PU + b));
+                            mbar_arrive(bar(B_P + b));
+                        }
+                        continue;
+                    }
                     tc_fence_after();
                     u.see = r.lim - (t0 + j) * UT;
                     u.part = __any_sync(0xffffffffu, u.see < UT) || gone;
-                    ok = softmax_unit<D, GR, PAIR>(ts, to, u, j > j0, M, l, [&]() {
+                    ok = softmax_unit<D, GR, PAIR>(ts, to, u, j > j0, M, l, [&](int h) {
                         // the weights let buffer 1's sums be written again: not before buffer 0's
                         // warps have read those of the item before
-                        if (!PAIR && b == 1 && j == j0 && items > 0 && !warp_wait(B_OFREE, items - 1)) return false;
+                        if (!PAIR && h == 1 && b == 1 && j == j0 && items > 0 && !warp_wait(B_OFREE, items - 1)) return false;
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(B_PU + b));
+                        if (lane == 0) mbar_arrive(bar((h == 1 ? B_PU : B_P) + b));
                         return true;
                     }, [&]() {
                         const bool there = warp_wait(B_U + b, ns - 1);
@@ -782,10 +861,7 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                         return there;
                     });
                     if (!ok) break;
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_P + b));
-                    // the next unit's scales, while its scores are made
+                    // the next unit's scale slot, while its scores are made
                     if (j + dj < mine) {
                         ok = warp_wait(B_SC + (kk + dj) % NSC, (uint32_t)((kk + dj) / NSC));
                         scales_of(kk + dj);
