@@ -43,6 +43,7 @@ struct AttnArgs {
     float *part_ml;              // [CTA][2][RB][2]: reference exponent M, weight sum
     int4 *entry;                 // [CTA] {last CTA (-1: no divided item), request, head, block}
     int S, total_q, Hq, Hkv, G, W, page_log2, N;
+    bool wide;                   // out and part_o are 32-byte aligned
     uint64_t limit_ns;
 };
 

@@ -164,47 +164,67 @@ __device__ __forceinline__ TileRow tile_row(const AttnArgs &a, const Cursor<RB, 
     return t;
 }
 
-// The row's query, normalised, as a row of the K-major tile at `dst` (nullptr: not stored).
-// Returns the row's score factor.
+// The queries of a warp's 32 rows (rows row0 .. row0 + 31 of the item at c), in two steps:
+// begin_queries starts their copies, raw, to the K-major tile's rows 32 qd on (D / 8 lanes a
+// row: a lane reading its own row would touch 32 lines an instruction); end_queries, in the
+// same lanes' pieces, turns them to halves, all 32 rows scaled by one power of two that brings
+// the largest finite magnitude below 2^15, and returns the rows' score factor.  A row far
+// smaller than the largest one keeps scores good to 2^-25 of the largest row's, more than a
+// softmax can show.  Loops, not unrolled code: they run once an item, from cold caches.
 template <int D>
-__device__ __forceinline__ float stage_query(const AttnArgs &a, const TileRow &t, int row, uint8_t *dst) {
-    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + (int64_t)t.qrow * a.q_stride + (int64_t)t.hq * D;
-    float amax = 0.f;
-    auto piece = [&](int i) { return t.live ? reinterpret_cast<const uint4 *>(q)[i] : make_uint4(0, 0, 0, 0); };
-    // two reads of the row (the second from L1) rather than 64 registers held; eight loads in
-    // flight, since each is a trip to L2
+__device__ __forceinline__ uint32_t query_place(int qd, int i) {    // of this lane's piece of step i
+    constexpr int LPR = D / 8, RPI = 32 / LPR;    // lanes a row, rows a step
+    const uint32_t lane = threadIdx.x & 31, piece = lane % LPR, row = 32u * qd + RPI * i + lane / LPR;
+    return (piece >> 3) * tl::SLAB + row * 128u + (((piece & 7u) ^ (row & 7u)) << 4);
+}
+template <int D, int RB>
+__device__ __forceinline__ void begin_queries(const AttnArgs &a, const Cursor<RB, tl::UT> &c, int row0, int qd, uint32_t dst) {
+    constexpr int LPR = D / 8, RPI = 32 / LPR, IT = 32 / RPI;
+    const int lane = threadIdx.x & 31;
+    const int rows = min(RB, c.r.n * a.G - c.b * RB), first = row0 + lane / LPR;
+    int tok = (c.b * RB + first) / a.G, g = c.b * RB + first - tok * a.G;
+    const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + (int64_t)c.h * a.G * D + (lane % LPR) * 8;
 #pragma unroll 1
-    for (int i0 = 0; i0 < D / 8; i0 += 8) {
-        uint4 u[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) u[i] = piece(i0 + i);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
-        }
+    for (int i = 0; i < IT; ++i) {
+        const bool live = first + RPI * i < rows;
+        const void *src = live ? q + (int64_t)(c.r.q0 + tok) * a.q_stride + (int64_t)g * D : q;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + query_place<D>(qd, i)), "l"(src),
+                     "r"(live ? 16 : 0)      // a row that is not there: zeros
+                     : "memory");
+        for (g += RPI; g >= a.G; g -= a.G) ++tok;
     }
-    const float fac = row_factor(amax) * a.sign;
-    if (dst) {
+}
+template <int D>
+__device__ __forceinline__ float end_queries(const AttnArgs &a, int qd, uint8_t *dst) {
+    constexpr int IT = D / 8;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    uint32_t m = 0;                       // magnitudes compare as the bit patterns do
+#pragma unroll 4
+    for (int i = 0; i < IT; ++i) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(dst + query_place<D>(qd, i));
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu)));
+    }
+    m = __reduce_max_sync(0xffffffffu, max(m & 0xffff0000u, m << 16));
+    if (m >= 0x7f800000u) {               // infinities and NaN do not count
+        m = 0;
 #pragma unroll 1
-        for (int i0 = 0; i0 < D / 8; i0 += 8) {      // a slab of 64 values
-            uint4 u[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) u[i] = piece(i0 + i);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-                uint32_t h[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    h[e] = pack_h2(__uint_as_float(w[e] << 16) * fac, __uint_as_float(w[e] & 0xffff0000u) * fac);
-                *reinterpret_cast<uint4 *>(dst + (uint32_t)(i0 >> 3) * tl::SLAB + (uint32_t)row * 128u +
-                                           (((uint32_t)i ^ (uint32_t)(row & 7)) << 4)) =
-                    make_uint4(h[0], h[1], h[2], h[3]);
-            }
+        for (int i = 0; i < IT * 8; ++i) {
+            const uint32_t w = *reinterpret_cast<const uint16_t *>(dst + query_place<D>(qd, i >> 3) + 2 * (i & 7)) & 0x7fffu;
+            m = max(m, w < 0x7f80u ? w << 16 : 0u);
         }
+        m = __reduce_max_sync(0xffffffffu, m);
+    }
+    const float fac = row_factor(__uint_as_float(m)) * a.sign;
+#pragma unroll 2
+    for (int i = 0; i < IT; ++i) {
+        uint4 *p = reinterpret_cast<uint4 *>(dst + query_place<D>(qd, i));
+        const uint4 u = *p;
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            h[e] = pack_h2(__uint_as_float(w[e] << 16) * fac, __uint_as_float(w[e] & 0xffff0000u) * fac);
+        *p = make_uint4(h[0], h[1], h[2], h[3]);
     }
     return a.scale_log2 * fabsf(1.f / fac);
 }
@@ -412,21 +432,35 @@ __device__ __forceinline__ bool softmax_unit(uint32_t ts, uint32_t to, const Row
     }
 }
 
-// A row's result: the output, or the part that the merge kernel joins.
+// A row's result: the output, or the part that the merge kernel joins.  A lane writes its own
+// row: 32 bytes a store where everything is so aligned, whole sectors.
+__device__ __forceinline__ void store32(void *p, const uint32_t *w, bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                     "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+}
 template <int D, int RB>
 __device__ __forceinline__ void write_chunk(const AttnArgs &a, const TileRow &t, bool whole, int64_t slot, int cb,
                                             float inv, float (&o)[32]) {
     if (!t.live) return;
+    uint32_t w[32];
     if (whole) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] *= inv;
         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)t.qrow * a.Hq + t.hq) * D + 32 * cb;
 #pragma unroll
-        for (int e = 0; e < 32; e += 8) Vec16<__nv_bfloat16>::store(dst + e, o + e);
+        for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) store32(dst + 16 * e, w + 8 * e, a.wide);
     } else {
         float *dst = a.part_o + slot * D + 32 * cb;
 #pragma unroll
-        for (int e = 0; e < 32; e += 4) Vec16<float>::store(dst + e, o + e);
+        for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) store32(dst + 8 * e, w + 8 * e, a.wide);
     }
 }
 __device__ __forceinline__ void write_stats(const AttnArgs &a, const TileRow &t, bool whole, int64_t slot, float M, float l) {
@@ -451,6 +485,7 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
     __shared__ int64_t s_scan[NT / 32];
     __shared__ uint32_t s_tmem;
     __shared__ int s_gone[NSC];
+    __shared__ float s_cs[4];        // one-tile form: the score factors of the tile's four groups of rows
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     auto bar = [&](int i) { return smem_u32(&s_bar[i]); };
@@ -776,11 +811,19 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
         int k = 0;                            // unit of the CTA
         TileRow r;
         float cs = 0.f;
-        // this buffer's rows of the item at c: their place, and their queries for the products
+        // this buffer's rows of the item at c: their place, and their queries for the products.  The
+        // one-tile form has one tile of queries, which buffer 0's warps stage and whose factors
+        // they leave for buffer 1's.
+        const int tile_row0 = (PAIR ? b * TR : 0) + 32 * qd;
+        uint8_t *const qt = sm + L::OFF_Q + (uint32_t)(PAIR ? b : 0) * NSL * SLAB;
+        bool begun = false;                   // the next item's copies are on their way
         auto enter_item = [&]() {
             r = tile_row<RB>(a, c, (PAIR ? b * TR : 0) + row);
-            cs = stage_query<D>(a, r, row, PAIR || b == 0 ? sm + L::OFF_Q + (uint32_t)(PAIR ? b : 0) * NSL * SLAB : nullptr);
             if (PAIR || b == 0) {
+                if (!begun) begin_queries<D, RB>(a, c, tile_row0, qd, smem_u32(qt));
+                begun = false;
+                cs = end_queries<D>(a, qd, qt);
+                if (!PAIR && lane == 0) s_cs[qd] = cs;
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(B_Q + (PAIR ? b : 0)));
@@ -788,24 +831,20 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
         };
         bool mine_item = !PAIR || b < tiles_of(c);
         if (mine_item) enter_item();
-        // the next item's rows start on their way to L2 while this one is worked on
-        auto prefetch_next = [&]() {
+        // PAIR: the next item's queries, once this one's last scores are there (the tile is free)
+        auto begin_next = [&]() {
+            if (!PAIR || k + (c.nt - c.t) >= units) return;
             Cur n = c;
-            if (k + (c.nt - c.t) >= units) return;
             n.next_of_item(a);
-            const TileRow x = tile_row<RB>(a, n, (PAIR ? b * TR : 0) + row);
-            if (!x.live) return;
-            const char *p = reinterpret_cast<const char *>(static_cast<const __nv_bfloat16 *>(a.q) + (int64_t)x.qrow * a.q_stride +
-                                                           (int64_t)x.hq * D);
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p));
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p + D * 2 - 16));
+            if (b >= tiles_of(n)) return;
+            begin_queries<D, RB>(a, n, tile_row0, qd, smem_u32(qt));
+            begun = true;
         };
 #pragma unroll 1
         while (k < units && ok) {
             const int mine = min(c.nt - c.t, units - k);      // the CTA's units of this item
             const bool first = c.t == 0, last = c.t + mine == c.nt, whole = first && last;
             const int t0 = c.t;
-            prefetch_next();
             if (tid == 256) {
                 // the CTA's entry: an item that begins here and ends elsewhere (its last)
                 if (first && !last)
@@ -835,6 +874,8 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                         scales_of(kk);
                     }
                     if (!ok) break;
+                    if (j + dj >= mine) begin_next();
+                    if (!PAIR && b == 1 && j == j0) cs = u.cs = s_cs[qd];     // staged before these scores
                     if (!any_live) {      // a warp without rows: its weights are never looked at
                         if (!PAIR && b == 1 && j == j0 && items > 0 && !(ok = warp_wait(B_OFREE, items - 1))) break;
                         __syncwarp();
@@ -950,6 +991,7 @@ template <Kv8 KV, int D, bool PAIR, int GR>
 cudaError_t launch_tile_g(AttnArgs &a, void *ws, int ctas, int64_t rows, cudaStream_t s) {
     using L = tl::Lay<D, PAIR>;
     place_parts(a, ws, ctas, L::RB);
+    a.wide = ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.part_o)) & 31) == 0;
     auto kernel = kv8_tile_kernel<KV, D, PAIR, GR>;
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(kernel, L::SMEM, allowed);
