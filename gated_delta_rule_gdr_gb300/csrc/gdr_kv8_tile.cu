@@ -243,6 +243,8 @@ template <int GR> struct RowUnit {
     int see;                       // keys of the unit that the row sees
     bool part;                     // some row of the warp sees fewer than all, or a page is gone
     float cs;
+    float4 held[2];                // GR 1: the scales of the two halves
+    __device__ __forceinline__ float4 scales(int h, int i) const { return GR == 1 ? held[h] : sc[4 * h + i]; }
 };
 // A factor of at least 2^-126 keeps masked scores at -inf where a scale is zero.
 __device__ __forceinline__ float unit_factor(float cs, float ks) { return fmaxf(cs * ks, 1.2e-38f); }
@@ -325,12 +327,11 @@ __device__ __forceinline__ float half_max(const float (&v)[2][32], int h, const 
 #pragma unroll
     for (int i = 0; i < GR; ++i) {
         auto x = [&](int e) { return v[(N * i + e) >> 5][(N * i + e) & 31]; };
-        float m = fmaxf(fmaxf(x(0), x(1)), x(2));
+        float m[2] = {fmaxf(x(0), x(1)), fmaxf(x(2), x(3))};     // two chains
 #pragma unroll
-        for (int e = 3; e + 1 < N; e += 2) m = fmaxf(fmaxf(m, x(e)), x(e + 1));
-        m = fmaxf(m, x(N - 1));
-        const float4 s4 = u.sc[GR == 1 ? 4 * h : 4 * h + i];
-        mx = fmaxf(mx, fmaf(m, unit_factor(u.cs, s4.x), s4.z));
+        for (int e = 4; e < N; e += 2) m[(e / 2) & 1] = fmaxf(fmaxf(m[(e / 2) & 1], x(e)), x(e + 1));
+        const float4 s4 = u.scales(h, i);
+        mx = fmaxf(mx, fmaf(fmaxf(m[0], m[1]), unit_factor(u.cs, s4.x), s4.z));
     }
     return mx;
 }
@@ -346,7 +347,7 @@ __device__ __forceinline__ float half_weights(uint32_t ts, int h, const RowUnit<
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
             if (e % N == 0) {
-                const float4 s4 = u.sc[GR == 1 ? 4 * h : 4 * h + (32 * cb + e) / 16];
+                const float4 s4 = u.scales(h, (32 * cb + e) / 16);
                 const float kf = unit_factor(u.cs, s4.x), add = s4.z + ref;
                 kf2 = f2_pack(kf, kf), add2 = f2_pack(add, add);
                 iv = s4.w;
@@ -861,6 +862,7 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                 bool gone = false;
                 auto scales_of = [&](int kk) {     // of unit kk, whose scale slot has been waited for
                     u.sc = s_sc + (kk % NSC) * 8;
+                    if constexpr (PAIR && GR == 1) u.held[0] = u.sc[0], u.held[1] = u.sc[4];
                     gone = s_gone[kk % NSC];
                 };
 #pragma unroll 1
