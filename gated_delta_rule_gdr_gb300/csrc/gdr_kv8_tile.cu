@@ -599,7 +599,9 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                 if (k + 1 < units) look_up();
             }
             if (ok) publish();
-            if (s_abort && lane == 0)    // leave no copy in flight
+            // Leave no copy in flight.  Whoever gives up may do so after this warp's last look, so
+            // it waits on every path; all but the last few have landed long ago.
+            if (lane == 0)
                 for (int y = max(0, x - NRAW); y < x; ++y)
                     mbar_wait(bar(B_RAWFULL + y % NRAW), (uint32_t)(y / NRAW) & 1u, kCleanupLimitNs);
         } else if (warp <= (PAIR ? 2 : 1)) {
@@ -728,7 +730,7 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                     if (c.t == 0) k0 = k + 1;
                 }
             }
-            if (s_abort && issued) {   // let this warp's products land before the TMEM goes away
+            if (issued) {   // let this warp's products land before the TMEM goes away, on every path
                 if (elect_one()) {
                     mma_commit(bar(B_DRAIN + warp - 1));
                     mbar_wait(bar(B_DRAIN + warp - 1), 0u, kCleanupLimitNs);
@@ -980,6 +982,10 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
             }
             ++items;
         }
+    }
+    if (warp >= 8) {      // and a softmax warp's queries and weights, where it gave up under them
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        tmem_wait_st();
     }
     tc_fence_before();
     __syncthreads();

@@ -393,6 +393,44 @@ def test_length_beyond_the_table_is_clamped():
     assert (c == 0).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lens", [[17], [700, 33, 0, 1290], [150000, 33]])
+@pytest.mark.parametrize("rows", [8, 16, 24, 96, 320])
+def test_injected_timeout_is_reported_and_recovers(dtype, lens, rows):
+    """Every kernel of the attention with waits that give up at once (no fault, no hang): the
+    error word says so, and the next call gives the results of the one before.  A wait that
+    finds its data there is no timeout (short work, or fp32 whose products take longer than its
+    loads): then the call's results stand."""
+    x = attn_case(lens, [rows // 8] * len(lens), 16, 2, 128, 16, dtype, "e4m3", seed=rows)
+    args = [x["q"].cuda(), x["kc"].view(CODE["e4m3"]).cuda(), x["vc"].view(CODE["e4m3"]).cuda(), x["ks"].cuda(),
+            x["vs"].cuda(), x["table"].cuda(), i32(lens), x["scale"]]
+    kw = dict(cu_q=i32(x["cu"]), max_q=rows // 8, want_lse=True)
+    before = gdr.kv8_attn(*args, **kw)
+    other = torch.ones(1 << 28, dtype=torch.uint8, device="cuda")    # nothing of the cache is in the L2
+    assert gdr.last_device_error() == 0
+    with gdr.option(wait_limit_ns=0):
+        got = gdr.kv8_attn(*args, **kw)
+        error = gdr.last_device_error()
+    assert error == 5 or (error == 0 and (dtype == F32 or max(lens) < 2000))     # GDR_ERR_TIMEOUT
+    assert gdr.last_device_error() == 0 and other[-1] == 1
+    if error == 0:
+        assert all(torch.equal(u, v) for u, v in zip(got, before))
+    for u, v in zip(gdr.kv8_attn(*args, **kw), before):
+        assert torch.equal(u, v)
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+@pytest.mark.parametrize("lens,qs,Hq,Hkv,D,page", [
+    ([33, 64, 500, 1], [3, 2, 4, 1], 16, 2, 128, 16),       # 8 to 32 rows: warps with whole, part and no rows
+    ([1025, 31, 700], [9, 7, 8], 6, 2, 64, 32),             # 21 to 27 rows, tokens split by 3
+    ([90, 3000], [17, 1], 4, 4, 128, 64),                   # one query head a cached head
+    ([2000, 0, 64], [1, 1, 1], 64, 2, 64, 128),             # 32 rows of single tokens
+])
+def test_seventeen_to_thirty_two_rows(kv, lens, qs, Hq, Hkv, D, page):
+    check(attn_case(lens, qs, Hq, Hkv, D, page, BF16, kv, seed=7 + D))
+    check(attn_case(lens, qs, Hq, Hkv, D, page, BF16, kv, seed=8 + D, gone=0.3))
+
+
 @pytest.mark.slow
 def test_offsets_past_32_bits():
     """A cache of over 2^32 bytes of keys: the request's pages lie at its end."""
