@@ -526,7 +526,7 @@ gdr_status_t gdr_mla_decode(const void *q_abs, const void *ckv, const int *seqle
  * The cache.  Pages of `page` tokens (16, 32, 64 or 128).  Codes, 8 bits each:
  *   k_cache, v_cache  [num_pages][Hkv][page][D]      D = 64 or 128
  * and one fp32 scale for each page and head:
- *   k_scale, v_scale  [num_pages][Hkv]               value = code * scale
+ *   k_scale, v_scale  [num_pages][Hkv]               value = code * scale, scales positive
  *   block_table       [S][table_width] int32         the pages of request s, in order
  * num_pages * Hkv * page must be below 2^31.  k_cache, v_cache: 16-byte aligned.
  */
@@ -595,8 +595,8 @@ gdr_status_t gdr_kv8_append(const void *k, const void *v, int64_t k_stride, int6
  *   kv_len    [S] tokens cached, the new ones included (at most table_width * page)
  *   cu_q      [S+1] first query of each request, cu_q[0] = 0, cu_q[S] <= total_q; or NULL:
  *             one query a request (max_q = 1, total_q = S)
- *   max_q     the most queries any request has (it chooses the kernel, the result does not
- *             depend on it)
+ *   max_q     the most queries any request has, or more: it chooses the kernel, and a larger
+ *             one changes a result by rounding only.  Below that the result is undefined
  *   scale     score scale, for example 1 / sqrt(D)
  *   out       [total_q][Hq][D] dtype;  lse [total_q][Hq] fp32 or NULL
  * Query i of a request with n queries and kv tokens sees keys j <= kv - n + i whose page is
@@ -607,7 +607,9 @@ gdr_status_t gdr_kv8_append(const void *k, const void *v, int64_t k_stride, int6
  * codes of cached tokens must not be NaN (gdr_kv8_append writes none); value scales are
  * taken within [2^-40, 2^40].
  * Sums, maxima and the output accumulate in fp32; the weights meet the value codes in
- * products of 11-bit operands (22-bit for fp32 q), the codes and bf16 q enter exactly.
+ * products of 11-bit operands (22-bit for fp32 q); the codes enter exactly, and bf16 q down
+ * to 2^-29 of the largest magnitude in its row (of the 32 rows around it where a request has
+ * more than 32 rows of a cached head), less than a softmax can show.
  *   workspace  16-byte aligned, gdr_kv8_attn_workspace_size bytes (0: may be NULL):
  *             partial results of requests whose cache is split; scratch on entry and exit
  */
