@@ -609,7 +609,7 @@ cudaError_t launch_split_r(AttnArgs &a, const void *kc, const void *vc, void *ws
     if (e != cudaSuccess) return e;
     if ((e = launch_after(kernel, dim3((unsigned)ctas), 32 * sp::NW<RG>, sp::SMEM<R, RG, D>, s, mk, mv, a)) != cudaSuccess)
         return e;
-    return launch_merge<E, D, RB, RG == 1 ? 8 : 2>(a, ctas, rows > RB ? RB : (int)rows, s);
+    return launch_merge<E, D, RB>(a, rows, s);
 }
 
 // The item's shape by the most rows of a cached head that a request has.

@@ -18,6 +18,7 @@
 #include "gdr_fused_common.cuh"
 #include "gdr_kv8.cuh"
 
+#include <algorithm>
 #include <atomic>
 
 namespace gdr {
@@ -27,6 +28,9 @@ namespace kv8 {
 constexpr float kOff = 7.f;     // weights are 2^(x - M + kOff): room below 1 before a half loses bits
 constexpr float kTau = 8.f;     // M moves only when a score exceeds it by more than this
 constexpr float kVsMin = 9.094947017729282e-13f, kVsMax = 1.099511627776e12f;   // 2^-40, 2^40
+// Rows that the merge takes with eight warps each: what is resident at once.  Beyond, the waves
+// cost more than the shorter walks give (256 requests of 8 rows: 0.191 ms against 0.180).
+constexpr int kMergeWide = 1216;
 }  // namespace kv8
 
 struct AttnArgs {
@@ -43,6 +47,7 @@ struct AttnArgs {
     float *part_ml;              // [CTA][2][RB][2]: reference exponent M, weight sum
     int4 *entry;                 // [CTA] {last CTA (-1: no divided item), request, head, block}
     int S, total_q, Hq, Hkv, G, W, page_log2, N;
+    int ctas;                    // of the attention kernel
     bool wide;                   // out and part_o are 32-byte aligned
     uint64_t limit_ns;
 };
@@ -254,72 +259,143 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
 }
 
 // ------------------------------------------------------------------ merge of divided items
-// WPR warps take one row, the parts in turn (few rows, many parts), or one warp takes RPW rows
-// one after another (many rows, few parts: fewer CTAs, each of which first waits for its
-// entry); lanes the D values.
+// A CTA takes rows of the blockIdx.x-th divided item.  WPR warps take one row, a run of its parts
+// each (few rows, many parts: one request of 5 x 8 rows on 4000 keys, 32 parts an item, 57 -> 17
+// us for the whole call against a warp that walks the parts of row after row), or one warp takes
+// RPW rows at once (many rows, few parts).  A lane weighs a part, then the lanes take the D
+// values: eight loads are in flight at once, since each is a trip to the L2.
 template <typename E, int D, int RB, int WPR, int RPW>
-__global__ void __launch_bounds__(256) kv8_merge_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(256, 4) kv8_merge_kernel(const AttnArgs a) {
     static_assert(WPR == 1 || RPW == 1, "");
     constexpr int VL = D / 32;
     __shared__ float s_o[WPR > 1 ? 8 : 1][D];
     __shared__ float s_l[8];
+    __shared__ uint32_t s_mask[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w0 = warp / WPR * WPR;
     grid_dependency_wait();
     grid_launch_dependents();
-    const int c0 = blockIdx.x;
+    // the item: of the CTA whose entry is the blockIdx.x-th that has one, 1024 entries at a time;
+    // with a CTA for every entry, its own
+    int c0 = gridDim.x == a.ctas ? (int)blockIdx.x : -1;
+    for (int base = 0, before = 0; base < a.ctas && c0 < 0; base += 1024) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = base + 256 * i + threadIdx.x;
+            const unsigned m = __ballot_sync(0xffffffffu, c < a.ctas && a.entry[min(c, a.ctas - 1)].x >= 0);
+            if (lane == 0) s_mask[8 * i + warp] = m;
+        }
+        __syncthreads();
+        int incl = __popc(s_mask[lane]);
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += y;
+        }
+        incl += before;
+        const unsigned past = __ballot_sync(0xffffffffu, incl > (int)blockIdx.x);
+        if (past) {
+            const int g = __ffs(past) - 1;
+            const unsigned m = s_mask[g];
+            const int k = (int)blockIdx.x - (__shfl_sync(0xffffffffu, incl, g) - __popc(m));
+            c0 = base + 32 * g + (int)__fns(m, 0, k + 1);
+        }
+        before = __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (c0 < 0) return;
     const int4 en = a.entry[c0];
     if (en.x < 0) return;
     const Request r = request_of(a, en.y);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w0 = warp / WPR * WPR;
-    const int row0 = (blockIdx.y * (8 / WPR) + warp / WPR) * RPW, parts = en.x - c0 + 1;
+    const int rows = min(RB, r.n * a.G - en.w * RB), parts = en.x - c0 + 1;
+    const int row0 = (blockIdx.y * (8 / WPR) + warp / WPR) * RPW;
+    if (row0 >= rows) return;        // (with WPR > 1 the whole CTA)
+    // row rr of part p; a row that is not there is read as the last one and not written
+    auto slot = [&](int p, int rr) { return ((int64_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * RB + min(row0 + rr, rows - 1); };
+    float ref[RPW], l[RPW], o[RPW][VL];
+    float2 ml[RPW];
+#pragma unroll
+    for (int rr = 0; rr < RPW; ++rr) {
+        ref[rr] = -INFINITY;
+        l[rr] = 0.f;
+#pragma unroll
+        for (int e = 0; e < VL; ++e) o[rr][e] = 0.f;
+    }
+    for (int p = lane; p - lane < parts; p += 32)
+#pragma unroll
+        for (int rr = 0; rr < RPW; ++rr) {
+            const float2 x = p < parts ? *reinterpret_cast<const float2 *>(a.part_ml + 2 * slot(p, rr)) : make_float2(-INFINITY, 0.f);
+            ref[rr] = fmaxf(ref[rr], x.x);
+            if (p == lane) ml[rr] = x;
+        }
+    float M[RPW];
+#pragma unroll
+    for (int rr = 0; rr < RPW; ++rr) {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) ref[rr] = fmaxf(ref[rr], __shfl_xor_sync(0xffffffffu, ref[rr], off));
+        M[rr] = ref[rr] == -INFINITY ? 0.f : ref[rr];
+    }
+    const int per = (parts + WPR - 1) / WPR, end = min(parts, (warp - w0 + 1) * per);
+    for (int p0 = (warp - w0) * per; p0 < end; p0 += 32) {
+        const int n = min(32, end - p0);
+        float w[RPW];
+#pragma unroll
+        for (int rr = 0; rr < RPW; ++rr) {
+            if (p0 > 0) ml[rr] = *reinterpret_cast<const float2 *>(a.part_ml + 2 * slot(min(p0 + lane, parts - 1), rr));
+            // a part without an exponent weighs 0; if its sums are NaN (all its scores are) they stay NaN
+            w[rr] = part_weight(ml[rr].x, M[rr]);
+            if (lane < n) l[rr] = fmaf(w[rr], ml[rr].y, l[rr]);
+        }
+#pragma unroll(8 / RPW)
+        for (int j = 0; j < n; ++j)
+#pragma unroll
+            for (int rr = 0; rr < RPW; ++rr) {
+                const float wj = __shfl_sync(0xffffffffu, w[rr], j);
+                const float *src = a.part_o + slot(p0 + j, rr) * D + lane * VL;
+                if constexpr (VL == 4) {
+                    const float4 x = *reinterpret_cast<const float4 *>(src);
+                    o[rr][0] = fmaf(wj, x.x, o[rr][0]), o[rr][1] = fmaf(wj, x.y, o[rr][1]);
+                    o[rr][VL - 2] = fmaf(wj, x.z, o[rr][VL - 2]), o[rr][VL - 1] = fmaf(wj, x.w, o[rr][VL - 1]);
+                } else {
+                    const float2 x = *reinterpret_cast<const float2 *>(src);
+                    o[rr][0] = fmaf(wj, x.x, o[rr][0]), o[rr][1] = fmaf(wj, x.y, o[rr][1]);
+                }
+            }
+    }
+#pragma unroll
+    for (int rr = 0; rr < RPW; ++rr)
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], off);
+    if constexpr (WPR > 1) {
+        if (lane == 0) s_l[warp] = l[0];
+#pragma unroll
+        for (int e = 0; e < VL; ++e) s_o[warp][lane * VL + e] = o[0][e];
+        __syncthreads();
+        if (warp != w0) return;
+        l[0] = 0.f;
+#pragma unroll
+        for (int w = 0; w < WPR; ++w) l[0] += s_l[w0 + w];
+#pragma unroll
+        for (int e = 0; e < VL; ++e) {
+            o[0][e] = 0.f;
+#pragma unroll
+            for (int w = 0; w < WPR; ++w) o[0][e] += s_o[w0 + w][lane * VL + e];
+        }
+    }
 #pragma unroll
     for (int rr = 0; rr < RPW; ++rr) {
         const int row = row0 + rr, at = en.w * RB + row;
-        const bool live = row < RB && at < r.n * a.G;
-        auto slot = [&](int p) { return ((int64_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * RB + row; };
-        float M = -INFINITY;
-        for (int p = lane; p < parts && live; p += 32) M = fmaxf(M, a.part_ml[2 * slot(p)]);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-        const float ref = M == -INFINITY ? 0.f : M;
-        float o[VL] = {}, l = 0.f;
-#pragma unroll 4
-        for (int p = warp - w0; p < parts && live; p += WPR) {
-            const int64_t k = slot(p);
-            const float2 ml = *reinterpret_cast<const float2 *>(a.part_ml + 2 * k);
-            // a part without an exponent weighs 0; if its sums are NaN (all its scores are) they stay NaN
-            const float w = part_weight(ml.x, ref);
-            l = fmaf(w, ml.y, l);
-            const float *src = a.part_o + k * D + lane * VL;
-#pragma unroll
-            for (int e = 0; e < VL; ++e) o[e] = fmaf(w, src[e], o[e]);
-        }
-        if constexpr (WPR > 1) {
-            if (lane == 0) s_l[warp] = l;
-#pragma unroll
-            for (int e = 0; e < VL; ++e) s_o[warp][lane * VL + e] = o[e];
-            __syncthreads();
-            if (warp != w0) return;
-            l = 0.f;
-#pragma unroll
-            for (int w = 0; w < WPR; ++w) l += s_l[w0 + w];
-#pragma unroll
-            for (int e = 0; e < VL; ++e) {
-                o[e] = 0.f;
-#pragma unroll
-                for (int w = 0; w < WPR; ++w) o[e] += s_o[w0 + w][lane * VL + e];
-            }
-        }
-        if (!live) continue;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        if (row >= rows) break;
+        const float inv = l[rr] == 0.f ? 0.f : 1.f / l[rr];
         const int64_t orow = (int64_t)(r.q0 + at / a.G) * a.Hq + en.z * a.G + at % a.G;
 #pragma unroll
         for (int e = 0; e < VL; ++e) {
             if constexpr (sizeof(E) == 4)
-                static_cast<float *>(a.out)[orow * D + lane * VL + e] = o[e] * inv;
+                static_cast<float *>(a.out)[orow * D + lane * VL + e] = o[rr][e] * inv;
             else
-                static_cast<__nv_bfloat16 *>(a.out)[orow * D + lane * VL + e] = __float2bfloat16_rn(o[e] * inv);
+                static_cast<__nv_bfloat16 *>(a.out)[orow * D + lane * VL + e] = __float2bfloat16_rn(o[rr][e] * inv);
         }
-        if (a.lse && lane == 0) a.lse[orow] = l == 0.f ? -INFINITY : (ref - kv8::kOff + log2f(l)) * 0.693147180559945f;
+        if (a.lse && lane == 0)
+            a.lse[orow] = l[rr] == 0.f ? -INFINITY : (M[rr] - kv8::kOff + log2f(l[rr])) * 0.693147180559945f;
     }
 }
 
@@ -339,10 +415,18 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t sm
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
-template <typename E, int D, int RB, int WPR>
-cudaError_t launch_merge(const AttnArgs &a, int ctas, int rows, cudaStream_t s) {
-    constexpr int RPW = WPR == 1 ? 4 : 1, RPC = 8 / WPR * RPW;
-    return launch_after(kv8_merge_kernel<E, D, RB, WPR, RPW>, dim3((unsigned)ctas, (unsigned)(((rows < RB ? rows : RB) + RPC - 1) / RPC)),
+// CTAs for as many items as can be divided among the attention's `a.ctas` (each at most one, and
+// there are no more than the requests' blocks of rows), or for every entry where that is not
+// much more: looking for the item takes 1.5 us.
+template <typename E, int D, int RB>
+cudaError_t launch_merge(const AttnArgs &a, int64_t rows, cudaStream_t s) {
+    constexpr int RPW = RB >= 16 ? 2 : 1;
+    const int64_t most = std::min(rows, (int64_t)RB);
+    const int64_t blocks = std::min((int64_t)a.S * ((rows + RB - 1) / RB), (int64_t)a.total_q * a.G / RB + a.S);
+    const int64_t items = 2 * blocks * a.Hkv < a.ctas ? blocks * a.Hkv : a.ctas;
+    if (items * most <= kv8::kMergeWide)
+        return launch_after(kv8_merge_kernel<E, D, RB, 8, 1>, dim3((unsigned)items, (unsigned)most), 256, 0, s, a);
+    return launch_after(kv8_merge_kernel<E, D, RB, 1, RPW>, dim3((unsigned)items, (unsigned)((most + 8 * RPW - 1) / (8 * RPW))),
                         256, 0, s, a);
 }
 
@@ -351,6 +435,7 @@ size_t part_bytes(int ctas, int RB, int D) {
     return (size_t)ctas * (sizeof(int4) + (size_t)2 * RB * (2 + D) * sizeof(float));
 }
 void place_parts(AttnArgs &a, void *ws, int ctas, int RB) {
+    a.ctas = ctas;
     a.entry = static_cast<int4 *>(ws);
     a.part_ml = reinterpret_cast<float *>(a.entry + ctas);
     a.part_o = a.part_ml + (size_t)ctas * 2 * RB * 2;

@@ -1005,7 +1005,7 @@ cudaError_t launch_tile_g(AttnArgs &a, void *ws, int ctas, int64_t rows, cudaStr
     cudaError_t e = allow_smem(kernel, L::SMEM, allowed);
     if (e != cudaSuccess) return e;
     if ((e = launch_after(kernel, dim3((unsigned)ctas), tl::NT, L::SMEM, s, a)) != cudaSuccess) return e;
-    return launch_merge<__nv_bfloat16, D, L::RB, 1>(a, ctas, (int)(rows < L::RB ? rows : L::RB), s);
+    return launch_merge<__nv_bfloat16, D, L::RB>(a, rows, s);
 }
 template <Kv8 KV, int D, bool PAIR>
 cudaError_t launch_tile_f(AttnArgs &a, void *ws, int ctas, int64_t rows, cudaStream_t s) {
