@@ -36,20 +36,18 @@ namespace {
 
 namespace sp {
 constexpr int SLAB = 32;               // tokens a warp takes at a time
-// An item is RG groups of R blocks of 8 rows.  RG 1: four warps take the slabs of a unit in
-// turn, each with a ring of its own, and join their sums at the item's end.  RG 2: one warp a
-// group of rows, both on the same slabs of one ring (the first fills it), nothing to join.
-template <int RG> constexpr int NW = RG == 1 ? 4 : RG;         // warps a CTA
-template <int RG> constexpr int UT = RG == 1 ? 4 * SLAB : SLAB;   // tokens of a unit
-template <int RG> constexpr int RINGS = RG == 1 ? 4 : 1;
+// An item is R blocks of 8 rows.  Four warps take the slabs of a unit in turn, each with a ring of
+// its own, and join their sums at the item's end.
+constexpr int NW = 4;                  // warps a CTA
+constexpr int UT = NW * SLAB;          // tokens of a unit
 // Slabs of a ring and CTAs an SM (two blocks' fragments need the registers of 8 warps an SM).
-template <int R, int RG> constexpr int ST = RG > 1 ? 3 * RG : R == 2 ? 3 : 2;
-template <int R, int RG> constexpr int CPS = RG > 1 ? 8 / RG : R == 2 ? 2 : 3;
+template <int R> constexpr int ST = R == 2 ? 3 : 2;
+template <int R> constexpr int CPS = R == 2 ? 2 : 3;
 template <int D> constexpr uint32_t SLAB_BYTES = SLAB * D;
 template <int D> constexpr uint32_t STAGE = 2 * SLAB_BYTES<D>;     // keys, then values
-template <int R, int RG, int D> constexpr uint32_t OFF_RED = RINGS<RG> * ST<R, RG> * STAGE<D>;   // RG 1: [4 warps][4 rows][D]
-template <int R, int RG, int D> constexpr uint32_t OFF_SCAL = OFF_RED<R, RG, D> + (RG == 1 ? 4 * 4 * D * 4 : 0);
-template <int R, int RG, int D> constexpr uint32_t SMEM = OFF_SCAL<R, RG, D> + RINGS<RG> * ST<R, RG> * 4 * 4;   // [ring][ST][2 groups][2]
+template <int R, int D> constexpr uint32_t OFF_RED = NW * ST<R> * STAGE<D>;   // [4 warps][4 rows][D]
+template <int R, int D> constexpr uint32_t OFF_SCAL = OFF_RED<R, D> + 4 * 4 * D * 4;
+template <int R, int D> constexpr uint32_t SMEM = OFF_SCAL<R, D> + NW * ST<R> * 4 * 4;   // [ring][ST][2 groups][2]
 }  // namespace sp
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -83,35 +81,29 @@ __device__ __forceinline__ uint32_t slab_offset(uint32_t t, uint32_t c) {
     return row * 128u + ((ch ^ (row & 7u)) << 4);
 }
 
-template <typename E, Kv8 KV, int D, int R, int RG>
-__global__ void __launch_bounds__((32 * sp::NW<RG>), (sp::CPS<R, RG>))
+template <typename E, Kv8 KV, int D, int R>
+__global__ void __launch_bounds__(32 * sp::NW, sp::CPS<R>)
 kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                  const AttnArgs a) {
-    using sp::SLAB, sp::SLAB_BYTES, sp::STAGE;
-    constexpr int ST = sp::ST<R, RG>, NW = sp::NW<RG>, UT = sp::UT<RG>, RB = 8 * R * RG, WR = 8 * R;
+    using sp::SLAB, sp::SLAB_BYTES, sp::STAGE, sp::NW, sp::UT;
+    constexpr int ST = sp::ST<R>, RB = 8 * R;
     constexpr bool HL = sizeof(E) == 4;          // two halves for queries and weights
     constexpr int NKS = D / 16, NVT = D / 16;    // k steps of K q^T, row tiles of O^T
     constexpr int LD = D / 4, LO = D / 8;        // values of a query, of an output row that a lane holds
     extern __shared__ __align__(1024) uint8_t sm[];
-    __shared__ __align__(8) uint64_t s_bar[(RG == 1 ? NW : 2) * ST];
+    __shared__ __align__(8) uint64_t s_bar[NW * ST];
     __shared__ Place s_place;
     __shared__ int64_t s_scan[NW];
-    __shared__ float s_stat[2][NW][WR];          // M, l of each warp at an item's end
+    __shared__ float s_stat[2][NW][RB];          // M, l of each warp at an item's end
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
-    const int ring = RG == 1 ? warp : 0, rg = RG == 1 ? 0 : warp;     // this warp's ring, and group of rows
-    const bool loads = RG == 1 || warp == 0;
-    float *s_red = reinterpret_cast<float *>(sm + sp::OFF_RED<R, RG, D>);
-    float *s_scal = reinterpret_cast<float *>(sm + sp::OFF_SCAL<R, RG, D>) + ring * ST * 4;
-    const uint32_t stage0 = smem_u32(sm) + (uint32_t)ring * ST * STAGE<D>;
-    auto bar = [&](int i) { return smem_u32(&s_bar[ring * ST + i]); };
-    auto empty = [&](int i) { return smem_u32(&s_bar[ST + i]); };       // RG > 1: every warp is done with the slab
+    float *s_red = reinterpret_cast<float *>(sm + sp::OFF_RED<R, D>);
+    float *s_scal = reinterpret_cast<float *>(sm + sp::OFF_SCAL<R, D>) + warp * ST * 4;
+    const uint32_t stage0 = smem_u32(sm) + (uint32_t)warp * ST * STAGE<D>;
+    auto bar = [&](int i) { return smem_u32(&s_bar[warp * ST + i]); };
 
-    if (loads && lane == 0) {
-        // a slab's copies, and (where others read them) its scales
-        for (int i = 0; i < ST; ++i) mbar_init(bar(i), RG == 1 ? 1 : 2);
-        if constexpr (RG > 1)
-            for (int i = 0; i < ST; ++i) mbar_init(empty(i), RG);
+    if (lane == 0) {
+        for (int i = 0; i < ST; ++i) mbar_init(bar(i), 1);
         fence_mbar_init();
         if (warp == 0) s_abort = 0;
     }
@@ -142,7 +134,7 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     auto look_up = [&]() {
         page = -1;
         if (lane < 2 && left > 0) {
-            const int tok = ld.t * UT + ring * SLAB + 16 * lane;
+            const int tok = ld.t * UT + warp * SLAB + 16 * lane;
             if (tok < ld.r.kv) page = a.table[(int64_t)ld.s * a.W + (tok >> a.page_log2)];
             page_h = ld.h;
         }
@@ -154,28 +146,18 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             s_scal[pend * 4 + lane * 2 + 1] = pend_v;
         }
         __syncwarp();
-        if (RG > 1 && lane == 0) mbar_arrive(bar(pend));
         pend = -1;
     };
-    int filled = 0;
-    auto issue = [&]() -> bool {
+    auto issue = [&]() {
         flush();
-        if (left == 0) return true;
-        if constexpr (RG > 1)
-            if (filled >= ST) {
-                const uint32_t ph = (uint32_t)(filled / ST - 1) & 1u;
-                bool free = mbar_test_wait(empty(fill), ph);
-                if (!free) free = role_wait_slow(empty(fill), ph, a.limit_ns, &s_abort, false);
-                if (!__all_sync(0xffffffffu, free)) return false;
-            }
-        ++filled;
+        if (left == 0) return;
         const bool there = lane < 2 && page >= 0 && page < a.N;
         const unsigned m = __ballot_sync(0xffffffffu, there);
         if (lane == 0) mbar_arrive_expect_tx(bar(fill), (uint32_t)__popc(m) * 32u * D);
         __syncwarp();
         pend_k = 0.f, pend_v = -1.f;     // a page that is gone
         if (there) {
-            const int tok = ld.t * UT + ring * SLAB + 16 * lane;
+            const int tok = ld.t * UT + warp * SLAB + 16 * lane;
             const int64_t ph = (int64_t)page * a.Hkv + page_h;
             const int row = (int)((ph << a.page_log2) + (tok & (P - 1)));
             const uint32_t dst = stage0 + (uint32_t)fill * STAGE<D> + (uint32_t)lane * 16 * D;
@@ -189,16 +171,12 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         --left;
         ld.next_unit(a);
         look_up();
-        return true;
     };
     bool ok = true;
-    if (loads) {
-        look_up();
-        // with several readers a slab is refilled one later, when they are likely done with it
+    look_up();
 #pragma unroll 1
-        for (int i = 0; i < (RG == 1 ? ST : ST - 1); ++i) ok = issue() && ok;
-        __syncwarp();
-    }
+    for (int i = 0; i < ST; ++i) issue();
+    __syncwarp();
 
     // ---- the items
     Cur c;
@@ -209,7 +187,7 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
 #pragma unroll 1
     for (int done = 0; done < units;) {
         const int t_first = c.t, t_last = min(c.nt, t_first + units - done);   // this CTA's units of the item
-        const int rows = min(WR, c.r.n * a.G - c.b * RB - WR * rg), row0 = c.b * RB + WR * rg;   // of this warp (may be none)
+        const int row0 = c.b * RB, rows = min(RB, c.r.n * a.G - row0);
         // query fragments: row 8 n + g, values LD t4 .. LD t4 + LD - 1, word j of a key holding
         // values 4 j .. 4 j + 3 of them
         uint32_t qf[HL ? 2 : 1][R][NKS][2];
@@ -275,8 +253,8 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 waited += ok;
             }
             const uint32_t kb = stage0 + (uint32_t)stage * STAGE<D>, vb = kb + SLAB_BYTES<D>;
-            const int tok0 = t * UT + ring * SLAB;
-            if (ok && tok0 < c.end && (RG == 1 || rows > 0)) {
+            const int tok0 = t * UT + warp * SLAB;
+            if (ok && tok0 < c.end) {
                 float ksc[2], vsc[2];      // of the slab's two groups of 16 tokens
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -436,9 +414,7 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                 }
             }
             __syncwarp();
-            if constexpr (RG > 1)
-                if (lane == 0) mbar_arrive(empty(stage));
-            if (ok && loads) ok = issue();
+            if (ok) issue();
             if (++stage == ST) stage = 0, phase ^= 1;
         }
 
@@ -449,7 +425,7 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             for (int e = 0; e < 2; ++e) {
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], off);
-                if (RG == 1 && g == 0) {
+                if (g == 0) {
                     s_stat[0][warp][8 * n + 2 * t4 + e] = M[n][e];
                     s_stat[1][warp][8 * n + 2 * t4 + e] = l[n][e];
                 }
@@ -462,38 +438,6 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         const int64_t slot = ((int64_t)blockIdx.x * 2 + (first ? 1 : 0)) * RB;
         if (first && !last)
             entry = make_int4(cta_of(u0 + done + c.nt - 1, total, s_place.ctas), c.s, c.h, c.b);
-        if constexpr (RG > 1) {
-            // the warp has its rows' sums whole: a lane's LO values of rows 2 t4, 2 t4 + 1
-#pragma unroll
-            for (int n = 0; n < R; ++n)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int lr = 8 * n + 2 * t4 + e;
-                    if (lr >= rows) continue;
-                    float y[LO];
-#pragma unroll
-                    for (int j = 0; j < NVT; ++j) y[2 * j] = o[n][j][e], y[2 * j + 1] = o[n][j][2 + e];
-                    if (first && last) {
-                        const int at = row0 + lr, i = at / a.G;
-                        const int64_t row = (int64_t)(c.r.q0 + i) * a.Hq + c.h * a.G + (at - i * a.G);
-                        const float inv = l[n][e] == 0.f ? 0.f : 1.f / l[n][e];
-                        E *dst = static_cast<E *>(a.out) + row * D + LO * g;
-#pragma unroll
-                        for (int v = 0; v < LO; ++v) y[v] *= inv;
-#pragma unroll
-                        for (int v = 0; v < LO; v += Vec16<E>::N) Vec16<E>::store(dst + v, y + v);
-                        if (a.lse && g == 0)
-                            a.lse[row] = l[n][e] == 0.f ? -INFINITY
-                                                        : ((M[n][e] == -INFINITY ? 0.f : M[n][e]) - kv8::kOff + log2f(l[n][e])) *
-                                                              0.693147180559945f;
-                    } else {
-                        const int64_t row = slot + WR * rg + lr;
-#pragma unroll
-                        for (int v = 0; v < LO; v += 4) Vec16<float>::store(a.part_o + row * D + LO * g + v, y + v);
-                        if (g == 0) *reinterpret_cast<float2 *>(a.part_ml + 2 * row) = make_float2(M[n][e], l[n][e]);
-                    }
-                }
-        } else {
 #pragma unroll
         for (int pass = 0; pass < 2 * R; ++pass) {       // rows 4 pass .. 4 pass + 3
             if (4 * pass >= rows) break;
@@ -568,14 +512,12 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             }
             __syncthreads();
         }
-        }
         done += t_last - t_first;
         c.next_of_item(a);
     }
     if (!ok) {   // leave no copy in flight
         entry.x = -1;
-        if (loads) flush();
-        const int issued = loads ? units - left : 0;
+        const int issued = units - left;
         for (int k = waited; k < issued; ++k) mbar_wait(bar(k % ST), (uint32_t)(k / ST) & 1u, kCleanupLimitNs);
     }
     if (tid == 0) a.entry[blockIdx.x] = entry;
@@ -595,42 +537,38 @@ bool make_cache_map(CUtensorMap *m, const void *ptr, int64_t tokens, int D) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename E, Kv8 KV, int D, int R, int RG>
+template <typename E, Kv8 KV, int D, int R>
 cudaError_t launch_split_r(AttnArgs &a, const void *kc, const void *vc, void *ws, int64_t rows, cudaStream_t s) {
-    constexpr int RB = 8 * R * RG;
-    const int ctas = sp::CPS<R, RG> * sm_count();
+    constexpr int RB = 8 * R;
+    const int ctas = sp::CPS<R> * sm_count();
     place_parts(a, ws, ctas, RB);
     CUtensorMap mk, mv;
     const int64_t tokens = ((int64_t)a.N * a.Hkv) << a.page_log2;
     if (!make_cache_map(&mk, kc, tokens, D) || !make_cache_map(&mv, vc, tokens, D)) return cudaErrorInvalidValue;
-    auto kernel = kv8_split_kernel<E, KV, D, R, RG>;
+    auto kernel = kv8_split_kernel<E, KV, D, R>;
     static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_smem(kernel, sp::SMEM<R, RG, D>, allowed);
+    cudaError_t e = allow_smem(kernel, sp::SMEM<R, D>, allowed);
     if (e != cudaSuccess) return e;
-    if ((e = launch_after(kernel, dim3((unsigned)ctas), 32 * sp::NW<RG>, sp::SMEM<R, RG, D>, s, mk, mv, a)) != cudaSuccess)
+    if ((e = launch_after(kernel, dim3((unsigned)ctas), 32 * sp::NW, sp::SMEM<R, D>, s, mk, mv, a)) != cudaSuccess)
         return e;
     return launch_merge<E, D, RB>(a, rows, s);
 }
 
 // The item's shape by the most rows of a cached head that a request has.
-enum class Shape { R8, R16, R32, TILE };
+enum class Shape { R8, R16, TILE };
 Shape shape_of(int max_q, int G, Elem e) {
     const int64_t rows = (int64_t)max_q * G;
     if (rows <= 8) return Shape::R8;
-    // fp32 (the accuracy path) stays at 16 rows: its fragments are twice as large
-    if (rows <= 16 || e == Elem::F32) return Shape::R16;
-    // bf16 rows beyond 16: two warps on a slab up to 32 (32 requests of 3 drafted tokens x 8
-    // heads, 16 k keys each: 0.242 ms against the tile kernel's 0.277), the tile kernel beyond
-    // (5 drafted tokens: 0.277 ms against 0.457 with four warps on a slab)
-    return rows <= 32 ? Shape::R32 : Shape::TILE;
+    // fp32 (the accuracy path) stays at 16 rows: its fragments are twice as large.  bf16 up to 16
+    // rows: 32 requests on 16 k keys 0.145 ms here, 0.182 in the tile kernel; beyond, 32 rows in
+    // warps of their own on shared slabs took 0.243 ms against the tile kernel's 0.182 (on 300
+    // keys 0.022 against 0.034: an item's ends cost the tile kernel more)
+    return rows <= 16 || e == Elem::F32 ? Shape::R16 : Shape::TILE;
 }
 template <typename E, Kv8 KV, int D>
 cudaError_t launch_split(AttnArgs &a, Shape sh, const void *kc, const void *vc, void *ws, int64_t rows, cudaStream_t s) {
-    if (sh == Shape::R8) return launch_split_r<E, KV, D, 1, 1>(a, kc, vc, ws, rows, s);
-    if constexpr (sizeof(E) == 2) {
-        if (sh == Shape::R32) return launch_split_r<E, KV, D, 2, 2>(a, kc, vc, ws, rows, s);
-    }
-    return launch_split_r<E, KV, D, 2, 1>(a, kc, vc, ws, rows, s);
+    return sh == Shape::R8 ? launch_split_r<E, KV, D, 1>(a, kc, vc, ws, rows, s)
+                           : launch_split_r<E, KV, D, 2>(a, kc, vc, ws, rows, s);
 }
 
 }  // namespace
@@ -638,9 +576,8 @@ cudaError_t launch_split(AttnArgs &a, Shape sh, const void *kc, const void *vc, 
 size_t kv8_attn_workspace_bytes(int, int max_q, int, int Hq, int Hkv, int D, Elem e) {
     const int sms = sm_count();
     switch (shape_of(max_q, Hq / Hkv, e)) {
-        case Shape::R8: return part_bytes(sp::CPS<1, 1> * sms, 8, D);
-        case Shape::R16: return part_bytes(sp::CPS<2, 1> * sms, 16, D);
-        case Shape::R32: return part_bytes(sp::CPS<2, 2> * sms, 32, D);
+        case Shape::R8: return part_bytes(sp::CPS<1> * sms, 8, D);
+        case Shape::R16: return part_bytes(sp::CPS<2> * sms, 16, D);
         case Shape::TILE: break;
     }
     return part_bytes(sms, kKv8TileRows, D);

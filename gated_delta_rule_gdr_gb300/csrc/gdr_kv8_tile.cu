@@ -19,7 +19,7 @@
 // rows, where the cache's bytes bound): one tile of rows, whose units alternate between the
 // two score and output buffers; the two halves of the sum are joined at the item's end.
 //
-// Warps: 0 loads (page entries and scales looked up one unit ahead), 1 and 2 issue the products
+// Warps: 0 and 3 load (keys; values and scales), 1 and 2 issue the products
 // (1 owns the TMEM), 4-7 widen (two the keys, two the values), 8-11 and 12-15 the softmax of buffer 0 and 1, a thread a row:
 // maxima and sums never leave the thread.  No barrier spans the CTA inside the loop; every
 // wait is bounded.
@@ -42,14 +42,16 @@ enum : int {
     B_RAWFULL = 0, B_RAWFREE = B_RAWFULL + NRAW, B_CVFULL = B_RAWFREE + NRAW, B_CVFREE = B_CVFULL + MAXCV,
     B_SC = B_CVFREE + MAXCV, B_Q = B_SC + NSC, B_S = B_Q + 2, B_PU = B_S + 2, B_P = B_PU + 2, B_O = B_P + 2,
     B_ML = B_O + 2, B_OFREE = B_ML + 1, B_DRAIN = B_OFREE + 1, B_U = B_DRAIN + 2,
-    NUM_BARS = B_U + 2
+    B_X = B_U + 2, NUM_BARS = B_X + 1
 };
-template <int D, bool PAIR> struct Lay {
-    static constexpr int RB = PAIR ? kKv8TileRows : TR;   // rows of an item
+template <int D, bool PAIR, int NC> struct Lay {
+    static constexpr int RB = PAIR ? kKv8TileRows : TR / NC;   // rows of an item
+    static constexpr uint32_t XR = (TR - TR / NC) * 128;  // sums of the copies that are joined, 32 columns (NC > 1)
     static constexpr int NCV = PAIR ? 3 : 4;              // widened slots
     static constexpr uint32_t RAW = UT * D, CV = UT * D * 2;
     static constexpr uint32_t OFF_Q = 0;                  // one tile, or two
-    static constexpr uint32_t OFF_CV = (PAIR ? 2 : 1) * TR * D * 2;
+    static constexpr uint32_t QT = (PAIR ? 2 : 1) * TR * D * 2;
+    static constexpr uint32_t OFF_CV = QT > 2 * XR ? QT : 2 * XR;
     static constexpr uint32_t OFF_RAW = OFF_CV + NCV * CV;
     static constexpr uint32_t OFF_SC = OFF_RAW + NRAW * RAW;     // [NSC][8 groups]{ks, vs, log2 vs, 1/vs}
     static constexpr uint32_t OFF_ML = OFF_SC + NSC * 8 * 16;    // [TR]{M, l} of buffer 1 (not PAIR)
@@ -243,8 +245,8 @@ template <int GR> struct RowUnit {
     int see;                       // keys of the unit that the row sees
     bool part;                     // some row of the warp sees fewer than all, or a page is gone
     float cs;
-    float4 held[2];                // GR 1: the scales of the two halves
-    __device__ __forceinline__ float4 scales(int h, int i) const { return GR == 1 ? held[h] : sc[4 * h + i]; }
+    float4 held[2];                // GR 1: the scales of the two halves (PAIR; NC 2: of the warp's, twice)
+    __device__ __forceinline__ float4 scales(int h, int i) const { return GR == 1 ? (h ? held[1] : held[0]) : sc[4 * h + i]; }
 };
 // A factor of at least 2^-126 keeps masked scores at -inf where a scale is zero.
 __device__ __forceinline__ float unit_factor(float cs, float ks) { return fmaxf(cs * ks, 1.2e-38f); }
@@ -263,10 +265,8 @@ __device__ __forceinline__ void load_chunk(uint32_t ts, int ch, const RowUnit<GR
     }
 }
 template <int GR>
-__device__ __forceinline__ float chunk_max(uint32_t ts, int ch, const RowUnit<GR> &u, float mx) {
+__device__ __forceinline__ float chunk_max(const float (&v)[32], int ch, const RowUnit<GR> &u, float mx) {
     constexpr int N = GR == 1 ? 32 : 16;
-    float v[32];
-    load_chunk<GR>(ts, ch, u, v);
 #pragma unroll
     for (int i = 0; i < 32 / N; ++i) {
         const float4 s4 = u.sc[GR == 1 ? 4 * (ch >> 1) : 2 * ch + i];
@@ -278,11 +278,9 @@ __device__ __forceinline__ float chunk_max(uint32_t ts, int ch, const RowUnit<GR
     return mx;
 }
 template <int GR>
-__device__ __forceinline__ float chunk_weights(uint32_t ts, int ch, const RowUnit<GR> &u, float ref, float l) {
+__device__ __forceinline__ float chunk_weights(uint32_t ts, int ch, const RowUnit<GR> &u, const float (&v)[32], float ref, float l) {
     constexpr int N = GR == 1 ? 32 : 16;
-    float v[32];
     uint32_t p[16];
-    load_chunk<GR>(ts, ch, u, v);
 #pragma unroll
     for (int i = 0; i < 32 / N; ++i) {
         const float4 s4 = u.sc[GR == 1 ? 4 * (ch >> 1) : 2 * ch + i];
@@ -400,8 +398,8 @@ __device__ __forceinline__ bool move_reference(uint32_t to, float mx, bool resca
 // wait could meet one for the next item's queries, which in turn wait for this unit.
 // Measured: chunks against halves 0.274 / 0.352 ms at 32 x 5 rows of 8 heads on 16 k keys, 1.48
 // / 1.16 ms at 1000 tokens on 65 k.
-template <int D, int GR, bool BY_HALVES, typename Publish, typename UpperDone>
-__device__ __forceinline__ bool softmax_unit(uint32_t ts, uint32_t to, const RowUnit<GR> &u, bool rescale, float &M, float &l,
+template <int D, int GR, bool BY_HALVES, int NC, typename Publish, typename UpperDone>
+__device__ __forceinline__ bool softmax_unit(uint32_t ts, uint32_t to, const RowUnit<GR> &u, int copy, bool rescale, float &M, float &l,
                                              Publish publish, UpperDone upper_done) {
     auto ref = [&]() { return kv8::kOff - (M == -INFINITY ? 0.f : M); };
     if constexpr (BY_HALVES) {
@@ -417,14 +415,37 @@ __device__ __forceinline__ bool softmax_unit(uint32_t ts, uint32_t to, const Row
         l = half_weights<GR>(ts, 0, u, v, ref(), l);
         tmem_wait_st();
         return publish(0);
-    } else {
-        float mx = -INFINITY;
+    } else if constexpr (NC > 1) {
+        // the copy's keys only, from registers; the other copies' weigh nothing in its rows
+        if constexpr (NC == 2) {
+            float v[2][32];
+            load_half<GR>(ts, copy, u, v);
+            move_reference<D>(to, half_max<GR>(v, copy, u, -INFINITY), rescale, M, l, []() { return true; });
+            l = half_weights<GR>(ts, copy, u, v, ref(), l);
+        } else {
+            float v[32];
+            load_chunk<GR>(ts, copy, u, v);
+            move_reference<D>(to, chunk_max<GR>(v, copy, u, -INFINITY), rescale, M, l, []() { return true; });
+            l = chunk_weights<GR>(ts, copy, u, v, ref(), l);
+        }
+        const uint32_t zero[16] = {};
 #pragma unroll 1
-        for (int ch = 3; ch >= 0; --ch) mx = chunk_max<GR>(ts, ch, u, mx);
+        for (int ch = 0; ch < 4; ++ch)
+            if (ch / (4 / NC) != copy) tmem_st16(ts + kP + 16u * ch, zero);
+        tmem_wait_st();
+        return publish(1) && publish(0);
+    } else {
+        float mx = -INFINITY, v[32];
+#pragma unroll 1
+        for (int ch = 3; ch >= 0; --ch) {
+            load_chunk<GR>(ts, ch, u, v);
+            mx = chunk_max<GR>(v, ch, u, mx);
+        }
         move_reference<D>(to, mx, rescale, M, l, []() { return true; });
 #pragma unroll 1
         for (int ch = 3; ch >= 0; --ch) {
-            l = chunk_weights<GR>(ts, ch, u, ref(), l);
+            load_chunk<GR>(ts, ch, u, v);
+            l = chunk_weights<GR>(ts, ch, u, v, ref(), l);
             if (ch & 1) continue;
             tmem_wait_st();
             if (!publish(ch >> 1)) return false;
@@ -473,10 +494,10 @@ __device__ __forceinline__ void write_stats(const AttnArgs &a, const TileRow &t,
             l == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) - kv8::kOff + log2f(l)) * 0.693147180559945f;
 }
 
-template <Kv8 KV, int D, bool PAIR, int GR>
+template <Kv8 KV, int D, bool PAIR, int NC, int GR>
 __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
     using namespace tl;
-    using L = Lay<D, PAIR>;
+    using L = Lay<D, PAIR, NC>;
     constexpr int RB = L::RB, NCV = L::NCV, NSL = D / 64;
     using Cur = Cursor<RB, UT>;
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -514,6 +535,7 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
         }
         mbar_init(bar(B_ML), 4);
         mbar_init(bar(B_OFREE), 4);
+        mbar_init(bar(B_X), 4);
         s_abort = 0;
         fence_mbar_init();
     }
@@ -544,65 +566,73 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
     auto tiles_of = [&](const Cur &c) { return PAIR && c.r.n * a.G - c.b * RB > TR ? 2 : 1; };
 
     if (warp < 8) {
-        if (warp == 0) {
+        if (warp == 0 || warp == 3) {
             // ============================================================ loads
+            // Warp 0 the keys, warp 3 the values and the scales: an issue of copies is a few hundred
+            // cycles, and one warp's for both lay in the way of the ring of two units.
+            const int w = warp == 0 ? 0 : 1;
             // Lane i < 8 has keys 16 i .. 16 i + 15 of the unit; the first lane of a page copies it.
-            Cur c;
+            // A page entry is read LA units before its copies and the page's scales one before, so
+            // that neither trip to memory lies between one unit's copies and the next's.
+            constexpr int LA = 2;
+            Cur c;                           // of the unit whose entries are read next
             c.start(a, s_place);
-            int page = -1;
-            auto look_up = [&]() {
-                page = -1;
+            int page[LA], head[LA], ahead = 0;    // of units k .. k + LA - 1
+            auto look_up = [&](int &pg, int &h) {
+                pg = -1;
+                h = 0;
+                if (ahead >= units) return;
                 const int tok = c.t * UT + 16 * lane;
-                if (lane < 8 && tok < c.r.kv) page = a.table[(int64_t)c.s * a.W + (tok >> a.page_log2)];
+                if (lane < 8 && tok < c.r.kv) pg = a.table[(int64_t)c.s * a.W + (tok >> a.page_log2)];
+                h = c.h;
+                if (++ahead < units) c.next_unit(a);
             };
-            look_up();
+            auto scales_of = [&](int pg, int h, float &ks, float &vs) {
+                ks = 0.f, vs = -1.f;         // a page that is gone
+                if (pg >= 0 && pg < a.N) {
+                    const int64_t ph = (int64_t)pg * a.Hkv + h;
+                    ks = a.ks[ph];
+                    vs = a.vs[ph];
+                }
+            };
+            const bool first_of_page = lane < 8 && (16 * lane & (P - 1)) == 0;
+#pragma unroll
+            for (int i = 0; i < LA; ++i) look_up(page[i], head[i]);
+            float ks = 0.f, vs = 0.f, ks1 = 0.f, vs1 = 0.f;
+            if (w == 1) scales_of(page[0], head[0], ks, vs);
             bool ok = true;
-            int x = 0, pend = -1;
-            float pk = 0.f, pv = 0.f;
-            auto publish = [&]() {     // the scales of a unit, once they are here
-                if (pend < 0) return;
-                const unsigned gone = __ballot_sync(0xffffffffu, lane < 8 && pv < 0.f);
-                if (lane < 8)
-                    s_sc[(pend % NSC) * 8 + lane] = pv < 0.f ? make_float4(0.f, -1.f, 0.f, 0.f)
-                                                             : make_float4(pk, pv, log2f(pv), 1.f / pv);
-                if (lane == 0) s_gone[pend % NSC] = gone != 0;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(B_SC + pend % NSC));
-                pend = -1;
-            };
+            int x = w;
 #pragma unroll 1
-            for (int k = 0; k < units; ++k) {
-                const bool there = lane < 8 && page >= 0 && page < a.N;
-                const int tok = c.t * UT + 16 * lane;
-                const bool leader = there && (tok & (P - 1)) == 0;
+            for (int k = 0; k < units; ++k, x += 2) {
+                const bool there = page[0] >= 0 && page[0] < a.N, leader = there && first_of_page;
                 const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, leader)) * (uint32_t)(P * D);
-                const int64_t ph = (int64_t)page * a.Hkv + c.h;
-                publish();
-#pragma unroll 1
-                for (int w = 0; w < 2; ++w, ++x) {      // keys, values
-                    const int sl = x % NRAW;
-                    if (x >= NRAW && !(ok = warp_wait(B_RAWFREE + sl, (uint32_t)(x / NRAW - 1)))) break;
-                    if (lane == 0) mbar_arrive_expect_tx(bar(B_RAWFULL + sl), bytes);
-                    __syncwarp();
-                    if (leader)
-                        bulk_load(sb + L::OFF_RAW + (uint32_t)sl * L::RAW + (uint32_t)(16 * lane * D),
-                                  (w ? a.vc : a.kc) + (ph << a.page_log2) * D, (uint32_t)(P * D), bar(B_RAWFULL + sl));
-                }
-                if (!ok) break;
-                pk = 0.f, pv = -1.f;     // a page that is gone
-                if (there) {
-                    pk = a.ks[ph];
-                    pv = fminf(fmaxf(a.vs[ph], kv8::kVsMin), kv8::kVsMax);
-                }
-                pend = k;
-                c.next_unit(a);
-                if (k + 1 < units) look_up();
+                const int64_t at = (((int64_t)page[0] * a.Hkv + head[0]) << a.page_log2) * D;
+                if (w == 1) scales_of(page[1], head[1], ks1, vs1);
+#pragma unroll
+                for (int i = 0; i + 1 < LA; ++i) page[i] = page[i + 1], head[i] = head[i + 1];
+                look_up(page[LA - 1], head[LA - 1]);
+                const int sl = x % NRAW;
+                if (x >= NRAW && !(ok = warp_wait(B_RAWFREE + sl, (uint32_t)(x / NRAW - 1)))) break;
+                if (lane == 0) mbar_arrive_expect_tx(bar(B_RAWFULL + sl), bytes);
+                __syncwarp();
+                if (leader)
+                    bulk_load(sb + L::OFF_RAW + (uint32_t)sl * L::RAW + (uint32_t)(16 * lane * D), (w ? a.vc : a.kc) + at,
+                              (uint32_t)(P * D), bar(B_RAWFULL + sl));
+                if (w == 0) continue;
+                // the scales: their slot is free, since the values of NSC units ago have been used
+                const unsigned gone = __ballot_sync(0xffffffffu, lane < 8 && !there);
+                vs = fminf(fmaxf(vs, kv8::kVsMin), kv8::kVsMax);
+                if (lane < 8)
+                    s_sc[(k % NSC) * 8 + lane] = there ? make_float4(ks, vs, __log2f(vs), __fdividef(1.f, vs)) : make_float4(0.f, -1.f, 0.f, 0.f);
+                if (lane == 0) s_gone[k % NSC] = gone != 0;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_SC + k % NSC));
+                ks = ks1, vs = vs1;
             }
-            if (ok) publish();
             // Leave no copy in flight.  Whoever gives up may do so after this warp's last look, so
             // it waits on every path; all but the last few have landed long ago.
             if (lane == 0)
-                for (int y = max(0, x - NRAW); y < x; ++y)
+                for (int y = max(w, x - NRAW); y < x; y += 2)
                     mbar_wait(bar(B_RAWFULL + y % NRAW), (uint32_t)(y / NRAW) & 1u, kCleanupLimitNs);
         } else if (warp <= (PAIR ? 2 : 1)) {
             // ============================================================ products
@@ -713,8 +743,15 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                     if (ok) scores(k & 1, 0, k);
                     n.next_unit(a);
                 };
-                next_scores(0);
-                if (units > 1) next_scores(1);
+                // Of units up to the second after k.  NC > 1: of unit k + 1's item only, since the next
+                // item's queries are staged when this one's sums have been read.
+                int scored = 0;
+                auto more_scores = [&](int k) {      // c is at unit k + 1
+                    while (ok && scored < units && scored <= k + 2 &&
+                           (NC == 1 || (n.s == c.s && n.h == c.h && n.b == c.b)))
+                        next_scores(scored++);
+                };
+                more_scores(-1);
                 int k0 = 0;              // the item's first unit
 #pragma unroll 1
                 for (int k = 0; ok && k < units; ++k) {
@@ -725,9 +762,9 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                     if (!ok) break;
                     sums(b, k, 0, k - k0 < 2);
                     sums_done(b, k, k + 2 >= k1);
-                    if (k + 2 < units) next_scores(k + 2);
                     c.next_unit(a);
                     if (c.t == 0) k0 = k + 1;
+                    more_scores(k);
                 }
             }
             if (issued) {   // let this warp's products land before the TMEM goes away, on every path
@@ -802,14 +839,14 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
     } else {
         // ================================================================ softmax of buffer b
         const int b = (warp - 8) >> 2, qd = warp & 3;
-        const int row = 32 * qd + lane;                 // of the tile
+        const int row = 32 * qd + lane, copy = PAIR ? 0 : 32 * qd / RB;   // of the tile; of the item's rows
         const uint32_t tl = tmem + ((uint32_t)(32 * qd) << 16);
         const uint32_t ts = tl + TM_S + 128u * b, to = tl + TM_O + 128u * b;
         float2 *s_ml = reinterpret_cast<float2 *>(sm + L::OFF_ML);
         Cur c;
         c.start(a, s_place);
         bool ok = true;
-        uint32_t ns = 0, no = 0, no1 = 0, items = 0;   // units and items of this buffer (and of
+        uint32_t ns = 0, no = 0, no1 = 0, nx = 0, items = 0;   // units and items of this buffer (and of
                                                        // the other's sums), items of the CTA
         int k = 0;                            // unit of the CTA
         TileRow r;
@@ -817,11 +854,11 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
         // this buffer's rows of the item at c: their place, and their queries for the products.  The
         // one-tile form has one tile of queries, which buffer 0's warps stage and whose factors
         // they leave for buffer 1's.
-        const int tile_row0 = (PAIR ? b * TR : 0) + 32 * qd;
+        const int tile_row0 = PAIR ? b * TR + 32 * qd : 32 * qd % RB;
         uint8_t *const qt = sm + L::OFF_Q + (uint32_t)(PAIR ? b : 0) * NSL * SLAB;
         bool begun = false;                   // the next item's copies are on their way
         auto enter_item = [&]() {
-            r = tile_row<RB>(a, c, (PAIR ? b * TR : 0) + row);
+            r = tile_row<RB>(a, c, tile_row0 + lane);
             if (PAIR || b == 0) {
                 if (!begun) begin_queries<D, RB>(a, c, tile_row0, qd, smem_u32(qt));
                 begun = false;
@@ -865,6 +902,7 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                 auto scales_of = [&](int kk) {     // of unit kk, whose scale slot has been waited for
                     u.sc = s_sc + (kk % NSC) * 8;
                     if constexpr (PAIR && GR == 1) u.held[0] = u.sc[0], u.held[1] = u.sc[4];
+                    if constexpr (NC == 2 && GR == 1) u.held[0] = u.held[1] = u.sc[4 * copy];
                     gone = s_gone[kk % NSC];
                 };
 #pragma unroll 1
@@ -892,7 +930,7 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                     tc_fence_after();
                     u.see = r.lim - (t0 + j) * UT;
                     u.part = __any_sync(0xffffffffu, u.see < UT) || gone;
-                    ok = softmax_unit<D, GR, PAIR>(ts, to, u, j > j0, M, l, [&](int h) {
+                    ok = softmax_unit<D, GR, PAIR, NC>(ts, to, u, copy, j > j0, M, l, [&](int h) {
                         // the weights let buffer 1's sums be written again: not before buffer 0's
                         // warps have read those of the item before
                         if (!PAIR && h == 1 && b == 1 && j == j0 && items > 0 && !warp_wait(B_OFREE, items - 1)) return false;
@@ -915,7 +953,7 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
             }
             // ---- the item's sums, after the next item's queries are on their way
             const TileRow done = r;
-            const int64_t slot = ((int64_t)blockIdx.x * 2 + (first ? 1 : 0)) * RB + (PAIR ? b * TR : 0) + row;
+            const int64_t slot = ((int64_t)blockIdx.x * 2 + (first ? 1 : 0)) * RB + tile_row0 + lane;
             const bool had = mine_item;
             const int had0 = PAIR ? mine : (mine + 1 - (k & 1)) >> 1, had1 = PAIR ? mine : (mine + (k & 1)) >> 1;
             k += mine;
@@ -949,6 +987,68 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_ML));
                 }
+                next_item_queries();
+            } else if constexpr (NC > 1) {
+                // The copies' sums are joined through the query tile, 32 columns at a time in two
+                // places in turn; copy 0 writes them.  Its queries are read no more: all scores are done.
+                ok = ok && warp_wait(B_ML, items);
+                if (ok && had0 > 0) ok = warp_wait(B_O + 0, no++);
+                if (ok && had1 > 0) ok = warp_wait(B_O + 1, no1++);
+                if (!ok) break;
+                tc_fence_after();
+                auto meet = [&]() {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_X));
+                    return warp_wait(B_X, nx++);
+                };
+                const float2 ml = s_ml[row];
+                const float Mt = fmaxf(M, ml.x);
+                const float w0 = M == Mt ? 1.f : part_weight(M, Mt), w1 = ml.x == Mt ? 1.f : part_weight(ml.x, Mt);
+                s_ml[row] = make_float2(Mt, l * w0 + ml.y * w1);
+                if (!(ok = meet())) break;
+                float Ma = -INFINITY, la = 0.f;
+#pragma unroll
+                for (int q = 0; q < NC; ++q) Ma = fmaxf(Ma, s_ml[q * RB + row % RB].x);
+#pragma unroll
+                for (int q = 0; q < NC; ++q) {
+                    const float2 x = s_ml[q * RB + row % RB];
+                    la = fmaf(x.x == Ma ? 1.f : part_weight(x.x, Ma), x.y, la);
+                }
+                const float f = Mt == Ma ? 1.f : part_weight(Mt, Ma), inv = la == 0.f ? 0.f : 1.f / la;
+#pragma unroll 1
+                for (int cb = 0; cb < D / 32; ++cb) {
+                    float o[32], o1[32];
+                    tmem_ld32(to + 32u * cb, o);          // a buffer without sums is read, not used
+                    tmem_ld32(to + 128u + 32u * cb, o1);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = ((had0 > 0 ? o[e] * w0 : 0.f) + (had1 > 0 ? o1[e] * w1 : 0.f)) * f;
+                    // row x of the copies after the first, 16-byte pieces spread over the banks
+                    auto piece = [&](int x, int e) {
+                        return reinterpret_cast<float4 *>(sm + L::OFF_Q + (cb & 1) * L::XR + x * 128 + ((e ^ (x & 7)) << 4));
+                    };
+                    if (copy > 0)
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            *piece(row - RB, e) = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    if (!(ok = meet())) break;
+                    if (copy == 0) {
+#pragma unroll 1
+                        for (int q = 0; q < NC - 1; ++q)
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                const float4 x = *piece(q * RB + row, e);
+                                o[4 * e] += x.x, o[4 * e + 1] += x.y, o[4 * e + 2] += x.z, o[4 * e + 3] += x.w;
+                            }
+                        write_chunk<D, RB>(a, done, whole, slot, cb, inv, o);
+                    }
+                }
+                if (!ok) break;
+                if (copy == 0) write_stats(a, done, whole, slot, Ma, la);
+                tc_fence_before();
+                if (!(ok = meet())) break;            // copy 0 has read what the others left
+                if (lane == 0) mbar_arrive(bar(B_OFREE));
                 next_item_queries();
             } else {
                 // the other buffer's scores are done once its M and l are here (or it had none), so
@@ -995,29 +1095,32 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
     grid_launch_dependents();
 }
 
-template <Kv8 KV, int D, bool PAIR, int GR>
+template <Kv8 KV, int D, bool PAIR, int NC, int GR>
 cudaError_t launch_tile_g(AttnArgs &a, void *ws, int ctas, int64_t rows, cudaStream_t s) {
-    using L = tl::Lay<D, PAIR>;
+    using L = tl::Lay<D, PAIR, NC>;
     place_parts(a, ws, ctas, L::RB);
     a.wide = ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.part_o)) & 31) == 0;
-    auto kernel = kv8_tile_kernel<KV, D, PAIR, GR>;
+    auto kernel = kv8_tile_kernel<KV, D, PAIR, NC, GR>;
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(kernel, L::SMEM, allowed);
     if (e != cudaSuccess) return e;
     if ((e = launch_after(kernel, dim3((unsigned)ctas), tl::NT, L::SMEM, s, a)) != cudaSuccess) return e;
     return launch_merge<__nv_bfloat16, D, L::RB>(a, rows, s);
 }
-template <Kv8 KV, int D, bool PAIR>
+template <Kv8 KV, int D, bool PAIR, int NC>
 cudaError_t launch_tile_f(AttnArgs &a, void *ws, int ctas, int64_t rows, cudaStream_t s) {
-    return a.page_log2 >= 6 ? launch_tile_g<KV, D, PAIR, 1>(a, ws, ctas, rows, s)
-                            : launch_tile_g<KV, D, PAIR, 4>(a, ws, ctas, rows, s);
+    return a.page_log2 >= 6 ? launch_tile_g<KV, D, PAIR, NC, 1>(a, ws, ctas, rows, s)
+                            : launch_tile_g<KV, D, PAIR, NC, 4>(a, ws, ctas, rows, s);
 }
 
-// Pairs of tiles where a request may have more rows than one tile.
+// Pairs of tiles where a request may have more rows than one tile; where they fill a half or a
+// quarter of one, that many copies of them.
 template <Kv8 KV, int D>
 cudaError_t launch_tile_d(AttnArgs &a, void *ws, int ctas, int64_t rows, cudaStream_t s) {
-    return rows > tl::TR ? launch_tile_f<KV, D, true>(a, ws, ctas, rows, s)
-                         : launch_tile_f<KV, D, false>(a, ws, ctas, rows, s);
+    return rows > tl::TR       ? launch_tile_f<KV, D, true, 1>(a, ws, ctas, rows, s)
+           : rows > tl::TR / 2 ? launch_tile_f<KV, D, false, 1>(a, ws, ctas, rows, s)
+           : rows > tl::TR / 4 ? launch_tile_f<KV, D, false, 2>(a, ws, ctas, rows, s)
+                               : launch_tile_f<KV, D, false, 4>(a, ws, ctas, rows, s);
 }
 
 }  // namespace
