@@ -1,26 +1,38 @@
-// gdr_kv8_tile.cu -- attention over the 8-bit paged cache for many bf16 query rows a cached
-// head: prompts, chunks of prompts against a long cache, drafted tokens (gdr_kv8_attn).
+// gdr_kv8_tile.cu -- attention over the 8-bit paged cache for more than 16 bf16 query rows a
+// cached head: prompts, chunks of prompts against a long cache, drafted tokens (gdr_kv8_attn).
 //
 // The same mathematics as the split kernel's (gdr_kv8_attn.cu): with a whole-number reference
 // exponent M for each row over x_j + log2 vs,
 //   P_j = 2^(x_j + log2 vs - M + 7),  O += P_j vcode_j,  l += P_j / vs,  o = O / l.
 //
-// Bound: the two products, 4 rows keys D flops, on the 5th-generation tensor cores.  An item
-// is two tiles of 128 rows (row = query x group of heads) that share every key, a unit 128
-// keys.  A tile's scores S (128 x 128 fp32) and sums O live in TMEM; its weights go back over
-// S as halves and are the A operand of the second product from there, so that they never
-// touch shared memory.
+// A unit is 128 keys; an item's rows (row = query x group of heads) are tiles of 128.  A tile's
+// scores S (128 x 128 fp32) and sums O live in TMEM; its weights go back over S as halves and
+// are the A operand of the second product from there, so that they never touch shared memory.
 // The codes come by bulk copies (a page's block of a head is contiguous) and are widened to
 // halves in the tensor core's swizzled layout: keys K-major, values MN-major from the same
 // [token][64 values] rows, so values need no transpose.
 //
-// Two forms.  PAIR (items of 256 rows): two tiles of different rows share every key, the
-// softmax of one runs under the products of the other.  Otherwise (items of at most 128
-// rows, where the cache's bytes bound): one tile of rows, whose units alternate between the
-// two score and output buffers; the two halves of the sum are joined at the item's end.
+// Three forms, by the most rows of a cached head that a request has:
+//   PAIR (above 128): items of 256 rows.  Two tiles of different rows share every key, the
+//       softmax of one runs under the products of the other.
+//   one tile (65 to 128): its units alternate between the two score and sum buffers.
+//   copies (up to 64 or 32, NC = 2 or 4): the tile holds the rows NC times, and a copy's warps
+//       take the softmax of their half or quarter of the unit's keys only, with weights of zero
+//       elsewhere: what a warp does a unit is 1 / NC, and all four parts of the SM work at the
+//       exponentials.  The copies' sums are joined at the item's end.
 //
-// Warps: 0 and 3 load (keys; values and scales), 1 and 2 issue the products
-// (1 owns the TMEM), 4-7 widen (two the keys, two the values), 8-11 and 12-15 the softmax of buffer 0 and 1, a thread a row:
+// Bounds.  PAIR: the two products, 4 rows keys D flops.  Measured: 1000 tokens of 4 heads a
+// cached head, 8 of those, on 65 k keys (1.07 TFLOP) 0.963 ms = 1.11 PFLOP/s, 57 % of a large
+// matrix product's measured rate; four prompts of 4096 (275 GFLOP counting only what is seen)
+// 0.406 ms.  The tensor cores wait for the softmax's chain of TMEM loads, maxima, exponentials
+// and stores (two tiles hide about half of it), and run at about 1.5 GHz under the power limit.
+// Copies: the cache's bytes.  32 requests of 5 x 8 rows on up to 32 k keys (555 MB) 0.187 ms =
+// 3.0 TB/s.  Of the 2400 cycles that a unit takes the widening warps work 1500 and wait 700 for a
+// slot that the products give back; shared memory is busy for as much: a unit's 32 KB of codes
+// are read once, written widened (64 KB) and read by the products with the queries (96 KB).
+//
+// Warps: 0 and 3 load (keys; values and scales), 1 and 2 issue the products (1 owns the TMEM),
+// 4-5 widen keys, 6-7 values, 8-11 and 12-15 the softmax of buffer 0 and 1, a thread a row:
 // maxima and sums never leave the thread.  No barrier spans the CTA inside the loop; every
 // wait is bounded.
 
@@ -395,9 +407,10 @@ __device__ __forceinline__ bool move_reference(uint32_t to, float mx, bool resca
 // lower half's maximum is taken after the upper half's weights are out, and waits for their
 // products if it moves M.  Else (the cache's bytes bound): chunk by chunk, all maxima first, and
 // nothing here waits for a product: with one warp issuing for both buffers, in order, such a
-// wait could meet one for the next item's queries, which in turn wait for this unit.
-// Measured: chunks against halves 0.274 / 0.352 ms at 32 x 5 rows of 8 heads on 16 k keys, 1.48
-// / 1.16 ms at 1000 tokens on 65 k.
+// wait could meet one for the next item's queries, which in turn wait for this unit.  Chunks
+// measured against halves: 0.274 / 0.352 ms for 32 requests of 5 x 8 rows on up to 32 k keys in
+// one tile, 1.48 / 1.16 ms for pairs at 1000 tokens on 65 k.  NC > 1: the keys of this warp's
+// copy alone, in registers (one tile against two copies 0.225 / 0.219 ms there).
 template <int D, int GR, bool BY_HALVES, int NC, typename Publish, typename UpperDone>
 __device__ __forceinline__ bool softmax_unit(uint32_t ts, uint32_t to, const RowUnit<GR> &u, int copy, bool rescale, float &M, float &l,
                                              Publish publish, UpperDone upper_done) {
@@ -569,11 +582,13 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
         if (warp == 0 || warp == 3) {
             // ============================================================ loads
             // Warp 0 the keys, warp 3 the values and the scales: an issue of copies is a few hundred
-            // cycles, and one warp's for both lay in the way of the ring of two units.
+            // cycles, and one warp's for both (1600 of 2400 cycles a unit) lay in the way of the ring
+            // of two units: 32 requests of 5 x 8 rows 0.200 -> 0.187 ms.
             const int w = warp == 0 ? 0 : 1;
             // Lane i < 8 has keys 16 i .. 16 i + 15 of the unit; the first lane of a page copies it.
             // A page entry is read LA units before its copies and the page's scales one before, so
-            // that neither trip to memory lies between one unit's copies and the next's.
+            // that neither trip to memory lies between one unit's copies and the next's (0.219 ->
+            // 0.200 ms, with pages of 16 0.244 -> 0.207; four prompts of 4096 0.397 -> 0.404).
             constexpr int LA = 2;
             Cur c;                           // of the unit whose entries are read next
             c.start(a, s_place);
@@ -1114,7 +1129,8 @@ cudaError_t launch_tile_f(AttnArgs &a, void *ws, int ctas, int64_t rows, cudaStr
 }
 
 // Pairs of tiles where a request may have more rows than one tile; where they fill a half or a
-// quarter of one, that many copies of them.
+// quarter of one, that many copies of them (32 requests on up to 32 k keys, 24 and 40 rows: one
+// copy 0.221 and 0.225 ms, four and two 0.212 and 0.219, before the loads were two warps').
 template <Kv8 KV, int D>
 cudaError_t launch_tile_d(AttnArgs &a, void *ws, int ctas, int64_t rows, cudaStream_t s) {
     return rows > tl::TR       ? launch_tile_f<KV, D, true, 1>(a, ws, ctas, rows, s)

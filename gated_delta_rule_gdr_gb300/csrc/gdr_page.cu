@@ -16,6 +16,9 @@
 // pages and released pages: one launch, no order between CTAs.  In place, and still
 // without an order: tokens read only table entries below old_s and ring entries of this
 // call's grants, the writes go to entries at or above old_s and behind the ring's end.
+//
+// Bound: the launch and the scans' latency (300 requests of one token 6.6 us, 24 KB; 60 prompts
+// of some 250 k tokens together 8.0 us, 2.0 MB, of which the bytes are 0.3 us).
 
 #include "gdr_internal.h"
 
