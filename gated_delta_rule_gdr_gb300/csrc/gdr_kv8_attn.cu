@@ -43,6 +43,7 @@ constexpr int SLAB = 32;               // tokens a warp takes at a time
 // its own, and join their sums at the item's end.
 constexpr int NW = 4;                  // warps a CTA
 constexpr int UT = NW * SLAB;          // tokens of a unit
+constexpr int ITEM = 2;                // what an item's ends cost, in units
 // Slabs of a ring and CTAs an SM (two blocks' fragments need the registers of 8 warps an SM).
 template <int R> constexpr int ST = R == 2 ? 3 : 2;
 template <int R> constexpr int CPS = R == 2 ? 2 : 3;
@@ -96,7 +97,7 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     extern __shared__ __align__(1024) uint8_t sm[];
     __shared__ __align__(8) uint64_t s_bar[NW * ST];
     __shared__ Place s_place;
-    __shared__ int64_t s_scan[NW];
+    __shared__ int64_t s_scan[2 * NW];
     __shared__ float s_stat[2][NW][RB];          // M, l of each warp at an item's end
     __shared__ volatile int s_abort;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
@@ -115,8 +116,8 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         tma_prefetch_desc(&tm_v);
     }
     grid_dependency_wait();
-    find_place<RB, UT, 32 * NW>(a, &s_place, s_scan);
-    const int64_t u0 = s_place.u0, total = s_place.total;
+    find_place<RB, UT, 32 * NW, sp::ITEM>(a, &s_place, s_scan);
+    const int64_t u0 = s_place.u0;
     const int units = (int)(s_place.u1 - u0);
     if (units == 0) {
         if (tid == 0) a.entry[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -188,7 +189,7 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     uint32_t phase = 0;
     int waited = 0;
 #pragma unroll 1
-    for (int done = 0; done < units;) {
+    for (int done = 0, item = 0; done < units; ++item) {
         const int t_first = c.t, t_last = min(c.nt, t_first + units - done);   // this CTA's units of the item
         const int row0 = c.b * RB, rows = min(RB, c.r.n * a.G - row0);
         // query fragments: row 8 n + g, values LD t4 .. LD t4 + LD - 1, word j of a key holding
@@ -440,7 +441,7 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         const bool first = t_first == 0, last = t_last == c.nt;
         const int64_t slot = ((int64_t)blockIdx.x * 2 + (first ? 1 : 0)) * RB;
         if (first && !last)
-            entry = make_int4(cta_of(u0 + done + c.nt - 1, total, s_place.ctas), c.s, c.h, c.b);
+            entry = make_int4(cta_of(s_place, u0 + done + c.nt - 1, s_place.i0 + item), c.s, c.h, c.b);
 #pragma unroll
         for (int pass = 0; pass < 2 * R; ++pass) {       // rows 4 pass .. 4 pass + 3
             if (4 * pass >= rows) break;

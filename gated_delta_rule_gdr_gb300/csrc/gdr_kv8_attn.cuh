@@ -88,83 +88,107 @@ __device__ __forceinline__ int64_t units_of_head(const AttnArgs &a, const Reques
 
 struct Place {      // a unit: request, head, block of rows, unit of the block's keys
     int s, h, b, t;
-    int ctas;                // CTAs with work
-    int64_t u0, u1, total;   // this CTA's units, all units
+    int ctas, extra;         // CTAs with work; units that an item's ends count for
+    int64_t u0, u1, i0;      // this CTA's units, the items before the first one's
+    int64_t total;           // what is shared: all units, and `extra` for each item
 };
 
-// This CTA's units and the place of the first one.  All NT threads call it; `place` is in
-// shared memory and valid after it returns.
-template <int RB, int UT, int NT>
+// This CTA's units and the place of the first one.  An item costs its units and, for its queries
+// and its end, as much as E more; what is divided evenly is the sum of both (the units of an
+// item follow its E), or the units alone where a CTA's share would be no more than E.  All NT
+// threads call it; `place` is in shared memory and valid after it returns.
+template <int RB, int UT, int NT, int E>
 __device__ __forceinline__ void find_place(const AttnArgs &a, Place *place, int64_t *s_scan) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int NW = NT / 32;
-    int64_t run = 0, mine = 0, before = 0, sum = 0;
-    // units before each request of a chunk of NT requests; the last chunk stays in registers
+    struct Sum {
+        int64_t u, i;        // units, items
+    };
+    Sum mine{}, before{}, sum{};
+    // what comes before each request of a chunk of NT requests; the last chunk stays in registers
     auto scan = [&](int base) {
         const int s = base + tid;
-        mine = s < a.S ? units_of_head<RB, UT>(a, request_of(a, s)) * a.Hkv : 0;
-        int64_t incl = mine;
+        mine = Sum{0, 0};
+        if (s < a.S) {
+            const Request r = request_of(a, s);
+            mine.u = units_of_head<RB, UT>(a, r) * a.Hkv;
+            mine.i = (int64_t)blocks_of<RB>(a, r) * a.Hkv;
+        }
+        Sum incl = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += y;
+            const int64_t u = __shfl_up_sync(0xffffffffu, incl.u, off), i = __shfl_up_sync(0xffffffffu, incl.i, off);
+            if (lane >= off) incl.u += u, incl.i += i;
         }
         __syncthreads();
-        if (lane == 31) s_scan[warp] = incl;
+        if (lane == 31) s_scan[2 * warp] = incl.u, s_scan[2 * warp + 1] = incl.i;
         __syncthreads();
-        before = incl - mine;
-        sum = 0;
+        before = Sum{incl.u - mine.u, incl.i - mine.i};
+        sum = Sum{0, 0};
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            if (w < warp) before += s_scan[w];
-            sum += s_scan[w];
+            const int64_t u = s_scan[2 * w], i = s_scan[2 * w + 1];
+            if (w < warp) before.u += u, before.i += i;
+            sum.u += u, sum.i += i;
         }
     };
-    int64_t total = 0;
+    Sum all{};
     for (int base = 0; base < a.S; base += NT) {
         scan(base);
-        total += sum;
+        all.u += sum.u, all.i += sum.i;
     }
+    const int e = all.u + E * all.i >= (int64_t)(E + 1) * gridDim.x ? E : 0;
+    const int64_t total = all.u + e * all.i;
     // fewer units than CTAs: one each, so that the parts of an item lie in consecutive CTAs
+    // (as they do with e > 0, when no CTA's share is less than the way from one unit to the next)
     const int64_t ctas = min((int64_t)gridDim.x, max(total, (int64_t)1));
-    const int64_t u0 = blockIdx.x < ctas ? total * blockIdx.x / ctas : total;
-    const int64_t u1 = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : total;
+    const int64_t w0 = blockIdx.x < ctas ? total * blockIdx.x / ctas : total;
+    const int64_t w1 = blockIdx.x < ctas ? total * (blockIdx.x + 1) / ctas : total;
     if (tid == 0) {
-        place->u0 = u0;
-        place->u1 = u1;
+        place->u0 = all.u;
+        place->u1 = all.u;
         place->total = total;
         place->ctas = (int)ctas;
+        place->extra = e;
     }
-    if (u0 < u1) {
+    __syncthreads();
+    if (w0 < w1) {
+        Sum run{};
         for (int base = 0; base < a.S; base += NT) {
             if (a.S > NT) scan(base);
-            if (u0 >= run + before && u0 < run + before + mine) {
-                const int s = base + tid;
-                const Request r = request_of(a, s);
-                int64_t rem = u0 - run - before;
-                const int64_t per = mine / a.Hkv;
-                place->s = s;
-                place->h = (int)(rem / per);
-                rem -= place->h * per;
+            const int64_t at = run.u + before.u + e * (run.i + before.i), end = at + mine.u + e * mine.i;
+#pragma unroll 1
+            for (int k = 0; k < 2; ++k) {            // the first unit at or after w0, and after w1
+                const int64_t w = k ? w1 : w0;
+                if (w < at || w >= end) continue;
+                const Request r = request_of(a, base + tid);
+                const int64_t per_u = mine.u / a.Hkv, per_i = mine.i / a.Hkv, h = (w - at) / (per_u + e * per_i);
+                int64_t rem = w - at - h * (per_u + e * per_i), u = run.u + before.u + h * per_u;
                 int b = 0;
                 for (;; ++b) {
-                    const int u = units_of<UT>(block_end<RB>(a, r, b));
-                    if (rem < u) break;
-                    rem -= u;
+                    const int n = units_of<UT>(block_end<RB>(a, r, b));
+                    if (rem < n + e) break;
+                    rem -= n + e;
+                    u += n;
                 }
-                place->b = b;
-                place->t = (int)rem;
+                const int t = (int)max(rem - e, (int64_t)0);
+                if (k) {
+                    place->u1 = u + t;
+                } else {
+                    place->u0 = u + t;
+                    place->i0 = run.i + before.i + h * per_i + b;
+                    place->s = base + tid, place->h = (int)h, place->b = b, place->t = t;
+                }
             }
-            run += sum;
-            if (u0 < run) break;
+            run.u += sum.u, run.i += sum.i;
         }
     }
     __syncthreads();
 }
 
-// The CTA that has unit u.
-__device__ __forceinline__ int cta_of(int64_t u, int64_t total, int ctas) {
-    return (int)(((u + 1) * ctas - 1) / total);
+// The CTA that has unit u, which belongs to item i.
+__device__ __forceinline__ int cta_of(const Place &p, int64_t u, int64_t i) {
+    return (int)(((u + p.extra * (i + 1) + 1) * p.ctas - 1) / p.total);
 }
 
 // Moves to the next item: next block, head, request with queries.

@@ -58,6 +58,7 @@ enum : int {
 };
 template <int D, bool PAIR, int NC> struct Lay {
     static constexpr int RB = PAIR ? kKv8TileRows : TR / NC;   // rows of an item
+    static constexpr int ITEM = PAIR ? 3 : 8;             // what an item's ends cost, in units
     static constexpr uint32_t XR = (TR - TR / NC) * 128;  // sums of the copies that are joined, 32 columns (NC > 1)
     static constexpr int NCV = PAIR ? 3 : 4;              // widened slots
     static constexpr uint32_t RAW = UT * D, CV = UT * D * 2;
@@ -517,7 +518,7 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
     const uint32_t sb = smem_u32(sm);
     __shared__ __align__(8) uint64_t s_bar[NUM_BARS];
     __shared__ Place s_place;
-    __shared__ int64_t s_scan[NT / 32];
+    __shared__ int64_t s_scan[2 * NT / 32];
     __shared__ uint32_t s_tmem;
     __shared__ int s_gone[NSC];
     __shared__ float s_cs[4];        // one-tile form: the score factors of the tile's four groups of rows
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
         fence_mbar_init();
     }
     grid_dependency_wait();
-    find_place<RB, UT, NT>(a, &s_place, s_scan);
+    find_place<RB, UT, NT, L::ITEM>(a, &s_place, s_scan);
     const int64_t u0 = s_place.u0;
     const int units = (int)(s_place.u1 - u0);
     if (units == 0) {
@@ -903,7 +904,7 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
             if (tid == 256) {
                 // the CTA's entry: an item that begins here and ends elsewhere (its last)
                 if (first && !last)
-                    a.entry[blockIdx.x] = make_int4(cta_of(u0 + k + c.nt - 1, s_place.total, s_place.ctas), c.s, c.h, c.b);
+                    a.entry[blockIdx.x] = make_int4(cta_of(s_place, u0 + k + c.nt - 1, s_place.i0 + items), c.s, c.h, c.b);
                 else if (k + mine == units)
                     a.entry[blockIdx.x] = make_int4(-1, 0, 0, 0);
             }
