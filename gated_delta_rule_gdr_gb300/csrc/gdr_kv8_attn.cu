@@ -9,8 +9,8 @@
 // the value scale rides in the exponent's addend and costs nothing per element.
 //
 // Bound: the cache's bytes.  Measured: 256 requests of 100 to 8192 keys, 8 heads a cached head
-// (1029 MB) 0.180 ms = 5.7 TB/s, 84 % of the measured copy rate; one of a million keys (1074
-// MB) 0.171 ms = 6.3 TB/s; loads alone, without the arithmetic, took 0.177 and 0.167.  At group
+// (1029 MB) 0.166 ms = 6.2 TB/s, 91 % of the measured copy rate; one of a million keys (1074
+// MB) 0.172 ms = 6.2 TB/s; loads alone took the million 0.167.  At group
 // size 8 a byte of keys or values meets 16 flops, far
 // below what the tensor cores need, so the kernel's job is to keep enough loads in flight
 // and to stay within the issue slots: 12 warps an SM, each with two 8 KB slabs (32 tokens of
@@ -43,7 +43,9 @@ constexpr int SLAB = 32;               // tokens a warp takes at a time
 // its own, and join their sums at the item's end.
 constexpr int NW = 4;                  // warps a CTA
 constexpr int UT = NW * SLAB;          // tokens of a unit
-constexpr int ITEM = 2;                // what an item's ends cost, in units
+// What an item's ends cost, in units (0 / 1 / 2 / 3: 256 requests of 100 to 8192 keys 0.179 / 0.172 /
+// 0.166 / 0.166 ms, of 100 to 600 0.043 / 0.039 / 0.036 / 0.036).
+constexpr int ITEM = 2;
 // Slabs of a ring and CTAs an SM (two blocks' fragments need the registers of 8 warps an SM).
 template <int R> constexpr int ST = R == 2 ? 3 : 2;
 template <int R> constexpr int CPS = R == 2 ? 2 : 3;
@@ -566,7 +568,8 @@ Shape shape_of(int max_q, int G, Elem e) {
     // fp32 (the accuracy path) stays at 16 rows: its fragments are twice as large.  bf16 up to 16
     // rows: 32 requests on 16 k keys 0.145 ms here, 0.182 in the tile kernel; beyond, 32 rows in
     // warps of their own on shared slabs took 0.243 ms against the tile kernel's 0.182 (on 300
-    // keys 0.022 against 0.034: an item's ends cost the tile kernel more)
+    // keys 0.022 against 0.034: an item's ends cost the tile kernel more; both with all units
+    // divided evenly)
     return rows <= 16 || e == Elem::F32 ? Shape::R16 : Shape::TILE;
 }
 template <typename E, Kv8 KV, int D>

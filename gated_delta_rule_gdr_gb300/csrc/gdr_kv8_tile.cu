@@ -22,12 +22,12 @@
 //       exponentials.  The copies' sums are joined at the item's end.
 //
 // Bounds.  PAIR: the two products, 4 rows keys D flops.  Measured: 1000 tokens of 4 heads a
-// cached head, 8 of those, on 65 k keys (1.07 TFLOP) 0.963 ms = 1.11 PFLOP/s, 57 % of a large
+// cached head, 8 of those, on 65 k keys (1.07 TFLOP) 0.984 ms = 1.09 PFLOP/s, 56 % of a large
 // matrix product's measured rate; four prompts of 4096 (275 GFLOP counting only what is seen)
-// 0.406 ms.  The tensor cores wait for the softmax's chain of TMEM loads, maxima, exponentials
-// and stores (two tiles hide about half of it), and run at about 1.5 GHz under the power limit.
-// Copies: the cache's bytes.  32 requests of 5 x 8 rows on up to 32 k keys (555 MB) 0.187 ms =
-// 3.0 TB/s.  Of the 2400 cycles that a unit takes the widening warps work 1500 and wait 700 for a
+// 0.347 ms.  The tensor cores wait for the softmax's chain of TMEM loads, maxima, exponentials
+// and stores (two tiles hide about half of it).
+// Copies: the cache's bytes.  32 requests of 5 x 8 rows on up to 32 k keys (555 MB) 0.155 ms =
+// 3.6 TB/s.  Of the 2400 cycles that a unit takes the widening warps work 1500 and wait 700 for a
 // slot that the products give back; shared memory is busy for as much: a unit's 32 KB of codes
 // are read once, written widened (64 KB) and read by the products with the queries (96 KB).
 //
@@ -58,7 +58,10 @@ enum : int {
 };
 template <int D, bool PAIR, int NC> struct Lay {
     static constexpr int RB = PAIR ? kKv8TileRows : TR / NC;   // rows of an item
-    static constexpr int ITEM = PAIR ? 3 : 8;             // what an item's ends cost, in units
+    // What an item's ends cost, in units.  PAIR 0 / 2 / 3 / 4: four prompts of 4096 0.415 / 0.352 /
+    // 0.347 / 0.347 ms; else 0 / 6 / 8 / 12: 200 requests of 5 x 8 rows on up to 2000 keys 0.178 /
+    // 0.120 / 0.120 / 0.125, 32 on up to 32 k 0.187 / 0.158 / 0.155 / 0.159.
+    static constexpr int ITEM = PAIR ? 3 : 8;
     static constexpr uint32_t XR = (TR - TR / NC) * 128;  // sums of the copies that are joined, 32 columns (NC > 1)
     static constexpr int NCV = PAIR ? 3 : 4;              // widened slots
     static constexpr uint32_t RAW = UT * D, CV = UT * D * 2;

@@ -431,6 +431,17 @@ def test_seventeen_to_thirty_two_rows(kv, lens, qs, Hq, Hkv, D, page):
     check(attn_case(lens, qs, Hq, Hkv, D, page, BF16, kv, seed=8 + D, gone=0.3))
 
 
+@pytest.mark.parametrize("S,q,kv_max", [(700, 1, 300), (700, 2, 200), (1100, 5, 150), (530, 20, 140)])
+def test_many_requests(S, q, kv_max):
+    """More requests than a CTA has threads, of no to a few units each, some without queries:
+    the places that the CTAs find for themselves, and items that end where a CTA's share does."""
+    r = random.Random(S + q)
+    lens = [r.choice([0, 1, r.randint(0, kv_max), kv_max]) for _ in range(S)]
+    qs = [1] * S if q == 1 else [r.choice([0, 1, q, q]) for _ in range(S)]
+    qs[5] = q
+    check(attn_case(lens, qs, 8, 1, 64, 16, BF16, "int8", seed=S))
+
+
 @pytest.mark.slow
 def test_offsets_past_32_bits():
     """A cache of over 2^32 bytes of keys: the request's pages lie at its end."""
