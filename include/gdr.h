@@ -539,7 +539,8 @@ typedef enum {
  * Block tables and slot maps, on the device from the requests' lengths.
  *   kv_len    [S]  tokens cached so far
  *   q_len     [S]  new tokens of this step; negative: the request is finished and its
- *                  ceil(kv_len / page) pages return to the free ring
+ *                  ceil(kv_len / page) pages return to the free ring, but for entries
+ *                  outside [0, num_pages) (pages that are gone)
  *   block_table [S][table_width]  in/out: entries of the pages granted here are written
  *                  (a finished request's row is left as it is)
  *   free_ring [num_pages] in/out, free_state [2] = {head, count}: the free pages are

@@ -65,8 +65,9 @@ def plan(kv_len, q_len, table, ring, state, page, max_tokens):
         old = -(-kv // page)
         if n < 0:
             for i in range(old):
-                ring[(head + count + back) % N] = table[s, i]
-                back += 1
+                if 0 <= table[s, i] < N:             # else a page that is gone
+                    ring[(head + count + back) % N] = table[s, i]
+                    back += 1
             kv_out.append(0)
             granted.append(1)
         else:

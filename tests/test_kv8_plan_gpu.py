@@ -1,0 +1,82 @@
+"""gdr_page_plan on the GPU where requests do not hold plain rows of pages, against the integer
+oracle: pages that are gone.  All outputs are whole numbers: equal."""
+from __future__ import annotations
+
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_gdr_gb300 as gdr
+from oracle import kv8 as O
+
+pytestmark = pytest.mark.gpu
+NAMES = ("kv", "cu", "slots", "pos", "granted", "state", "table", "ring")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    gdr.load(build_if_missing=True)
+    yield
+    assert gdr.last_device_error() == 0
+
+
+def i32(v):
+    return torch.tensor(np.asarray(v), dtype=torch.int32, device="cuda")
+
+
+def check_plan(kv, q, table, ring, state, page, T):
+    t, r = i32(table), i32(ring)
+    got = gdr.page_plan(i32(kv), i32(q), t, r, i32(state), page, T)
+    want = O.plan(kv, q, table, ring, state, page, T)
+    for g, w, name in zip((*got, t, r), want, NAMES):
+        assert np.array_equal(g.cpu().numpy(), np.asarray(w)), name
+    return [np.asarray(w) for w in want]
+
+
+def pool(S, W, page, seed, *, kv_max, q_max, finished, free, markers, gone):
+    """Requests over a shuffled pool whose entries are `markers` here and there."""
+    r = random.Random(seed)
+    kv = [r.randint(0, kv_max) for _ in range(S)]
+    q = [-1 if r.random() < finished else r.randint(0, q_max) for _ in range(S)]
+    N = sum(-(-k // page) for k in kv) + free
+    perm = list(range(N))
+    r.shuffle(perm)
+    table, it = np.full((S, W), -7), iter(perm)
+    for s, k in enumerate(kv):
+        for i in range(-(-k // page)):
+            table[s, i] = next(it)
+            if r.random() < gone:
+                table[s, i] = r.choice(markers) if r.random() < 0.9 else N
+    head, ring = r.randrange(N), np.full(N, -3)
+    for i, p in enumerate(it):
+        ring[(head + i) % N] = p
+    return kv, q, table, ring, [head, free], sum(n for n in q if n > 0) + 5
+
+
+# ------------------------------------------------------------------ pages that are gone
+def test_a_finished_request_gives_back_the_pages_it_has():
+    """Pages of 16.  Request 0 ends with the pages 5, gone, 6; request 1 takes four free ones.
+    The next call hands out 5 and 6, and then there are no more."""
+    table, ring = i32([[5, -1, 6, -1, -1], [-1] * 5]), i32([0, 1, 2, 3, -1, -1, -1, -1])
+    kv, _, slots, _, ok, state = gdr.page_plan(i32([48, 0]), i32([-1, 64]), table, ring, i32([0, 4]), 16, 64)
+    assert ok.tolist() == [1, 1] and kv.tolist() == [0, 64]
+    assert slots.tolist() == list(range(64)) and table[1].tolist() == [0, 1, 2, 3, -1]
+    assert state.tolist() == [4, 2] and ring.tolist()[4:6] == [5, 6]
+    kv, _, slots, _, ok, state = gdr.page_plan(kv, i32([32, 0]), table, ring, state, 16, 32)
+    assert ok.tolist() == [1, 1] and slots.tolist() == list(range(80, 112)) and state.tolist() == [6, 0]
+    _, _, slots, _, ok, _ = gdr.page_plan(kv, i32([1, 0]), table, ring, state, 16, 1)
+    assert ok.tolist() == [0, 1] and slots.tolist() == [-1]
+
+
+@pytest.mark.parametrize("S,W,page,kv_max,finished,gone", [
+    (1, 40, 16, 640, 1.0, 0.3), (7, 1500, 16, 24000, 0.6, 0.02), (300, 40, 64, 2500, 0.3, 0.1),
+    (1500, 20, 32, 600, 0.5, 0.3), (9, 700, 128, 89000, 1.0, 1.0), (60, 300, 16, 4800, 0.5, 0.0),
+    (8192, 3, 16, 48, 0.4, 0.2), (300, 2000, 16, 3000, 0.5, 0.1), (8192, 70, 16, 100, 0.3, 0.2), (600, 900, 32, 9000, 0.3, 0.0),
+])
+def test_gone_pages_do_not_come_back(S, W, page, kv_max, finished, gone):
+    check_plan(*pool(S, W, page, S + W, kv_max=kv_max, q_max=0, finished=finished, free=50,
+                     markers=[-1, -2 ** 31, 2 ** 31 - 1], gone=gone)[:5], page, 5)
