@@ -7,7 +7,8 @@
 //   if it fits and needs no page, or the fitting requests up to and including it need at
 //   most `count` pages -- so the grant depends on the order of the requests alone
 //   table[s][old_s + i] = ring[(head + sum_{r<s} need_r + i) mod N]
-//   slot of token i     = table[s][(kv_s + i) / P] P + (kv_s + i) mod P
+//   slot of token i     = table[s][(kv_s + i) / P] P + (kv_s + i) mod P, -1 where that entry is
+//                         outside [0, N)
 //   a finished request's old_s pages go behind the ring's last one and its length to 0;
 //   entries of its row outside [0, N) are pages that are gone and stay out of the ring.
 //
@@ -176,11 +177,13 @@ __global__ void __launch_bounds__(PT) page_plan_kernel(const PlanArgs a) {
             // the end of the request's tokens: a saturated prefix means it does not fit
             const int64_t end = (int64_t)s_cu[s] + n;
             if (granted_pages(s, kv, n, (int)min(end, (int64_t)a.max_tokens + 1)) >= 0) {
-                pos = kv + (t - s_cu[s]);
-                const int p = pos / P;
+                const int at = kv + (t - s_cu[s]), p = at / P;
                 const int page = p < old ? a.table[(int64_t)s * a.W + p]
                                          : a.ring[((int64_t)head + s_need[s] + (p - old)) % a.N];
-                slot = page * P + (pos - p * P);
+                if ((unsigned)page < (unsigned)a.N) {      // else a page that is gone: no place
+                    pos = at;
+                    slot = page * P + (at - p * P);
+                }
             }
         }
         a.slots[t] = slot;

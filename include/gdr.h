@@ -551,7 +551,8 @@ typedef enum {
  *                   must not be kv_len or q_len itself
  *   cu_q      [S+1] first new token of each request in the packed batch (at most max_tokens)
  *   slots     [max_tokens] page * `page` + place of every new token; -1 past the last
- *                   token and for requests that were not granted
+ *                   token, for requests that were not granted, and for tokens of a page
+ *                   that is gone (a partly filled one that the table no longer has)
  *   positions [max_tokens] position of every new token in its request; -1 likewise
  *   granted   [S]   1, or 0 for a request that does not fit (kv_len + q_len above
  *                   table_width * page, or its tokens end past max_tokens) or for which no

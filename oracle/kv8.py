@@ -81,8 +81,10 @@ def plan(kv_len, q_len, table, ring, state, page, max_tokens):
                     table[s, i] = ring[(head + taken) % N]
                     taken += 1
                 for i in range(n):
-                    slots[tok + i] = table[s, (kv + i) // page] * page + (kv + i) % page
-                    pos[tok + i] = kv + i
+                    p = int(table[s, (kv + i) // page])
+                    if 0 <= p < N:
+                        slots[tok + i] = p * page + (kv + i) % page
+                        pos[tok + i] = kv + i
             tok += n
             kv_out.append(kv + n if ok else kv)
             granted.append(int(ok))

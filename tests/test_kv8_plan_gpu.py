@@ -80,3 +80,21 @@ def test_a_finished_request_gives_back_the_pages_it_has():
 def test_gone_pages_do_not_come_back(S, W, page, kv_max, finished, gone):
     check_plan(*pool(S, W, page, S + W, kv_max=kv_max, q_max=0, finished=finished, free=50,
                      markers=[-1, -2 ** 31, 2 ** 31 - 1], gone=gone)[:5], page, 5)
+
+
+@pytest.mark.parametrize("marker", [-1, 40, 1 << 26, -(1 << 26), 2 ** 31 - 1])
+def test_tokens_of_a_gone_page_have_no_slot(marker):
+    """Request 0's partly filled page is gone: its next tokens have no place (1 << 26 times 64
+    would wrap to slot 0 of another request's page), those past it do."""
+    table = np.full((2, 4), -1)
+    table[0, :2], table[1, 0] = (3, marker), 0
+    got = check_plan([70, 10], [60, 2], table, np.arange(40) % 7 + 10, [0, 7], 64, 64)
+    slots, pos = got[2], got[3]
+    assert (slots[:58] == -1).all() and (pos[:58] == -1).all()
+    assert slots[58:62].tolist() == [640, 641, 10, 11] and pos[58:62].tolist() == [128, 129, 10, 11]
+
+
+@pytest.mark.parametrize("S,W,page", [(5, 30, 16), (200, 40, 32), (1000, 12, 64)])
+def test_gone_pages_at_random(S, W, page):
+    check_plan(*(x := pool(S, W, page, S, kv_max=(W - 3) * page, q_max=3 * page, finished=0.1, free=2 * S,
+                           markers=[-1, 1 << 26, -(1 << 26)], gone=0.3))[:5], page, x[5])
