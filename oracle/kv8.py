@@ -62,7 +62,7 @@ def plan(kv_len, q_len, table, ring, state, page, max_tokens):
     tok = taken = back = want = 0
     for s in range(S):
         kv, n = int(kv_len[s]), int(q_len[s])
-        old = -(-kv // page)
+        old = min(-(-kv // page), W)
         if n < 0:
             for i in range(old):
                 if 0 <= table[s, i] < N:             # else a page that is gone

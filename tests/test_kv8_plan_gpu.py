@@ -1,5 +1,5 @@
 """gdr_page_plan on the GPU where requests do not hold plain rows of pages, against the integer
-oracle: pages that are gone.  All outputs are whole numbers: equal."""
+oracle: pages that are gone, lengths beyond the table.  All outputs are whole numbers: equal."""
 from __future__ import annotations
 
 import random
@@ -98,3 +98,14 @@ def test_tokens_of_a_gone_page_have_no_slot(marker):
 def test_gone_pages_at_random(S, W, page):
     check_plan(*(x := pool(S, W, page, S, kv_max=(W - 3) * page, q_max=3 * page, finished=0.1, free=2 * S,
                            markers=[-1, 1 << 26, -(1 << 26)], gone=0.3))[:5], page, x[5])
+
+
+# ------------------------------------------------------------------ lengths beyond the table
+def test_a_length_beyond_the_table_is_not_granted():
+    """Two columns of pages of 16.  A request whose length is past them is refused and keeps its
+    length, even without new tokens; at its end the pages of its row return."""
+    table = np.array([[0, 1], [2, 3], [4, 5], [6, 7]])
+    got = check_plan([33, 40, 100, 32], [0, 3, -1, 0], table, np.full(12, 8), [0, 4], 16, 8)
+    assert got[0].tolist() == [33, 40, 0, 32] and got[4].tolist() == [0, 0, 1, 1] and got[5].tolist() == [0, 6]
+    assert (got[2] == -1).all()
+    check_plan([2 ** 31 - 1, 5], [2 ** 31 - 1, 1], table[:2], np.full(12, 8), [3, 4], 16, 8)
