@@ -49,7 +49,6 @@ gdr_status_t check_staged(int BH, int T, int dk, int dv, int chunk) {
 }
 
 // ---- the 8-bit paged cache ----
-constexpr int kMaxRequests = 8192;
 bool page_ok(int page) { return page == 16 || page == 32 || page == 64 || page == 128; }
 bool fits31(int64_t a, int64_t b) { return a * b <= 0x7fffffff; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
@@ -61,7 +60,7 @@ bool kv8_shape_ok(int Hkv, int D, int page, int num_pages, gdr_dtype_t dtype, gd
            fits31((int64_t)num_pages * Hkv, page);
 }
 bool kv8_heads_ok(int Hq, int Hkv, int total_q, int S) {
-    return Hq <= 65536 && Hkv <= 4096 && S <= kMaxRequests && fits31(total_q, Hq);
+    return Hq <= 65536 && Hkv <= 4096 && S <= gdr::kMaxRequests && fits31(total_q, Hq);
 }
 // A row of H heads of D values, `stride` elements from the next one, 16-byte aligned.
 bool row_stride_ok(int64_t stride, int H, int D, int esz) {
@@ -717,7 +716,7 @@ gdr_status_t gdr_page_plan(const int *kv_len, const int *q_len, int *block_table
                            int *positions, int *granted, int *free_state_out, int S,
                            int table_width, int page, int num_pages, int max_tokens, void *stream) {
     if (S < 0 || table_width <= 0 || num_pages <= 0 || max_tokens < 0) return GDR_ERR_INVALID_ARG;
-    if (!page_ok(page) || S > kMaxRequests || max_tokens > (1 << 30) ||
+    if (!page_ok(page) || S > gdr::kMaxRequests || max_tokens > (1 << 30) ||
         !fits31(num_pages, page) || !fits31(table_width, page) || !fits31(S, table_width))
         return GDR_ERR_UNSUPPORTED;
     if (!free_ring || !free_state || !cu_q || !free_state_out || free_state == free_state_out)

@@ -188,6 +188,7 @@ cudaError_t take_mla_error_word(unsigned *value);
 
 // ---- the 8-bit paged cache: plan (gdr_page.cu), append (gdr_kv8_append.cu), attention
 // (gdr_kv8_attn.cu); arguments as in include/gdr.h, N = num_pages, W = table_width ----
+constexpr int kMaxRequests = 8192;
 size_t page_plan_smem(int S);
 cudaError_t launch_page_plan(const int *kv_len, const int *q_len, int *table, int *ring,
                              const int *free_state, int *kv_out, int *cu_q, int *slots, int *positions,

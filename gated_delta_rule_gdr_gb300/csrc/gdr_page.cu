@@ -298,8 +298,9 @@ cudaError_t launch_page_plan(const int *kv_len, const int *q_len, int *table, in
                      state_out, S, W, page, N, max_tokens, cluster};
     const size_t smem = page_plan_smem(S);
     if (smem > 48 * 1024) {
+        // the limit is the kernel's, on every thread: always what the largest batch needs
         cudaError_t e = cudaFuncSetAttribute(page_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem);
+                                             (int)page_plan_smem(kMaxRequests));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

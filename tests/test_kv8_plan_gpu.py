@@ -3,6 +3,7 @@ oracle: pages that are gone, lengths beyond the table.  All outputs are whole nu
 from __future__ import annotations
 
 import random
+import threading
 
 import numpy as np
 import pytest
@@ -109,3 +110,32 @@ def test_a_length_beyond_the_table_is_not_granted():
     assert got[0].tolist() == [33, 40, 0, 32] and got[4].tolist() == [0, 0, 1, 1] and got[5].tolist() == [0, 6]
     assert (got[2] == -1).all()
     check_plan([2 ** 31 - 1, 5], [2 ** 31 - 1, 1], table[:2], np.full(12, 8), [3, 4], 16, 8)
+
+
+# ------------------------------------------------------------------ calls of several threads
+def test_threads_plan_batches_of_different_sizes():
+    """A launch's shared-memory limit belongs to the kernel, not to the call: one thread's small
+    batch does not take it from another's large one."""
+    lib, codes = gdr.load(), set()
+
+    def work(S):
+        z = torch.zeros(S, dtype=torch.int32, device="cuda")
+        table, ring = torch.full((S, 1), -1, dtype=torch.int32, device="cuda"), i32([0, 1])
+        out = [torch.zeros(S + 8, dtype=torch.int32, device="cuda") for _ in range(4)]
+        state, stream = i32([0, 2]), torch.cuda.Stream()
+        ptr = [t.data_ptr() for t in (z, z, table, ring, state, out[0], out[1], z, z, out[2], out[3])]
+        torch.cuda.synchronize()
+        start.wait()
+        for i in range(4000):
+            codes.add(lib.gdr_page_plan(*ptr, S, 1, 16, 2, 0, stream.cuda_stream))
+            if i % 500 == 0:
+                stream.synchronize()
+        stream.synchronize()
+
+    start = threading.Barrier(2)
+    threads = [threading.Thread(target=work, args=(S,)) for S in (8192, 2000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert codes == {0}
