@@ -101,6 +101,7 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         "gdr_set_option": [i, ctypes.c_int64],
         "gdr_mla_decode": [vp, vp, vp, vp, vp, f, vp, i, i, i, i, i, vp, sz, vp],
         "gdr_page_plan": [vp] * 11 + [i] * 5 + [vp],
+        "gdr_page_plan_ex": [vp] * 13 + [i] * 5 + [vp],
         "gdr_kv8_append": [vp, vp, i64, i64, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp],
         "gdr_kv8_attn": [vp, i64, vp, vp, vp, vp, vp, vp, vp, f, vp, vp] + [i] * 11 + [vp, sz, vp],
     }
@@ -620,11 +621,13 @@ def _kv8_cache(k_cache, v_cache, k_scale, v_scale):
     return code, shape
 
 
-def page_plan(kv_len, q_len, block_table, free_ring, free_state, page: int, max_tokens: int):
+def page_plan(kv_len, q_len, block_table, free_ring, free_state, page: int, max_tokens: int, held=None):
     """Places for the new tokens of a step, on the device.  kv_len, q_len [S] (q_len < 0:
     finished), block_table [S,W], free_ring [num_pages], free_state [2] = (head, count), all
     int32; block_table and free_ring are updated in place.  Returns int32 (kv_len_out [S],
-    cu_q [S+1], slots [max_tokens], positions [max_tokens], granted [S], free_state_out [2])."""
+    cu_q [S+1], slots [max_tokens], positions [max_tokens], granted [S], free_state_out [2]).
+    held [S] int32: the pages that each request's row has, where tokens may have been taken back
+    (kv_len lowered after refused drafts); held_out [S], the next call's, is then returned too."""
     lib = _lib or load()
     S, W = block_table.shape
     n, dev = int(max_tokens), block_table.device
@@ -632,14 +635,18 @@ def page_plan(kv_len, q_len, block_table, free_ring, free_state, page: int, max_
     kv, granted = empty(S, dtype=i32, device=dev), empty(S, dtype=i32, device=dev)
     slots, positions = empty(n, dtype=i32, device=dev), empty(n, dtype=i32, device=dev)
     cu, st = empty(S + 1, dtype=i32, device=dev), empty(2, dtype=i32, device=dev)
-    code = lib.gdr_page_plan(_int(kv_len, "kv_len", (S,)), _int(q_len, "q_len", (S,)),
-                             _int(block_table, "block_table"), _int(free_ring, "free_ring"),
-                             _int(free_state, "free_state", (2,)), kv.data_ptr(), cu.data_ptr(),
-                             slots.data_ptr(), positions.data_ptr(), granted.data_ptr(),
-                             st.data_ptr(), S, W, page, free_ring.numel(), n, _raw_stream(dev.index))
+    held_out = None if held is None else empty(S, dtype=i32, device=dev)
+    code = lib.gdr_page_plan_ex(_int(kv_len, "kv_len", (S,)), _int(q_len, "q_len", (S,)),
+                                None if held is None else _int(held, "held", (S,)),
+                                _int(block_table, "block_table"), _int(free_ring, "free_ring"),
+                                _int(free_state, "free_state", (2,)), kv.data_ptr(), cu.data_ptr(),
+                                slots.data_ptr(), positions.data_ptr(), granted.data_ptr(),
+                                None if held is None else held_out.data_ptr(), st.data_ptr(), S, W, page,
+                                free_ring.numel(), n, _raw_stream(dev.index))
     if code:
         raise GdrError(code, "gdr_page_plan")
-    return kv, cu, slots, positions, granted, st
+    out = kv, cu, slots, positions, granted, st
+    return out if held is None else (*out, held_out)
 
 
 def kv8_append(k, v, slots, k_cache, v_cache, k_scale, v_scale) -> None:

@@ -711,10 +711,10 @@ gdr_status_t gdr_mla_decode(const void *q_abs, const void *ckv, const int *seqle
 
 // ---- the 8-bit paged cache ----
 
-gdr_status_t gdr_page_plan(const int *kv_len, const int *q_len, int *block_table, int *free_ring,
-                           const int *free_state, int *kv_len_out, int *cu_q, int *slots,
-                           int *positions, int *granted, int *free_state_out, int S,
-                           int table_width, int page, int num_pages, int max_tokens, void *stream) {
+gdr_status_t gdr_page_plan_ex(const int *kv_len, const int *q_len, const int *held, int *block_table,
+                              int *free_ring, const int *free_state, int *kv_len_out, int *cu_q, int *slots,
+                              int *positions, int *granted, int *held_out, int *free_state_out, int S,
+                              int table_width, int page, int num_pages, int max_tokens, void *stream) {
     if (S < 0 || table_width <= 0 || num_pages <= 0 || max_tokens < 0) return GDR_ERR_INVALID_ARG;
     if (!page_ok(page) || S > gdr::kMaxRequests || max_tokens > (1 << 30) ||
         !fits31(num_pages, page) || !fits31(table_width, page) || !fits31(S, table_width))
@@ -724,10 +724,21 @@ gdr_status_t gdr_page_plan(const int *kv_len, const int *q_len, int *block_table
     if (S > 0 && (!kv_len || !q_len || !block_table || !kv_len_out || !granted ||
                   kv_len == kv_len_out || q_len == kv_len_out))
         return GDR_ERR_INVALID_ARG;
+    if (S > 0 && held && (!held_out || held == held_out || held == kv_len_out)) return GDR_ERR_INVALID_ARG;
     if (max_tokens > 0 && (!slots || !positions)) return GDR_ERR_INVALID_ARG;
-    return from_cuda(gdr::launch_page_plan(kv_len, q_len, block_table, free_ring, free_state, kv_len_out,
-                                           cu_q, slots, positions, granted, free_state_out, S, table_width,
-                                           page, num_pages, max_tokens, static_cast<cudaStream_t>(stream)));
+    return from_cuda(gdr::launch_page_plan(kv_len, q_len, held, block_table, free_ring, free_state, kv_len_out,
+                                           cu_q, slots, positions, granted, held_out, free_state_out, S,
+                                           table_width, page, num_pages, max_tokens,
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+gdr_status_t gdr_page_plan(const int *kv_len, const int *q_len, int *block_table, int *free_ring,
+                           const int *free_state, int *kv_len_out, int *cu_q, int *slots,
+                           int *positions, int *granted, int *free_state_out, int S,
+                           int table_width, int page, int num_pages, int max_tokens, void *stream) {
+    return gdr_page_plan_ex(kv_len, q_len, nullptr, block_table, free_ring, free_state, kv_len_out, cu_q, slots,
+                            positions, granted, nullptr, free_state_out, S, table_width, page, num_pages,
+                            max_tokens, stream);
 }
 
 gdr_status_t gdr_kv8_append(const void *k, const void *v, int64_t k_stride, int64_t v_stride,

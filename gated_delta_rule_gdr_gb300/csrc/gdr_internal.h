@@ -190,9 +190,9 @@ cudaError_t take_mla_error_word(unsigned *value);
 // (gdr_kv8_attn.cu); arguments as in include/gdr.h, N = num_pages, W = table_width ----
 constexpr int kMaxRequests = 8192;
 size_t page_plan_smem(int S);
-cudaError_t launch_page_plan(const int *kv_len, const int *q_len, int *table, int *ring,
+cudaError_t launch_page_plan(const int *kv_len, const int *q_len, const int *held, int *table, int *ring,
                              const int *free_state, int *kv_out, int *cu_q, int *slots, int *positions,
-                             int *granted, int *state_out, int S, int W, int page, int N, int max_tokens,
+                             int *granted, int *held_out, int *state_out, int S, int W, int page, int N, int max_tokens,
                              cudaStream_t s);
 cudaError_t launch_kv8_append(const void *k, const void *v, int64_t k_stride, int64_t v_stride,
                               const int *slots, void *k_cache, void *v_cache, float *k_scale,

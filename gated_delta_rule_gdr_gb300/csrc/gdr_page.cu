@@ -2,7 +2,9 @@
 // requests' lengths (gdr_page_plan).
 //
 // kv_s tokens cached, n_s new ones (n_s < 0: finished), pages of P tokens, W table columns:
-//   old_s  = ceil(kv_s / P), at most W,  need_s = ceil((kv_s + n_s) / P) - old_s
+//   old_s  = ceil(kv_s / P), or the pages held_s that its row has where that is more (tokens
+//            were taken back), at most W
+//   need_s = max(0, ceil((kv_s + n_s) / P) - old_s)
 //   a request fits if kv_s + n_s <= W P and its tokens end within max_tokens; it is granted
 //   if it fits and needs no page, or the fitting requests up to and including it need at
 //   most `count` pages -- so the grant depends on the order of the requests alone
@@ -76,8 +78,8 @@ __device__ __forceinline__ int find_request(const int *prefix, int S, int i) {
 }
 
 struct PlanArgs {
-    const int *kv_len, *q_len, *free_state;
-    int *table, *ring, *kv_out, *cu_q, *slots, *positions, *granted, *state_out;
+    const int *kv_len, *q_len, *held, *free_state;
+    int *table, *ring, *kv_out, *cu_q, *slots, *positions, *granted, *held_out, *state_out;
     int S, W, page, N, max_tokens;
     int cluster;      // CTAs of the launch's clusters
 };
@@ -99,7 +101,10 @@ __global__ void __launch_bounds__(PT) page_plan_kernel(const PlanArgs a) {
     const int count = min(max(a.free_state[1], 0), a.N);
     const int head = (int)((unsigned)a.free_state[0] % (unsigned)a.N);
     auto kv_of = [&](int s) { return max(a.kv_len[s], 0); };
-    auto pages_of = [&](int kv) { return (min(kv, room) + P - 1) >> shift; };     // that its row has
+    auto pages_of = [&](int s, int kv) {        // that its row has
+        const int least = (min(kv, room) + P - 1) >> shift;
+        return a.held ? min(max(a.held[s], least), a.W) : least;
+    };
 
     int64_t sum = 0, all;
     for (int s = s0; s < s1; ++s) sum += max(a.q_len[s], 0);
@@ -107,12 +112,12 @@ __global__ void __launch_bounds__(PT) page_plan_kernel(const PlanArgs a) {
     int need = 0;
     int64_t fin = 0;                  // finished requests with pages << 32 | chunks of their entries
     for (int s = s0; s < s1; ++s) {
-        const int kv = kv_of(s), n = a.q_len[s], old = pages_of(kv);
+        const int kv = kv_of(s), n = a.q_len[s], old = pages_of(s, kv);
         s_cu[s] = (int)min(at, (int64_t)a.max_tokens);
         at += max(n, 0);
         // -1: does not fit
         int x = -1;
-        if (n >= 0 && (int64_t)kv + n <= room && at <= a.max_tokens) x = ((kv + n + P - 1) >> shift) - old;
+        if (n >= 0 && (int64_t)kv + n <= room && at <= a.max_tokens) x = max(((kv + n + P - 1) >> shift) - old, 0);
         s_need[s] = x;
         need += max(x, 0);
         if (n < 0 && old > 0) fin += (1ll << 32) + (old + CHUNK - 1) / CHUNK;
@@ -132,7 +137,7 @@ __global__ void __launch_bounds__(PT) page_plan_kernel(const PlanArgs a) {
         s_need[s] = min(b_need, count);
         if (x > 0 && ok) last = upto;
         b_need = upto;
-        const int kv = kv_of(s), n = a.q_len[s], old = pages_of(kv);
+        const int kv = kv_of(s), n = a.q_len[s], old = pages_of(s, kv);
         if (n < 0 && old > 0) {
             s_fin[b_fin >> 32] = s;
             s_chunk[b_fin >> 32] = (int)b_fin;
@@ -144,6 +149,7 @@ __global__ void __launch_bounds__(PT) page_plan_kernel(const PlanArgs a) {
             a.granted[s] = ok ? 1 : 0;
             a.kv_out[s] = n < 0 ? 0 : (ok ? kv + n : kv);
             a.cu_q[s] = s_cu[s];
+            if (a.held) a.held_out[s] = n < 0 ? 0 : old + (ok ? max(x, 0) : 0);
         }
     }
     // pages granted in all: the largest prefix that a granted request reaches
@@ -163,9 +169,9 @@ __global__ void __launch_bounds__(PT) page_plan_kernel(const PlanArgs a) {
     __syncthreads();
 
     // A request's need and grant, from its own lengths and the prefix before it.
-    auto granted_pages = [&](int s, int kv, int n, int end) {   // -1: not granted
+    auto granted_pages = [&](int s, int kv, int n, int old, int end) {   // -1: not granted
         if (n < 0 || (int64_t)kv + n > room || end > a.max_tokens) return -1;
-        const int x = ((kv + n + P - 1) >> shift) - pages_of(kv);
+        const int x = max(((kv + n + P - 1) >> shift) - old, 0);
         return x == 0 || s_need[s] + x <= taken ? x : -1;
     };
     const int stride = gridDim.x * PT, first = blockIdx.x * PT + tid;
@@ -174,10 +180,10 @@ __global__ void __launch_bounds__(PT) page_plan_kernel(const PlanArgs a) {
         int slot = -1, pos = -1;
         if (t < tokens) {
             const int s = find_request(s_cu, S, t);
-            const int kv = kv_of(s), n = a.q_len[s], old = pages_of(kv);
+            const int kv = kv_of(s), n = a.q_len[s], old = pages_of(s, kv);
             // the end of the request's tokens: a saturated prefix means it does not fit
             const int64_t end = (int64_t)s_cu[s] + n;
-            if (granted_pages(s, kv, n, (int)min(end, (int64_t)a.max_tokens + 1)) >= 0) {
+            if (granted_pages(s, kv, n, old, (int)min(end, (int64_t)a.max_tokens + 1)) >= 0) {
                 const int at = kv + (t - s_cu[s]), p = at >> shift;
                 const int page = p < old ? a.table[(int64_t)s * a.W + p]
                                          : a.ring[((int64_t)head + s_need[s] + (p - old)) % a.N];
@@ -192,7 +198,7 @@ __global__ void __launch_bounds__(PT) page_plan_kernel(const PlanArgs a) {
     }
     for (int i = first; i < taken; i += stride) {
         const int s = find_request(s_need, S, i);
-        const int old = pages_of(kv_of(s));
+        const int old = pages_of(s, kv_of(s));
         a.table[(int64_t)s * a.W + old + (i - s_need[s])] = a.ring[((int64_t)head + i) % a.N];
     }
 
@@ -285,17 +291,17 @@ __global__ void __launch_bounds__(PT) page_plan_kernel(const PlanArgs a) {
 
 size_t page_plan_smem(int S) { return ((size_t)7 * S + 4) * sizeof(int); }
 
-cudaError_t launch_page_plan(const int *kv_len, const int *q_len, int *table, int *ring,
+cudaError_t launch_page_plan(const int *kv_len, const int *q_len, const int *held, int *table, int *ring,
                              const int *free_state, int *kv_out, int *cu_q, int *slots, int *positions,
-                             int *granted, int *state_out, int S, int W, int page, int N, int max_tokens,
+                             int *granted, int *held_out, int *state_out, int S, int W, int page, int N, int max_tokens,
                              cudaStream_t s) {
     // about four tokens or requests a thread: the scans repeat in every CTA, so more CTAs cost nothing
     const int64_t items = (int64_t)max_tokens + 16ll * S;
     int64_t blocks = std::min(std::max((items + 4 * PT - 1) / (4 * PT), (int64_t)1), (int64_t)304);
     const int cluster = (int64_t)S * W >= kClusterEntries ? 8 : 1;
     blocks = (blocks + cluster - 1) / cluster * cluster;
-    const PlanArgs a{kv_len, q_len, free_state, table, ring, kv_out, cu_q, slots, positions, granted,
-                     state_out, S, W, page, N, max_tokens, cluster};
+    const PlanArgs a{kv_len, q_len, held, free_state, table, ring, kv_out, cu_q, slots, positions, granted,
+                     held_out, state_out, S, W, page, N, max_tokens, cluster};
     const size_t smem = page_plan_smem(S);
     if (smem > 48 * 1024) {
         // the limit is the kernel's, on every thread: always what the largest batch needs

@@ -571,6 +571,21 @@ gdr_status_t gdr_page_plan(const int *kv_len, const int *q_len, int *block_table
                            int table_width, int page, int num_pages, int max_tokens, void *stream);
 
 /*
+ * The same for requests that may hold more pages than their length needs: where drafted tokens
+ * were refused, the caller lowers kv_len and the pages that they had stay with the request.
+ * gdr_page_plan would take new ones over their table entries and lose them.
+ *   held      [S] pages that each row of block_table has (less than ceil(kv_len / page) counts
+ *                 as that, more than table_width as table_width); NULL: as gdr_page_plan.  Only
+ *                 pages past these are taken, and a finished request gives all of them back
+ *   held_out  [S] the same after the call, 0 for a finished request: the next call's `held`.
+ *                 Must not be held itself (nor kv_len_out be held); not written if held is NULL
+ */
+gdr_status_t gdr_page_plan_ex(const int *kv_len, const int *q_len, const int *held, int *block_table,
+                              int *free_ring, const int *free_state, int *kv_len_out, int *cu_q, int *slots,
+                              int *positions, int *granted, int *held_out, int *free_state_out, int S,
+                              int table_width, int page, int num_pages, int max_tokens, void *stream);
+
+/*
  * Quantises T tokens' keys and values into the cache.
  *   k, v      [T][Hkv][D] dtype, k_stride / v_stride elements between tokens (at least
  *             Hkv * D; rows 16-byte aligned)

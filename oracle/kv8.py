@@ -51,18 +51,21 @@ def scale_for(amax: float, kv: str) -> float:
     return 2.0 ** e
 
 
-def plan(kv_len, q_len, table, ring, state, page, max_tokens):
-    """Returns (kv_out, cu, slots, positions, granted, state_out, table, ring)."""
+def plan(kv_len, q_len, table, ring, state, page, max_tokens, held=None):
+    """Returns (kv_out, cu, slots, positions, granted, state_out, table, ring), and the pages each
+    row has afterwards if `held` says how many it had."""
     table, ring = np.array(table), np.array(ring)
     S, W = table.shape
     N = len(ring)
     head, count = int(state[0]), int(state[1])
-    kv_out, cu, granted = [], [0], []
+    kv_out, cu, granted, held_out = [], [0], [], []
     slots, pos = np.full(max_tokens, -1, np.int64), np.full(max_tokens, -1, np.int64)
     tok = taken = back = want = 0
     for s in range(S):
         kv, n = int(kv_len[s]), int(q_len[s])
         old = min(-(-kv // page), W)
+        if held is not None:
+            old = min(max(old, int(held[s])), W)
         if n < 0:
             for i in range(old):
                 if 0 <= table[s, i] < N:             # else a page that is gone
@@ -70,8 +73,9 @@ def plan(kv_len, q_len, table, ring, state, page, max_tokens):
                     back += 1
             kv_out.append(0)
             granted.append(1)
+            held_out.append(0)
         else:
-            new = -(-(kv + n) // page)
+            new = max(old, -(-(kv + n) // page))
             fits = kv + n <= W * page and tok + n <= max_tokens
             if fits:
                 want += new - old
@@ -88,8 +92,10 @@ def plan(kv_len, q_len, table, ring, state, page, max_tokens):
             tok += n
             kv_out.append(kv + n if ok else kv)
             granted.append(int(ok))
+            held_out.append(new if ok else old)
         cu.append(min(tok, max_tokens))
-    return kv_out, cu, slots, pos, granted, [(head + taken) % N, count - taken + back], table, ring
+    out = kv_out, cu, slots, pos, granted, [(head + taken) % N, count - taken + back], table, ring
+    return out if held is None else (*out, held_out)
 
 
 def append(x, slots, codes, scale, page, kv):

@@ -1,5 +1,6 @@
 """gdr_page_plan on the GPU where requests do not hold plain rows of pages, against the integer
-oracle: pages that are gone, lengths beyond the table.  All outputs are whole numbers: equal."""
+oracle: pages that are gone, lengths beyond the table, pages held beyond the length.  All
+outputs are whole numbers: equal."""
 from __future__ import annotations
 
 import random
@@ -139,3 +140,59 @@ def test_threads_plan_batches_of_different_sizes():
     for t in threads:
         t.join()
     assert codes == {0}
+
+
+# ------------------------------------------------------------------ pages held beyond the length
+def test_refused_drafts_keep_their_pages():
+    """15 tokens in pages of 16 and three drafts a step that are refused each time: the page that
+    the first drafts crossed into stays the request's, and returns at its end."""
+    kv, held, state = i32([15]), i32([1]), i32([0, 3])
+    table, ring = i32([[3, -1, -1]]), i32([0, 1, 2, -1])
+    for _ in range(5):
+        out = gdr.page_plan(kv, i32([3]), table, ring, state, 16, 3, held)
+        assert out[0].tolist() == [18] and out[2].tolist() == [63, 0, 1] and out[4].tolist() == [1]
+        state, held = out[5], out[6]
+        assert state.tolist() == [1, 2] and held.tolist() == [2] and table.tolist() == [[3, 0, -1]]
+    out = gdr.page_plan(kv, i32([-1]), table, ring, state, 16, 3, held)
+    assert out[5].tolist() == [1, 4] and out[6].tolist() == [0] and ring.tolist() == [0, 1, 2, 3]
+
+
+@pytest.mark.parametrize("S,W,page,seed", [(1, 9, 16, 1), (40, 30, 16, 2), (300, 40, 32, 3), (1300, 16, 128, 4), (270, 2000, 16, 5)])
+def test_held_pages_equal_oracle(S, W, page, seed):
+    r = random.Random(seed)
+    used, kv, q, held = 0, [], [], []
+    for _ in range(S):
+        has = r.randint(0, min(W, 60))
+        kv.append(r.randint(0, has * page) if r.random() < 0.9 else W * page + 3)
+        held.append(has if r.random() < 0.9 else r.choice([0, W + 5, -4]))
+        q.append(-1 if r.random() < 0.2 else r.randint(0, 4 * page))
+        used += W
+    N = used + 2 * S
+    perm = r.sample(range(N), N)
+    table, ring, head = np.array(perm[:used]).reshape(S, W), np.full(N, -3), r.randrange(N)
+    for i, p in enumerate(perm[used:]):
+        ring[(head + i) % N] = p
+    T = sum(n for n in q if n > 0)
+    t, g = i32(table), i32(ring)
+    got = gdr.page_plan(i32(kv), i32(q), t, g, i32([head, 2 * S]), page, T, i32(held))
+    want = O.plan(kv, q, table, ring, [head, 2 * S], page, T, held)
+    for a, b, name in zip((*got[:6], t, g, got[6]), want, (*NAMES, "held")):
+        assert np.array_equal(a.cpu().numpy(), np.asarray(b)), name
+
+
+def test_no_page_is_lost_while_drafts_are_refused():
+    """Forty steps of twenty requests that draft up to eight tokens, keep some, end and return:
+    the free pages and the held ones are all the pages, each once, after every step."""
+    r = random.Random(9)
+    S, W, page, N = 20, 12, 16, 150
+    kv, held, state = i32([0] * S), i32([0] * S), i32([5, N])
+    table, ring = torch.full((S, W), -1, dtype=torch.int32, device="cuda"), i32(r.sample(range(N), N))
+    for _ in range(40):
+        q = [-1 if r.random() < 0.06 else r.randint(0, 8) if r.random() < 0.8 else r.randint(0, 40) for _ in range(S)]
+        before = kv.tolist()
+        kv, _, _, _, ok, state, held = gdr.page_plan(kv, i32(q), table, ring, state, page, sum(n for n in q if n > 0), held)
+        h, (head, count) = held.tolist(), state.tolist()
+        pages = [p for s in range(S) for p in table[s, :h[s]].tolist()] + [ring[(head + i) % N].item() for i in range(count)]
+        assert sorted(pages) == list(range(N))
+        kept = [r.randint(b, max(a, b)) if n >= 0 else 0 for a, b, n in zip(kv.tolist(), before, q)]
+        kv = i32(kept)
