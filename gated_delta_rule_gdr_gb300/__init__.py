@@ -674,10 +674,11 @@ def kv8_attn_workspace_size(S, max_q, total_q, Hq, Hkv, D, dtype=torch.bfloat16)
 
 
 def kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, scale: float, *,
-             cu_q=None, max_q: int = 1, out=None, want_lse: bool = False, workspace=None):
+             cu_q=None, max_q: int = None, out=None, want_lse: bool = False, workspace=None):
     """Attention over the paged 8-bit cache.  q [total_q,Hq,D] fp32 or bf16 (tokens may be
     strided), block_table [S,W] and kv_len [S] int32, cu_q [S+1] int32 first query of each
-    request (None: one query a request), max_q the most queries of a request.  Query i of n
+    request (None: one query a request), max_q the most queries of a request (to be given with
+    cu_q: it chooses the kernel, and another value costs time).  Query i of n
     sees the first kv_len - n + 1 + i keys.  workspace: None (allocated here) or a uint8 CUDA
     tensor of kv8_attn_workspace_size bytes.  Returns out [total_q,Hq,D], or (out, lse
     [total_q,Hq] fp32) if want_lse."""
@@ -694,6 +695,12 @@ def kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, scale: 
     elif out.dtype is not dtype or out.shape != q.shape or not out.is_cuda or not out.is_contiguous():
         raise ValueError("out must be a contiguous CUDA tensor of q's shape and dtype")
     lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if want_lse else None
+    if max_q is None:
+        if cu_q is not None:
+            raise ValueError("cu_q wants max_q, the most queries of a request")
+        max_q = 1
+    elif max_q == 0:            # as a small one: what the lengths say is computed
+        max_q = 1
     el = DTYPE[dtype]
     need = lib.gdr_kv8_attn_workspace_size(S, max_q, T, Hq, Hkv, D, el)
     if workspace is None:

@@ -288,9 +288,11 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
 // us for the whole call against a warp that walks the parts of row after row), or one warp takes
 // RPW rows at once (many rows, few parts).  A lane weighs a part, then the lanes take the D
 // values: eight loads are in flight at once, since each is a trip to the L2.
-template <typename E, int D, int RB, int WPR, int RPW>
+// ROUND: the grid may be too small for the items and rows that there are (max_q says less than
+// the lengths do), and goes round; the loops cost up to 1 us (7 ragged fp32 requests: 22.1 and 23.4 us).
+template <typename E, int D, int RB, int WPR, int RPW, bool ROUND>
 __global__ void __launch_bounds__(256, 4) kv8_merge_kernel(const AttnArgs a) {
-    static_assert(WPR == 1 || RPW == 1, "");
+    static_assert(WPR == 1 ? !ROUND : RPW == 1, "");
     constexpr int VL = D / 32;
     __shared__ float s_o[WPR > 1 ? 8 : 1][D];
     __shared__ float s_l[8];
@@ -298,128 +300,148 @@ __global__ void __launch_bounds__(256, 4) kv8_merge_kernel(const AttnArgs a) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, w0 = warp / WPR * WPR;
     grid_dependency_wait();
     grid_launch_dependents();
-    // the item: of the CTA whose entry is the blockIdx.x-th that has one, 1024 entries at a time;
-    // with a CTA for every entry, its own
-    int c0 = gridDim.x == a.ctas ? (int)blockIdx.x : -1;
-    for (int base = 0, before = 0; base < a.ctas && c0 < 0; base += 1024) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int c = base + 256 * i + threadIdx.x;
-            const unsigned m = __ballot_sync(0xffffffffu, c < a.ctas && a.entry[min(c, a.ctas - 1)].x >= 0);
-            if (lane == 0) s_mask[8 * i + warp] = m;
-        }
-        __syncthreads();
-        int incl = __popc(s_mask[lane]);
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += y;
-        }
-        incl += before;
-        const unsigned past = __ballot_sync(0xffffffffu, incl > (int)blockIdx.x);
-        if (past) {
-            const int g = __ffs(past) - 1;
-            const unsigned m = s_mask[g];
-            const int k = (int)blockIdx.x - (__shfl_sync(0xffffffffu, incl, g) - __popc(m));
-            c0 = base + 32 * g + (int)__fns(m, 0, k + 1);
-        }
-        before = __shfl_sync(0xffffffffu, incl, 31);
-    }
-    if (c0 < 0) return;
-    const int4 en = a.entry[c0];
-    if (en.x < 0) return;
-    const Request r = request_of(a, en.y);
-    const int rows = min(RB, r.n * a.G - en.w * RB), parts = en.x - c0 + 1;
-    const int row0 = (blockIdx.y * (8 / WPR) + warp / WPR) * RPW;
-    if (row0 >= rows) return;        // (with WPR > 1 the whole CTA)
-    // row rr of part p; a row that is not there is read as the last one and not written
-    auto slot = [&](int p, int rr) { return ((int64_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * RB + min(row0 + rr, rows - 1); };
-    float ref[RPW], l[RPW], o[RPW][VL];
-    float2 ml[RPW];
-#pragma unroll
-    for (int rr = 0; rr < RPW; ++rr) {
-        ref[rr] = -INFINITY;
-        l[rr] = 0.f;
-#pragma unroll
-        for (int e = 0; e < VL; ++e) o[rr][e] = 0.f;
-    }
-    for (int p = lane; p - lane < parts; p += 32)
-#pragma unroll
-        for (int rr = 0; rr < RPW; ++rr) {
-            const float2 x = p < parts ? *reinterpret_cast<const float2 *>(a.part_ml + 2 * slot(p, rr)) : make_float2(-INFINITY, 0.f);
-            ref[rr] = fmaxf(ref[rr], x.x);
-            if (p == lane) ml[rr] = x;
-        }
-    float M[RPW];
-#pragma unroll
-    for (int rr = 0; rr < RPW; ++rr) {
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) ref[rr] = fmaxf(ref[rr], __shfl_xor_sync(0xffffffffu, ref[rr], off));
-        M[rr] = ref[rr] == -INFINITY ? 0.f : ref[rr];
-    }
-    const int per = (parts + WPR - 1) / WPR, end = min(parts, (warp - w0 + 1) * per);
-    for (int p0 = (warp - w0) * per; p0 < end; p0 += 32) {
-        const int n = min(32, end - p0);
-        float w[RPW];
-#pragma unroll
-        for (int rr = 0; rr < RPW; ++rr) {
-            if (p0 > 0) ml[rr] = *reinterpret_cast<const float2 *>(a.part_ml + 2 * slot(min(p0 + lane, parts - 1), rr));
-            // a part without an exponent weighs 0; if its sums are NaN (all its scores are) they stay NaN
-            w[rr] = part_weight(ml[rr].x, M[rr]);
-            if (lane < n) l[rr] = fmaf(w[rr], ml[rr].y, l[rr]);
-        }
-#pragma unroll(8 / RPW)
-        for (int j = 0; j < n; ++j)
+    bool again = false;
+    auto item = [&](int c0) {
+        const int4 en = a.entry[c0];
+        if (en.x < 0) return;
+        const Request r = request_of(a, en.y);
+        const int rows = min(RB, r.n * a.G - en.w * RB), parts = en.x - c0 + 1;
+        constexpr int STEP = 8 / WPR * RPW;
+#pragma unroll 1
+        for (int row0 = blockIdx.y * STEP + warp / WPR * RPW; row0 < rows; row0 += gridDim.y * STEP) {
+            // row rr of part p; a row that is not there is read as the last one and not written
+            auto slot = [&](int p, int rr) { return ((int64_t)(c0 + p) * 2 + (p == 0 ? 1 : 0)) * RB + min(row0 + rr, rows - 1); };
+            float ref[RPW], l[RPW], o[RPW][VL];
+            float2 ml[RPW];
 #pragma unroll
             for (int rr = 0; rr < RPW; ++rr) {
-                const float wj = __shfl_sync(0xffffffffu, w[rr], j);
-                const float *src = a.part_o + slot(p0 + j, rr) * D + lane * VL;
-                if constexpr (VL == 4) {
-                    const float4 x = *reinterpret_cast<const float4 *>(src);
-                    o[rr][0] = fmaf(wj, x.x, o[rr][0]), o[rr][1] = fmaf(wj, x.y, o[rr][1]);
-                    o[rr][VL - 2] = fmaf(wj, x.z, o[rr][VL - 2]), o[rr][VL - 1] = fmaf(wj, x.w, o[rr][VL - 1]);
-                } else {
-                    const float2 x = *reinterpret_cast<const float2 *>(src);
-                    o[rr][0] = fmaf(wj, x.x, o[rr][0]), o[rr][1] = fmaf(wj, x.y, o[rr][1]);
+                ref[rr] = -INFINITY;
+                l[rr] = 0.f;
+#pragma unroll
+                for (int e = 0; e < VL; ++e) o[rr][e] = 0.f;
+            }
+            for (int p = lane; p - lane < parts; p += 32)
+#pragma unroll
+                for (int rr = 0; rr < RPW; ++rr) {
+                    const float2 x = p < parts ? *reinterpret_cast<const float2 *>(a.part_ml + 2 * slot(p, rr)) : make_float2(-INFINITY, 0.f);
+                    ref[rr] = fmaxf(ref[rr], x.x);
+                    if (p == lane) ml[rr] = x;
+                }
+            float M[RPW];
+#pragma unroll
+            for (int rr = 0; rr < RPW; ++rr) {
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) ref[rr] = fmaxf(ref[rr], __shfl_xor_sync(0xffffffffu, ref[rr], off));
+                M[rr] = ref[rr] == -INFINITY ? 0.f : ref[rr];
+            }
+            const int per = (parts + WPR - 1) / WPR, end = min(parts, (warp - w0 + 1) * per);
+            for (int p0 = (warp - w0) * per; p0 < end; p0 += 32) {
+                const int n = min(32, end - p0);
+                float w[RPW];
+#pragma unroll
+                for (int rr = 0; rr < RPW; ++rr) {
+                    if (p0 > 0) ml[rr] = *reinterpret_cast<const float2 *>(a.part_ml + 2 * slot(min(p0 + lane, parts - 1), rr));
+                    // a part without an exponent weighs 0; if its sums are NaN (all its scores are) they stay NaN
+                    w[rr] = part_weight(ml[rr].x, M[rr]);
+                    if (lane < n) l[rr] = fmaf(w[rr], ml[rr].y, l[rr]);
+                }
+#pragma unroll(8 / RPW)
+                for (int j = 0; j < n; ++j)
+#pragma unroll
+                    for (int rr = 0; rr < RPW; ++rr) {
+                        const float wj = __shfl_sync(0xffffffffu, w[rr], j);
+                        const float *src = a.part_o + slot(p0 + j, rr) * D + lane * VL;
+                        if constexpr (VL == 4) {
+                            const float4 x = *reinterpret_cast<const float4 *>(src);
+                            o[rr][0] = fmaf(wj, x.x, o[rr][0]), o[rr][1] = fmaf(wj, x.y, o[rr][1]);
+                            o[rr][VL - 2] = fmaf(wj, x.z, o[rr][VL - 2]), o[rr][VL - 1] = fmaf(wj, x.w, o[rr][VL - 1]);
+                        } else {
+                            const float2 x = *reinterpret_cast<const float2 *>(src);
+                            o[rr][0] = fmaf(wj, x.x, o[rr][0]), o[rr][1] = fmaf(wj, x.y, o[rr][1]);
+                        }
+                    }
+            }
+#pragma unroll
+            for (int rr = 0; rr < RPW; ++rr)
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], off);
+            if constexpr (WPR > 1) {
+                if (ROUND && again) __syncthreads();
+                again = true;
+                if (lane == 0) s_l[warp] = l[0];
+#pragma unroll
+                for (int e = 0; e < VL; ++e) s_o[warp][lane * VL + e] = o[0][e];
+                __syncthreads();
+                if (warp != w0) {
+                    if constexpr (ROUND) continue;
+                    return;
+                }
+                l[0] = 0.f;
+#pragma unroll
+                for (int w = 0; w < WPR; ++w) l[0] += s_l[w0 + w];
+#pragma unroll
+                for (int e = 0; e < VL; ++e) {
+                    o[0][e] = 0.f;
+#pragma unroll
+                    for (int w = 0; w < WPR; ++w) o[0][e] += s_o[w0 + w][lane * VL + e];
                 }
             }
-    }
 #pragma unroll
-    for (int rr = 0; rr < RPW; ++rr)
+            for (int rr = 0; rr < RPW; ++rr) {
+                const int row = row0 + rr, at = en.w * RB + row;
+                if (row >= rows) break;
+                const float inv = l[rr] == 0.f ? 0.f : 1.f / l[rr];
+                const int64_t orow = (int64_t)(r.q0 + at / a.G) * a.Hq + en.z * a.G + at % a.G;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) l[rr] += __shfl_xor_sync(0xffffffffu, l[rr], off);
-    if constexpr (WPR > 1) {
-        if (lane == 0) s_l[warp] = l[0];
-#pragma unroll
-        for (int e = 0; e < VL; ++e) s_o[warp][lane * VL + e] = o[0][e];
-        __syncthreads();
-        if (warp != w0) return;
-        l[0] = 0.f;
-#pragma unroll
-        for (int w = 0; w < WPR; ++w) l[0] += s_l[w0 + w];
-#pragma unroll
-        for (int e = 0; e < VL; ++e) {
-            o[0][e] = 0.f;
-#pragma unroll
-            for (int w = 0; w < WPR; ++w) o[0][e] += s_o[w0 + w][lane * VL + e];
+                for (int e = 0; e < VL; ++e) {
+                    if constexpr (sizeof(E) == 4)
+                        static_cast<float *>(a.out)[orow * D + lane * VL + e] = o[rr][e] * inv;
+                    else
+                        static_cast<__nv_bfloat16 *>(a.out)[orow * D + lane * VL + e] = __float2bfloat16_rn(o[rr][e] * inv);
+                }
+                if (a.lse && lane == 0)
+                    a.lse[orow] = l[rr] == 0.f ? -INFINITY : (M[rr] - kv8::kOff + log2f(l[rr])) * 0.693147180559945f;
+            }
+            if constexpr (!ROUND) return;
         }
-    }
+    };
+    // the blockIdx.x-th entry that has an item (ROUND: and every gridDim.x-th after it), 1024 entries
+    // at a time; with a CTA for every entry, its own
+    const bool own = gridDim.x == a.ctas;
+    for (int base = 0, before = 0, next = blockIdx.x; base < a.ctas; base += 1024) {
+        int incl = 0;
+        if (!own) {
+            __syncthreads();
 #pragma unroll
-    for (int rr = 0; rr < RPW; ++rr) {
-        const int row = row0 + rr, at = en.w * RB + row;
-        if (row >= rows) break;
-        const float inv = l[rr] == 0.f ? 0.f : 1.f / l[rr];
-        const int64_t orow = (int64_t)(r.q0 + at / a.G) * a.Hq + en.z * a.G + at % a.G;
+            for (int i = 0; i < 4; ++i) {
+                const int c = base + 256 * i + threadIdx.x;
+                const unsigned m = __ballot_sync(0xffffffffu, c < a.ctas && a.entry[min(c, a.ctas - 1)].x >= 0);
+                if (lane == 0) s_mask[8 * i + warp] = m;
+            }
+            __syncthreads();
+            incl = __popc(s_mask[lane]);
 #pragma unroll
-        for (int e = 0; e < VL; ++e) {
-            if constexpr (sizeof(E) == 4)
-                static_cast<float *>(a.out)[orow * D + lane * VL + e] = o[rr][e] * inv;
-            else
-                static_cast<__nv_bfloat16 *>(a.out)[orow * D + lane * VL + e] = __float2bfloat16_rn(o[rr][e] * inv);
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, incl, off);
+                if (lane >= off) incl += y;
+            }
+            incl += before;
         }
-        if (a.lse && lane == 0)
-            a.lse[orow] = l[rr] == 0.f ? -INFINITY : (M[rr] - kv8::kOff + log2f(l[rr])) * 0.693147180559945f;
+#pragma unroll 1
+        while (true) {
+            int c0 = next;
+            if (!own) {
+                const unsigned past = __ballot_sync(0xffffffffu, incl > next);
+                if (past == 0) break;
+                const int g = __ffs(past) - 1;
+                const unsigned m = s_mask[g];
+                c0 = base + 32 * g + (int)__fns(m, 0, next - (__shfl_sync(0xffffffffu, incl, g) - __popc(m)) + 1);
+            }
+            item(c0);
+            if (own || !ROUND) return;
+            next += gridDim.x;
+        }
+        before = __shfl_sync(0xffffffffu, incl, 31);
     }
 }
 
@@ -441,17 +463,23 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t sm
 }
 // CTAs for as many items as can be divided among the attention's `a.ctas` (each at most one, and
 // there are no more than the requests' blocks of rows), or for every entry where that is not
-// much more: looking for the item takes 1.5 us.
+// much more: looking for the item takes 1.5 us.  `rows` goes by max_q; where the lengths could be
+// more than that, the wide form goes round and the other has CTAs for what they could be.
 template <typename E, int D, int RB>
 cudaError_t launch_merge(const AttnArgs &a, int64_t rows, cudaStream_t s) {
     constexpr int RPW = RB >= 16 ? 2 : 1;
-    const int64_t most = std::min(rows, (int64_t)RB);
-    const int64_t blocks = std::min((int64_t)a.S * ((rows + RB - 1) / RB), (int64_t)a.total_q * a.G / RB + a.S);
+    const int64_t all = (int64_t)a.total_q * a.G;      // rows of all requests
+    const int64_t most = std::min(rows, (int64_t)RB), could = std::min(all, (int64_t)RB);
+    const int64_t limit = (all + (int64_t)a.S * (RB - 1)) / RB, blocks = std::min((int64_t)a.S * ((rows + RB - 1) / RB), limit);
     const int64_t items = 2 * blocks * a.Hkv < a.ctas ? blocks * a.Hkv : a.ctas;
-    if (items * most <= kv8::kMergeWide)
-        return launch_after(kv8_merge_kernel<E, D, RB, 8, 1>, dim3((unsigned)items, (unsigned)most), 256, 0, s, a);
-    return launch_after(kv8_merge_kernel<E, D, RB, 1, RPW>, dim3((unsigned)items, (unsigned)((most + 8 * RPW - 1) / (8 * RPW))),
-                        256, 0, s, a);
+    const bool every = items == a.ctas || blocks == limit;
+    const unsigned x = (unsigned)items, all_x = (unsigned)std::min(limit * a.Hkv, (int64_t)a.ctas);
+    const unsigned wide = (unsigned)most, y = (unsigned)((could + 8 * RPW - 1) / (8 * RPW));
+    if (items * most <= kv8::kMergeWide) {
+        if (every && most == could) return launch_after(kv8_merge_kernel<E, D, RB, 8, 1, false>, dim3(x, wide), 256, 0, s, a);
+        return launch_after(kv8_merge_kernel<E, D, RB, 8, 1, true>, dim3(x, wide), 256, 0, s, a);
+    }
+    return launch_after(kv8_merge_kernel<E, D, RB, 1, RPW, false>, dim3(every ? x : all_x, y), 256, 0, s, a);
 }
 
 // Entries, then {M, l}, then the sums.

@@ -612,8 +612,9 @@ gdr_status_t gdr_kv8_append(const void *k, const void *v, int64_t k_stride, int6
  *   kv_len    [S] tokens cached, the new ones included (at most table_width * page)
  *   cu_q      [S+1] first query of each request, cu_q[0] = 0, cu_q[S] <= total_q; or NULL:
  *             one query a request (max_q = 1, total_q = S)
- *   max_q     the most queries any request has, or more: it chooses the kernel, and a larger
- *             one changes a result by rounding only.  Below that the result is undefined
+ *   max_q     the most queries any request has: it chooses the kernel.  Another value, a smaller
+ *             one too, costs time and changes a result by rounding only (0: there are no
+ *             queries, nothing is written)
  *   scale     score scale, for example 1 / sqrt(D)
  *   out       [total_q][Hq][D] dtype;  lse [total_q][Hq] fp32 or NULL
  * Query i of a request with n queries and kv tokens sees keys j <= kv - n + i whose page is

@@ -1,0 +1,96 @@
+"""kv8_attn on the GPU, row by row: a row's result depends on no other row, on no bound that the
+caller gives for the lengths, and holds where the largest weight's value is nothing.
+
+Tolerances.  A bf16 output is rounded once (uniform in half a unit of the last of 8 bits: at
+most 2^-7 / sqrt(12) = 2.26e-3 in relative L2) and its weights to 11 bits (at most 2^-11): 3e-3,
+of every row; fp32: 1e-5, the library's."""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import gated_delta_rule_gdr_gb300 as gdr
+import oracle
+from oracle import kv8 as O
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+TOL = {BF16: 3e-3, F32: 1e-5}
+CODE = {"e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    gdr.load(build_if_missing=True)
+    yield
+    assert gdr.last_device_error() == 0
+
+
+def i32(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def case(lens, qs, Hq, Hkv, D, page, dtype, kv, seed):
+    """Normal queries over caches of any codes but NaN; scores of standard deviation about 1."""
+    g = torch.Generator().manual_seed(seed)
+    need = [-(-n // page) for n in lens]
+    N = sum(need)
+    order, at = torch.randperm(N, generator=g).to(torch.int32), 0
+    table = torch.full((len(lens), max(need)), -1, dtype=torch.int32)
+    for s, n in enumerate(need):
+        table[s, :n] = order[at:at + n]
+        at += n
+    codes = []
+    for _ in range(2):
+        c = torch.randint(0, 256, (N, Hkv, page, D), dtype=torch.uint8, generator=g)
+        c[(c & 0x7f) == 0x7f] = 0x30
+        codes.append(c)
+    ks = torch.full((N, Hkv), 2.0 ** -6 if kv == "int8" else 2.0 ** -7)
+    vs = torch.exp2(torch.randint(-1, 2, (N, Hkv), generator=g).float())
+    return dict(q=torch.randn((sum(qs), Hq, D), generator=g).to(dtype), kc=codes[0], vc=codes[1], ks=ks, vs=vs,
+                table=table, lens=lens, cu=[sum(qs[:i]) for i in range(len(qs) + 1)], kv=kv, scale=1 / math.sqrt(D))
+
+
+def attend(x, **kw):
+    a = [x[n].cuda() for n in ("q", "kc", "vc", "ks", "vs", "table")]
+    a[1:3] = [t.view(CODE[x["kv"]]) for t in a[1:3]]
+    out = torch.full_like(a[0], math.nan)
+    return gdr.kv8_attn(*a, i32(x["lens"]), x["scale"], cu_q=i32(x["cu"]), want_lse=True, out=out, **kw)
+
+
+def want(x):
+    return O.attention(x["q"].double().numpy(), x["kc"].numpy(), x["vc"].numpy(), x["ks"].double().numpy(),
+                       x["vs"].double().numpy(), x["table"].numpy(), x["lens"], x["cu"], x["scale"], x["kv"])
+
+
+def worst_row(out, ref, keep=None):
+    a, b = out.double().cpu().numpy().reshape(-1, out.shape[-1]), ref.reshape(-1, out.shape[-1])
+    err = np.linalg.norm(a - b, axis=1) / np.maximum(np.linalg.norm(b, axis=1), 1e-300)
+    return float(err.max() if keep is None else err[keep.reshape(-1)].max())
+
+
+# ------------------------------------------------------------------ a small max_q
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("lens,qs,Hq,Hkv,max_q", [
+    ([4000], [5], 8, 1, 1),                       # items of 8 rows, five of them, all divided
+    ([3000, 2000, 1], [40, 7, 1], 4, 2, 1), ([5000, 300], [70, 30], 8, 2, 4), ([2500, 900], [90, 3], 8, 1, 3),
+    ([3000], [200], 8, 1, 8), ([4000, 128], [300, 128], 4, 1, 20), ([2000, 50], [5, 2], 16, 2, 0),
+    ([2000] * 50, [9] * 50, 8, 1, 1),
+])
+def test_a_small_max_q_costs_time_only(dtype, lens, qs, Hq, Hkv, max_q):
+    x = case(lens, qs, Hq, Hkv, 128, 16, dtype, "e4m3", 1)
+    out, lse = attend(x, max_q=max_q)
+    ro, rl = want(x)
+    assert worst_row(out, ro) <= TOL[dtype]
+    assert np.abs(lse.double().cpu().numpy() - rl).max() <= 1e-5 * max(1.0, np.abs(rl).max())
+
+
+def test_lengths_want_a_max_q():
+    x = case([40], [5], 2, 1, 64, 16, BF16, "int8", 2)
+    with pytest.raises(ValueError):
+        attend(x)
