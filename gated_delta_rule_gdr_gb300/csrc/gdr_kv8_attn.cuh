@@ -270,11 +270,12 @@ __device__ __forceinline__ float part_weight(float m, float ref) { return m == -
 
 // The power of two that brings a row of largest magnitude amax below 2^15, where a half
 // keeps 11 bits of everything that counts (bf16 values exactly, down to 2^-29 of the
-// largest); 1 for a row of zeros or with an infinity or NaN.
+// largest); 1 for a row of zeros.  With an infinity the least one, which leaves finite values
+// finite: they do not count beside it.
 __device__ __forceinline__ float row_factor(float amax) {
-    const int x = (int)(__float_as_uint(amax) >> 23) & 255;   // 2^(x - 127) <= amax
-    if (amax == 0.f || x == 255) return 1.f;
-    return __uint_as_float((uint32_t)(min(max(268 - x, 1), 254)) << 23);   // 2^(14 - (x - 127))
+    const int x = min((int)(__float_as_uint(amax) >> 23) & 255, 254);   // 2^(x - 127) <= amax
+    if (amax == 0.f) return 1.f;
+    return __uint_as_float((uint32_t)min(268 - x, 253) << 23);   // 2^(14 - (x - 127)); its inverse is normal
 }
 
 __device__ __forceinline__ uint32_t pack_h2(float a, float b) {

@@ -94,3 +94,20 @@ def test_lengths_want_a_max_q():
     x = case([40], [5], 2, 1, 64, 16, BF16, "int8", 2)
     with pytest.raises(ValueError):
         attend(x)
+
+
+# ------------------------------------------------------------------ rows far apart
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+@pytest.mark.parametrize("qs,Hq,Hkv,D", [([1, 1], 8, 1, 128), ([2, 2], 8, 1, 64), ([3, 5], 8, 1, 128), ([7, 6], 8, 1, 64),
+                                         ([13, 16], 8, 1, 128), ([100, 60], 8, 2, 128), ([40, 70], 10, 1, 64)])
+def test_rows_far_apart(kv, qs, Hq, Hkv, D):
+    """Every third row 2^40 or 2^120 times larger than the others, one infinite and one NaN: the
+    others' results stay as exact as alone."""
+    x = case([400, 333], qs, Hq, Hkv, D, 32, BF16, kv, 3)
+    rows = torch.arange(sum(qs) * Hq).reshape(sum(qs), Hq)
+    ro, _ = want(x)
+    x["q"] = torch.where((rows % 3 == 1)[..., None], x["q"] * 2.0 ** 40, x["q"])
+    x["q"] = torch.where((rows % 9 == 4)[..., None], x["q"] * 2.0 ** 80, x["q"])
+    x["q"].view(-1, D)[1, 5], x["q"].view(-1, D)[4, 6] = math.inf, math.nan
+    out, _ = attend(x, max_q=max(qs))
+    assert worst_row(out, ro, (rows % 3 != 1).numpy()) <= TOL[BF16]
