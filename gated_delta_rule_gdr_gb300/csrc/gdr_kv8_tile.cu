@@ -187,7 +187,7 @@ __device__ __forceinline__ TileRow tile_row(const AttnArgs &a, const Cursor<RB, 
 // row: a lane reading its own row would touch 32 lines an instruction); end_queries, in the
 // same lanes' pieces, turns them to halves and returns the rows' score factor.  All 32 rows are
 // scaled by one power of two that brings the largest magnitude below 2^15, if every piece of 8
-// values reaches 2^-14 of it (the smallest row then keeps values good to 2^-26 of its own
+// values reaches 2^-14 of it (the smallest row then keeps values good to 2^-25 of its own
 // largest); else each row by one of its own, so that a row depends on no other (a common factor
 // loses a row beside one 2^28 times larger).  Rows apart are marked by the factor's sign, and
 // their scores are brought back where masks are applied, off the usual way: a factor of its own

@@ -626,7 +626,7 @@ gdr_status_t gdr_kv8_append(const void *k, const void *v, int64_t k_stride, int6
  * taken within [2^-40, 2^40].
  * Sums, maxima and the output accumulate in fp32; the weights meet the value codes in
  * products of 11-bit operands (22-bit for fp32 q); the codes enter exactly, and bf16 q down
- * to 2^-29 of the largest magnitude in its row, less than a softmax can show.
+ * to 2^-25 of the largest magnitude in its row, less than a softmax can show.
  *   workspace  16-byte aligned, gdr_kv8_attn_workspace_size bytes (0: may be NULL):
  *             partial results of requests whose cache is split; scratch on entry and exit
  */
