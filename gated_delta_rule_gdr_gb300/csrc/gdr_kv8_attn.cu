@@ -5,7 +5,7 @@
 //   x_j = scale ks (q . kcode_j) / ln 2,  o = sum_j p_j vs vcode_j / sum_j p_j,  p_j = 2^x_j
 // with the scales ks, vs of j's page.  One pass: every row keeps a reference exponent M (a
 // whole number, so that moving it rescales exactly) over x_j + log2 vs, and
-//   P_j = 2^(x_j + log2 vs - M + 7),  O += P_j vcode_j,  l += P_j / vs,  o = O / l:
+//   P_j = 2^(x_j + log2 vs - M + 14),  O += P_j vcode_j,  l += P_j / vs,  o = O / l:
 // the value scale rides in the exponent's addend and costs nothing per element.
 //
 // Bound: the cache's bytes.  Measured: 256 requests of 100 to 8192 keys, 8 heads a cached head

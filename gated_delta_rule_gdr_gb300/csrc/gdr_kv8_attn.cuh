@@ -25,8 +25,9 @@ namespace gdr {
 namespace {
 
 namespace kv8 {
-constexpr float kOff = 7.f;     // weights are 2^(x - M + kOff): room below 1 before a half loses bits
-constexpr float kTau = 8.f;     // M moves only when a score exceeds it by more than this
+// Weights are 2^(x - M + kOff), at most 2^(kOff + kTau): a half holds them, 11 bits of those down to
+// 2^-14 and steps of 2^-24 below.  M moves when a score exceeds it by more than kTau.
+constexpr float kOff = 14.f, kTau = 1.5f;
 constexpr float kVsMin = 9.094947017729282e-13f, kVsMax = 1.099511627776e12f;   // 2^-40, 2^40
 // Rows that the merge takes with eight warps each: what is resident at once.  Beyond, the waves
 // cost more than the shorter walks give (256 requests of 8 rows: 0.191 ms against 0.180).

@@ -3,7 +3,7 @@
 //
 // The same mathematics as the split kernel's (gdr_kv8_attn.cu): with a whole-number reference
 // exponent M for each row over x_j + log2 vs,
-//   P_j = 2^(x_j + log2 vs - M + 7),  O += P_j vcode_j,  l += P_j / vs,  o = O / l.
+//   P_j = 2^(x_j + log2 vs - M + 14),  O += P_j vcode_j,  l += P_j / vs,  o = O / l.
 //
 // A unit is 128 keys; an item's rows (row = query x group of heads) are tiles of 128.  A tile's
 // scores S (128 x 128 fp32) and sums O live in TMEM; its weights go back over S as halves and
@@ -317,18 +317,29 @@ __device__ __forceinline__ void load_chunk(uint32_t ts, int ch, const RowUnit<GR
         }
     }
 }
-template <int GR>
-__device__ __forceinline__ float chunk_max(const float (&v)[32], int ch, const RowUnit<GR> &u, float mx) {
-    constexpr int N = GR == 1 ? 32 : 16;
-#pragma unroll
-    for (int i = 0; i < 32 / N; ++i) {
-        const float4 s4 = u.sc[GR == 1 ? 4 * (ch >> 1) : 2 * ch + i];
-        float m[2] = {fmaxf(v[N * i], v[N * i + 1]), fmaxf(v[N * i + 2], v[N * i + 3])};
-#pragma unroll
-        for (int e = 4; e < N; e += 2) m[(e / 2) & 1] = fmaxf(fmaxf(m[(e / 2) & 1], v[N * i + e]), v[N * i + e + 1]);
-        mx = fmaxf(mx, fmaf(fmaxf(m[0], m[1]), unit_factor(u.cs, s4.x), s4.z));
+// The largest exponent of some keys, and the largest of those that are not in its group (16 keys,
+// or a half of what is looked at where one scale covers it).
+struct Largest {
+    float mx = -INFINITY, next = -INFINITY;
+    __device__ __forceinline__ void add(float x) {
+        next = fmaxf(next, fminf(mx, x));
+        mx = fmaxf(mx, x);
     }
-    return mx;
+};
+template <int N, typename X>
+__device__ __forceinline__ float max_of(X x) {
+    float m = fmaxf(x(0), x(1));
+#pragma unroll
+    for (int e = 2; e < N; e += 2) m = fmaxf(fmaxf(m, x(e)), x(e + 1));
+    return m;
+}
+template <int GR>
+__device__ __forceinline__ void chunk_max(const float (&v)[32], int ch, const RowUnit<GR> &u, Largest &r) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const float4 s4 = u.sc[GR == 1 ? 4 * (ch >> 1) : 2 * ch + i];
+        r.add(fmaf(max_of<16>([&](int e) { return v[16 * i + e]; }), unit_factor(u.cs, s4.x), s4.z));
+    }
 }
 template <int GR>
 __device__ __forceinline__ float chunk_weights(uint32_t ts, int ch, const RowUnit<GR> &u, const float (&v)[32], float ref, float l) {
@@ -375,18 +386,15 @@ __device__ __forceinline__ void load_half(uint32_t ts, int h, const RowUnit<GR> 
     }
 }
 template <int GR>
-__device__ __forceinline__ float half_max(const float (&v)[2][32], int h, const RowUnit<GR> &u, float mx) {
-    constexpr int N = 64 / GR;
+__device__ __forceinline__ Largest half_max(const float (&v)[2][32], int h, const RowUnit<GR> &u) {
+    Largest r;
 #pragma unroll
-    for (int i = 0; i < GR; ++i) {
-        auto x = [&](int e) { return v[(N * i + e) >> 5][(N * i + e) & 31]; };
-        float m[2] = {fmaxf(x(0), x(1)), fmaxf(x(2), x(3))};     // two chains
-#pragma unroll
-        for (int e = 4; e < N; e += 2) m[(e / 2) & 1] = fmaxf(fmaxf(m[(e / 2) & 1], x(e)), x(e + 1));
+    for (int i = 0; i < (GR == 1 ? 2 : 4); ++i) {
+        constexpr int N = GR == 1 ? 32 : 16;
         const float4 s4 = u.scales(h, i);
-        mx = fmaxf(mx, fmaf(fmaxf(m[0], m[1]), unit_factor(u.cs, s4.x), s4.z));
+        r.add(fmaf(max_of<N>([&](int e) { return v[(N * i + e) >> 5][(N * i + e) & 31]; }), unit_factor(u.cs, s4.x), s4.z));
     }
-    return mx;
+    return r;
 }
 template <int GR>
 __device__ __forceinline__ float half_weights(uint32_t ts, int h, const RowUnit<GR> &u, const float (&v)[2][32], float ref,
@@ -422,12 +430,24 @@ __device__ __forceinline__ float half_weights(uint32_t ts, int h, const RowUnit<
     }
     return l;
 }
-// Moves M to hold scores whose largest exponent is mx, and the sums so far with it: rare, since
-// M holds what exceeds it by up to kTau.  settled() waits until no product writes the sums.
+// Moves M to hold scores whose largest exponent is mx, and the sums so far with it.  That is a trip
+// through the TMEM, so M is set kRoom above the largest score and holds what exceeds that by up to
+// 8.5: rare (3.5, 2.5 or 1.5: four prompts of 4096 0.406, 0.424, 0.438 ms against 0.343, the chunk on
+// 65 k 1.06, 1.09, 1.12 against 0.985).  But the room is lost to the small weights, and they are
+// all of the output where the largest one's value is nothing.  So a row whose largest score stands
+// 16 (2^16 in weight) above the scores before it goes without; its first ones are compared with
+// `next`, the largest of the keys that are not beside it, or (`lower`) with the half that comes
+// second.
+// settled() waits until no product writes the sums.
+constexpr float kRoom = 7.f, kAlone = 16.f;
 template <int D, typename Settled>
-__device__ __forceinline__ bool move_reference(uint32_t to, float mx, bool rescale, float &M, float &l, Settled settled) {
-    if (!__any_sync(0xffffffffu, mx > M + kv8::kTau)) return true;
-    const float m = fmaxf(M, ceilf(mx)), w = part_weight(M, m);
+__device__ __forceinline__ bool move_reference(uint32_t to, float mx, float next, bool rescale, bool lower, float &M, float &l,
+                                               Settled settled) {
+    const bool alone = lower && mx < M - (kRoom + kAlone) && mx > -INFINITY;
+    if (!__any_sync(0xffffffffu, mx > M + kv8::kTau || alone)) return true;
+    float m = fmaxf(M, ceilf(mx) + kRoom);
+    if (alone || mx > (M == -INFINITY ? next : M - kRoom) + kAlone) m -= kRoom;
+    const float w = part_weight(M, m);
     M = m;
     l *= w;
     if (!rescale) return true;
@@ -462,12 +482,13 @@ __device__ __forceinline__ bool softmax_unit(uint32_t ts, uint32_t to, const Row
         float v[2][32];
         load_half<GR>(ts, 1, u, v);
         // the earlier units' products have landed: the scores' barrier came after them
-        move_reference<D>(to, half_max<GR>(v, 1, u, -INFINITY), rescale, M, l, []() { return true; });
+        const float mx = half_max<GR>(v, 1, u).mx;
+        move_reference<D>(to, mx, mx, rescale, false, M, l, []() { return true; });
         l = half_weights<GR>(ts, 1, u, v, ref(), l);
         tmem_wait_st();
         if (!publish(1)) return false;
         load_half<GR>(ts, 0, u, v);
-        if (!move_reference<D>(to, half_max<GR>(v, 0, u, -INFINITY), true, M, l, upper_done)) return false;
+        if (!move_reference<D>(to, half_max<GR>(v, 0, u).mx, -INFINITY, true, !rescale, M, l, upper_done)) return false;
         l = half_weights<GR>(ts, 0, u, v, ref(), l);
         tmem_wait_st();
         return publish(0);
@@ -476,12 +497,15 @@ __device__ __forceinline__ bool softmax_unit(uint32_t ts, uint32_t to, const Row
         if constexpr (NC == 2) {
             float v[2][32];
             load_half<GR>(ts, copy, u, v);
-            move_reference<D>(to, half_max<GR>(v, copy, u, -INFINITY), rescale, M, l, []() { return true; });
+            const Largest x = half_max<GR>(v, copy, u);
+            move_reference<D>(to, x.mx, rescale ? x.mx : x.next, rescale, false, M, l, []() { return true; });
             l = half_weights<GR>(ts, copy, u, v, ref(), l);
         } else {
             float v[32];
             load_chunk<GR>(ts, copy, u, v);
-            move_reference<D>(to, chunk_max<GR>(v, copy, u, -INFINITY), rescale, M, l, []() { return true; });
+            Largest x;
+            chunk_max<GR>(v, copy, u, x);
+            move_reference<D>(to, x.mx, rescale ? x.mx : x.next, rescale, false, M, l, []() { return true; });
             l = chunk_weights<GR>(ts, copy, u, v, ref(), l);
         }
         const uint32_t zero[16] = {};
@@ -491,13 +515,14 @@ __device__ __forceinline__ bool softmax_unit(uint32_t ts, uint32_t to, const Row
         tmem_wait_st();
         return publish(1) && publish(0);
     } else {
-        float mx = -INFINITY, v[32];
+        float v[32];
+        Largest x;
 #pragma unroll 1
         for (int ch = 3; ch >= 0; --ch) {
             load_chunk<GR>(ts, ch, u, v);
-            mx = chunk_max<GR>(v, ch, u, mx);
+            chunk_max<GR>(v, ch, u, x);
         }
-        move_reference<D>(to, mx, rescale, M, l, []() { return true; });
+        move_reference<D>(to, x.mx, rescale ? x.mx : x.next, rescale, false, M, l, []() { return true; });
 #pragma unroll 1
         for (int ch = 3; ch >= 0; --ch) {
             load_chunk<GR>(ts, ch, u, v);
