@@ -28,7 +28,11 @@
 //           D / 8 consecutive values
 // with every 16-byte load of a quarter warp on distinct banks under the 128-byte swizzle.
 // The weights turn from accumulator to B layout by one 8 x 8 transpose (MOVM) per 8 keys.
-// fp32 queries and their weights are split in two halves each (22 bits), two MMAs for one.
+// fp32 queries are split in two halves (22 bits), two MMAs for one; their weights in three bfloat16
+// (24 bits), three for one, with the value codes as bfloat16: halves end at 2^-24, two of them as
+// one, and beside a large weight without a value (its output is what the small ones give) two
+// halves were off by 1e-4 at scores 14 nats below it.  64 decodes of 100 to 8000 keys: 71.3 us, with
+// the two halves 63.4.
 
 #include "gdr_kv8_attn.cuh"
 
@@ -62,6 +66,17 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_bf(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two halves that are codes as bfloat16, exactly (8 bits hold either type's).
+__device__ __forceinline__ uint32_t codes_bf(uint32_t h) {
+    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    return pack_bf16x2(x.x, x.y);
+}
 // The transpose of an 8 x 8 matrix of halves, a row's pair a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t v) {
     uint32_t r;
@@ -93,7 +108,7 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                  const AttnArgs a) {
     using sp::SLAB, sp::SLAB_BYTES, sp::STAGE, sp::NW, sp::UT;
     constexpr int ST = sp::ST<R>, RB = 8 * R;
-    constexpr bool HL = sizeof(E) == 4;          // two halves for queries and weights
+    constexpr bool HL = sizeof(E) == 4;          // fp32: queries and weights in parts
     constexpr int NKS = D / 16, NVT = D / 16;    // k steps of K q^T, row tiles of O^T
     constexpr int LD = D / 4, LO = D / 8;        // values of a query, of an output row that a lane holds
     extern __shared__ __align__(1024) uint8_t sm[];
@@ -364,7 +379,7 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                             }
                         }
                 }
-                uint32_t pf[HL ? 2 : 1][2][R][2];     // weights of 16 keys as the B operand
+                uint32_t pf[HL ? 3 : 1][2][R][2];     // weights of 16 keys as the B operand
 #pragma unroll
                 for (int n = 0; n < R; ++n)
 #pragma unroll
@@ -379,11 +394,17 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                         }
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const uint32_t hi = pack_h2(p[2 * k], p[2 * k + 1]);
-                            pf[0][i][n][k] = transpose8(hi);
                             if constexpr (HL) {
-                                const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                                pf[HL ? 1 : 0][i][n][k] = transpose8(pack_h2(p[2 * k] - h.x, p[2 * k + 1] - h.y));
+                                float r0 = p[2 * k], r1 = p[2 * k + 1];
+#pragma unroll
+                                for (int w = 0; w < (HL ? 3 : 1); ++w) {
+                                    const uint32_t b = pack_bf16x2(r0, r1);
+                                    pf[w][i][n][k] = transpose8(b);
+                                    r0 -= __uint_as_float(b << 16);
+                                    r1 -= __uint_as_float(b & 0xffff0000u);
+                                }
+                            } else {
+                                pf[0][i][n][k] = transpose8(pack_h2(p[2 * k], p[2 * k + 1]));
                             }
                         }
                     }
@@ -410,11 +431,16 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
                             uint32_t f[4];
                             decode4_h<KV>(__byte_perm(w[0][v], w[1][v], hf ? 0x7362 : 0x5140), f[0], f[1]);
                             decode4_h<KV>(__byte_perm(w[2][v], w[3][v], hf ? 0x7362 : 0x5140), f[2], f[3]);
+                            if constexpr (HL) {
 #pragma unroll
-                            for (int n = 0; n < R; ++n) {
-                                mma_f16(o[n][2 * v + hf], f, pf[0][i][n][0], pf[0][i][n][1]);
-                                if constexpr (HL)
-                                    mma_f16(o[n][2 * v + hf], f, pf[HL ? 1 : 0][i][n][0], pf[HL ? 1 : 0][i][n][1]);
+                                for (int k = 0; k < 4; ++k) f[k] = codes_bf(f[k]);
+#pragma unroll
+                                for (int w = (HL ? 3 : 1) - 1; w >= 0; --w)
+#pragma unroll
+                                    for (int n = 0; n < R; ++n) mma_bf(o[n][2 * v + hf], f, pf[w][i][n][0], pf[w][i][n][1]);
+                            } else {
+#pragma unroll
+                                for (int n = 0; n < R; ++n) mma_f16(o[n][2 * v + hf], f, pf[0][i][n][0], pf[0][i][n][1]);
                             }
                         }
                 }

@@ -625,9 +625,9 @@ gdr_status_t gdr_kv8_append(const void *k, const void *v, int64_t k_stride, int6
  * codes of cached tokens must not be NaN (gdr_kv8_append writes none); value scales are
  * taken within [2^-40, 2^40].
  * Sums, maxima and the output accumulate in fp32; the weights meet the value codes in
- * products of 11-bit operands (22-bit for fp32 q); the codes enter exactly, and bf16 q down
- * to 2^-25 of the largest magnitude in its row, less than a softmax can show.  Weights (times
- * the value scale) below 2^-27 of the row's largest one are held in steps of 2^-37 of it; where a
+ * products of 11-bit operands (fp32 q: 22-bit queries, 24-bit weights); the codes enter
+ * exactly, and bf16 q down to 2^-25 of the largest magnitude in its row, less than a softmax
+ * can show.  With bf16 q, weights (times the value scale) below 2^-27 of the row's largest one are held in steps of 2^-37 of it; where a
  * request has more than 16 rows of a cached head, and the largest score is less than 2^16 times
  * (11 nats) above the next ones, below 2^-20 in steps of 2^-30.
  *   workspace  16-byte aligned, gdr_kv8_attn_workspace_size bytes (0: may be NULL):

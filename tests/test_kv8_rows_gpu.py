@@ -115,7 +115,7 @@ def test_rows_far_apart(kv, qs, Hq, Hkv, D):
 
 # ------------------------------------------------------------------ a largest weight whose value is nothing
 @pytest.mark.parametrize("kv", ["e4m3", "int8"])
-@pytest.mark.parametrize("dtype,gap", [(BF16, 12.0), (BF16, 16.0), (BF16, 20.0)])
+@pytest.mark.parametrize("dtype,gap", [(BF16, 12.0), (BF16, 16.0), (BF16, 20.0), (F32, 12.0), (F32, 20.0), (F32, 60.0)])
 @pytest.mark.parametrize("qs,Hq,Hkv,D", [([1], 8, 1, 128), ([1], 8, 2, 64), ([2], 8, 1, 128), ([4], 8, 1, 128),
                                          ([8], 8, 1, 64), ([15], 8, 1, 128), ([150], 4, 1, 128)])
 def test_a_dominant_key_without_a_value(kv, dtype, gap, qs, Hq, Hkv, D):
@@ -123,7 +123,7 @@ def test_a_dominant_key_without_a_value(kv, dtype, gap, qs, Hq, Hkv, D):
     attention sink), so the output is what the small weights give.  bf16: the weights stand
     2^13 .. 2^14 for the row's largest, so 20 nats below (2^-28.9) they are 2^-15.9 or more, in
     steps of 2^-24: off by 2^-25.8 at most in rms, 2^-9.9 = 1.0e-3 of the weight, which with the
-    output's rounding is 2.5e-3 of 3e-3."""
+    output's rounding is 2.5e-3 of 3e-3.  fp32 keeps 24 bits of every weight."""
     x = case([1001], qs, Hq, Hkv, D, 16, dtype, kv, 4)
     one = 0x38 if kv == "e4m3" else 1                     # the code of 1
     big, value = (0x78, 256.0) if kv == "e4m3" else (100, 100.0)
