@@ -573,9 +573,11 @@ def last_device_error(device=None) -> int:
 #
 # These run once a layer for every token served, and their small calls take a few
 # microseconds on the device: the checks below read each property of a tensor once, and the
-# stream's handle is taken without building a Stream object.
+# stream's handle is taken without building a Stream object (by a function that a torch build
+# without CUDA does not have, so it is looked up when a call needs it).
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
+def _raw_stream(index):
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def _int(t, name, shape=None):
