@@ -779,7 +779,8 @@ gdr_status_t gdr_kv8_attn(const void *q, int64_t q_stride, const void *k_cache, 
     if (S == 0 || total_q == 0 || Hq == 0 || max_q == 0) return GDR_OK;
     if (Hkv == 0 || Hq % Hkv != 0 || table_width == 0 || num_pages == 0) return GDR_ERR_INVALID_ARG;
     if (!cu_q && (total_q != S || max_q != 1)) return GDR_ERR_INVALID_ARG;
-    if (!kv8_heads_ok(Hq, Hkv, total_q, S) || !fits31(table_width, page)) return GDR_ERR_UNSUPPORTED;
+    // a unit of keys ends up to 255 tokens past the last one
+    if (!kv8_heads_ok(Hq, Hkv, total_q, S) || (int64_t)table_width * page > 0x7fffff00) return GDR_ERR_UNSUPPORTED;
     if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !kv_len || !out)
         return GDR_ERR_INVALID_ARG;
     if (!row_stride_ok(q_stride, Hq, D, dtype == GDR_DTYPE_F32 ? 4 : 2)) return GDR_ERR_INVALID_ARG;

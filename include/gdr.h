@@ -609,7 +609,8 @@ gdr_status_t gdr_kv8_append(const void *k, const void *v, int64_t k_stride, int6
  * Attention of the last queries of S requests over their cached keys and values.
  *   q         [total_q][Hq][D] dtype, q_stride elements between tokens (at least Hq * D;
  *             rows 16-byte aligned); query head hq reads cached head hq / (Hq / Hkv)
- *   kv_len    [S] tokens cached, the new ones included (at most table_width * page)
+ *   kv_len    [S] tokens cached, the new ones included (at most table_width * page, which is
+ *             at most 2^31 - 256)
  *   cu_q      [S+1] first query of each request, cu_q[0] = 0, cu_q[S] <= total_q; or NULL:
  *             one query a request (max_q = 1, total_q = S)
  *   max_q     the most queries any request has: it chooses the kernel.  Another value, a smaller
@@ -627,9 +628,10 @@ gdr_status_t gdr_kv8_append(const void *k, const void *v, int64_t k_stride, int6
  * Sums, maxima and the output accumulate in fp32; the weights meet the value codes in
  * products of 11-bit operands (fp32 q: 22-bit queries, 24-bit weights); the codes enter
  * exactly, and bf16 q down to 2^-25 of the largest magnitude in its row, less than a softmax
- * can show.  With bf16 q, weights (times the value scale) below 2^-27 of the row's largest one are held in steps of 2^-37 of it; where a
- * request has more than 16 rows of a cached head, and the largest score is less than 2^16 times
- * (11 nats) above the next ones, below 2^-20 in steps of 2^-30.
+ * can show.  With bf16 q, weights (times the value scale) below 2^-27 of the row's largest one
+ * are held in steps of 2^-37 of it; where a request has more than 16 rows of a cached head, and
+ * the largest score is less than 11 nats (2^16) above the next ones, below 2^-20 in steps of
+ * 2^-30.  Scores of more than 5e6 in magnitude can overflow (NaN in that row).
  *   workspace  16-byte aligned, gdr_kv8_attn_workspace_size bytes (0: may be NULL):
  *             partial results of requests whose cache is split; scratch on entry and exit
  */
