@@ -193,7 +193,8 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         ld.next_unit(a);
         look_up();
     };
-    bool ok = true;
+    // a limit of zero: the first wait has run out before it begins, whether its data is there or not
+    bool ok = a.limit_ns != 0;
     look_up();
 #pragma unroll 1
     for (int i = 0; i < ST; ++i) issue();
@@ -548,6 +549,7 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
         c.next_of_item(a);
     }
     if (!ok) {   // leave no copy in flight
+        if (a.limit_ns == 0 && lane == 0) atomicOr(&g_device_error_word, kDevErrTimeout);
         entry.x = -1;
         const int issued = units - left;
         for (int k = waited; k < issued; ++k) mbar_wait(bar(k % ST), (uint32_t)(k / ST) & 1u, kCleanupLimitNs);

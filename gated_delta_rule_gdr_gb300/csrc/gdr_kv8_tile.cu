@@ -725,10 +725,12 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
             // uniform registers; one elected lane issues.
             constexpr uint32_t id_s = idesc_f16(TR, UT, false), id_o = idesc_f16(TR, D, true);
             bool ok = tmem == 0, issued = false;     // all of the TMEM is ours: its base is 0
-            if (!ok) {
+            auto give_up = [&]() {
+                ok = false;
                 s_abort = 1;
                 atomicOr(&g_device_error_word, kDevErrTimeout);
-            }
+            };
+            if (!ok) give_up();
             // scores of unit k into buffer b from query tile q; gives the key slot back
             auto scores = [&](int b, int q, int k) {
                 tc_fence_after();
@@ -791,6 +793,9 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                     }
                 };
                 next_scores(0, true, false);
+                // a limit of zero: the next wait has run out before it begins, whatever is there, and
+                // the others' that depend on it do
+                if (a.limit_ns == 0) give_up();
 #pragma unroll 1
                 for (int k = 0; ok && k < units; ++k) {
                     const bool last = c.t + 1 == c.nt || k + 1 == units, first = c.t == 0 || k == 0;
@@ -836,6 +841,7 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const AttnArgs a) {
                         next_scores(scored++);
                 };
                 more_scores(-1);
+                if (a.limit_ns == 0) give_up();      // (see above)
                 int k0 = 0;              // the item's first unit
 #pragma unroll 1
                 for (int k = 0; ok && k < units; ++k) {
