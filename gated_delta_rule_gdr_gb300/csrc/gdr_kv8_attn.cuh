@@ -29,9 +29,11 @@ namespace kv8 {
 // 2^-14 and steps of 2^-24 below.  M moves when a score exceeds it by more than kTau.
 constexpr float kOff = 14.f, kTau = 1.5f;
 constexpr float kVsMin = 9.094947017729282e-13f, kVsMax = 1.099511627776e12f;   // 2^-40, 2^40
-// Rows that the merge takes with eight warps each: what is resident at once.  Beyond, the waves
-// cost more than the shorter walks give (256 requests of 8 rows: 0.191 ms against 0.180).
-constexpr int kMergeWide = 1216;
+// CTAs of the merge that an SM holds (256 threads of 64 registers).  Rows are taken with eight warps
+// each while all of them are resident at once (512 rows of 8 x 2 tokens on 6000 keys 24.2 us, with
+// a warp each 25.4); beyond, the waves cost more than the shorter walks give (24 tokens on 1000
+// keys, 768 rows: 20.7 and 19.5; 56 tokens, 1792 rows: 26.7 and 21.4).
+constexpr int kMergeResident = 4;
 }  // namespace kv8
 
 struct AttnArgs {
@@ -293,7 +295,7 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
 // ROUND: the grid may be too small for the items and rows that there are (max_q says less than
 // the lengths do), and goes round; the loops cost up to 1 us (7 ragged fp32 requests: 22.1 and 23.4 us).
 template <typename E, int D, int RB, int WPR, int RPW, bool ROUND>
-__global__ void __launch_bounds__(256, 4) kv8_merge_kernel(const AttnArgs a) {
+__global__ void __launch_bounds__(256, kv8::kMergeResident) kv8_merge_kernel(const AttnArgs a) {
     static_assert(WPR == 1 ? !ROUND : RPW == 1, "");
     constexpr int VL = D / 32;
     __shared__ float s_o[WPR > 1 ? 8 : 1][D];
@@ -447,6 +449,23 @@ __global__ void __launch_bounds__(256, 4) kv8_merge_kernel(const AttnArgs a) {
     }
 }
 
+// SMs of the current device, asked once a device.
+int sm_count() {
+    static std::atomic<int> known[64];
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 152;
+    }
+    const bool in = dev >= 0 && dev < 64;
+    if (in && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+        cudaGetLastError();
+        return 152;
+    }
+    if (in) known[dev].store(sms, std::memory_order_relaxed);
+    return sms;
+}
 // A launch that may start while the kernel before it in the stream ends (both wait before they
 // read what another kernel writes).
 template <typename... P, typename... A>
@@ -477,7 +496,7 @@ cudaError_t launch_merge(const AttnArgs &a, int64_t rows, cudaStream_t s) {
     const bool every = items == a.ctas || blocks == limit;
     const unsigned x = (unsigned)items, all_x = (unsigned)std::min(limit * a.Hkv, (int64_t)a.ctas);
     const unsigned wide = (unsigned)most, y = (unsigned)((could + 8 * RPW - 1) / (8 * RPW));
-    if (items * most <= kv8::kMergeWide) {
+    if (items * most <= kv8::kMergeResident * sm_count()) {
         if (every && most == could) return launch_after(kv8_merge_kernel<E, D, RB, 8, 1, false>, dim3(x, wide), 256, 0, s, a);
         return launch_after(kv8_merge_kernel<E, D, RB, 8, 1, true>, dim3(x, wide), 256, 0, s, a);
     }
@@ -495,23 +514,6 @@ void place_parts(AttnArgs &a, void *ws, int ctas, int RB) {
     a.part_o = a.part_ml + (size_t)ctas * 2 * RB * 2;
 }
 
-// SMs of the current device, asked once a device.
-int sm_count() {
-    static std::atomic<int> known[64];
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 152;
-    }
-    const bool in = dev >= 0 && dev < 64;
-    if (in && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 152;
-    }
-    if (in) known[dev].store(sms, std::memory_order_relaxed);
-    return sms;
-}
 // The kernel's shared-memory limit, raised once a device (`done`: one flag a kernel).
 template <typename K>
 cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t> &done) {
