@@ -8,15 +8,17 @@
 // finite magnitude; the off codes already there are re-encoded if the scale grew.
 //
 // Bound: bytes.  Measured: 16384 tokens x 8 heads x 128 bf16 values (101 MB, 14.8 us at the copy
-// rate) 20.4 us = 4.9 TB/s; 37 requests of up to 400 fp32 tokens (24 MB, 3.6 us) 7.1 us; 64
-// single tokens 2.9 us, a launch.  A run's values are
+// rate) 20.2 us = 5.0 TB/s; 37 requests of up to 400 fp32 tokens (24 MB, 3.6 us) 6.9 us; 64
+// single tokens 2.7 us, a launch.  A run's values are
 // read once, held in registers as they came (16 bytes a piece) through the maximum, then
 // scaled, rounded and stored.  The maximum is taken on the bit patterns without their signs,
 // two bf16 values an operation; it also tells when a value is not finite, which alone costs a
 // second look.  Runs of at most 256 pieces are a warp's (one token, short chunks: as many
 // runs in flight as there are warps), longer ones the whole CTA's.  A CTA looks for the runs
 // that begin in its window of tokens; the window is short where there are few tokens, so that
-// a decode step spreads over the device.
+// a decode step spreads over the device.  A lane's pieces of keys and values together are more
+// than the fp32 instances' registers hold beside the division of the slow path: they spill 96 to
+// 416 bytes a thread.
 
 #include "gdr_kv8.cuh"
 

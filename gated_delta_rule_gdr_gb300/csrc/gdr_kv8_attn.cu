@@ -10,7 +10,7 @@
 //
 // Bound: the cache's bytes.  Measured: 256 requests of 100 to 8192 keys, 8 heads a cached head
 // (1029 MB) 0.166 ms = 6.2 TB/s, 91 % of the measured copy rate; one of a million keys (1074
-// MB) 0.172 ms = 6.2 TB/s; loads alone took the million 0.167.  At group
+// MB) 0.171 ms = 6.3 TB/s; loads alone took the million 0.167.  At group
 // size 8 a byte of keys or values meets 16 flops, far
 // below what the tensor cores need, so the kernel's job is to keep enough loads in flight
 // and to stay within the issue slots: 12 warps an SM, each with two 8 KB slabs (32 tokens of
@@ -594,10 +594,10 @@ Shape shape_of(int max_q, int G, Elem e) {
     const int64_t rows = (int64_t)max_q * G;
     if (rows <= 8) return Shape::R8;
     // fp32 (the accuracy path) stays at 16 rows: its fragments are twice as large.  bf16 up to 16
-    // rows: 32 requests on 16 k keys 0.145 ms here, 0.182 in the tile kernel; beyond, 32 rows in
-    // warps of their own on shared slabs took 0.243 ms against the tile kernel's 0.182 (on 300
-    // keys 0.022 against 0.034: an item's ends cost the tile kernel more; both with all units
-    // divided evenly)
+    // rows: 32 requests on 16 k keys 0.112 ms here, 0.136 in the tile kernel, 4 on 4000 keys 17.0
+    // and 26.8 us (32 on 300 keys 21.3 and 20.2); beyond, 32 rows in warps of their own on shared
+    // slabs took 0.243 ms against the tile kernel's 0.182 at the time (32 on 300 keys 22 us; 20.6
+    // in the tile kernel since an item's ends count in the division)
     return rows <= 16 || e == Elem::F32 ? Shape::R16 : Shape::TILE;
 }
 template <typename E, Kv8 KV, int D>

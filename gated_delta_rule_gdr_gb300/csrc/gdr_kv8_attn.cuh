@@ -4,9 +4,10 @@
 // Work.  A request's n queries and the G = Hq / Hkv query heads of one cached head form
 // n * G rows (row r: query r / G, head r % G), which all read the same keys.  An item is a
 // block of RB such rows with the keys its last row sees, in units of UT tokens (an item that
-// sees nothing keeps one unit, which writes its zeros).  All units of a call, ordered by
-// (request, head, block, tokens), are divided evenly among the CTAs, whatever the requests'
-// lengths are: a CTA takes units [total c / G, total (c + 1) / G).  Lengths stay on the
+// sees nothing keeps one unit, which writes its zeros).  All units of a call stand in one order
+// (request, head, block, tokens), each item's after as much more as its ends cost (E units), and
+// that length is divided evenly among the CTAs, whatever the requests' lengths are: of a total
+// of w, CTA c of n takes the units that lie in [w c / n, w (c + 1) / n).  Lengths stay on the
 // device; every CTA finds its first unit by a prefix sum over the requests.
 //
 // An item that falls to several CTAs leaves in each an unnormalised partial result (fp32

@@ -22,11 +22,11 @@
 //       exponentials.  The copies' sums are joined at the item's end.
 //
 // Bounds.  PAIR: the two products, 4 rows keys D flops.  Measured: 1000 tokens of 4 heads a
-// cached head, 8 of those, on 65 k keys (1.07 TFLOP) 0.984 ms = 1.09 PFLOP/s, 56 % of a large
+// cached head, 8 of those, on 65 k keys (1.07 TFLOP) 0.982 ms = 1.09 PFLOP/s, 56 % of a large
 // matrix product's measured rate; four prompts of 4096 (275 GFLOP counting only what is seen)
-// 0.347 ms.  The tensor cores wait for the softmax's chain of TMEM loads, maxima, exponentials
+// 0.343 ms.  The tensor cores wait for the softmax's chain of TMEM loads, maxima, exponentials
 // and stores (two tiles hide about half of it).
-// Copies: the cache's bytes.  32 requests of 5 x 8 rows on up to 32 k keys (555 MB) 0.155 ms =
+// Copies: the cache's bytes.  32 requests of 5 x 8 rows on up to 32 k keys (555 MB) 0.156 ms =
 // 3.6 TB/s.  Of the 2400 cycles that a unit takes the widening warps work 1500 and wait 700 for a
 // slot that the products give back; shared memory is busy for as much: a unit's 32 KB of codes
 // are read once, written widened (64 KB) and read by the products with the queries (96 KB).
@@ -1205,9 +1205,11 @@ cudaError_t launch_tile_f(AttnArgs &a, void *ws, int ctas, int64_t rows, cudaStr
                             : launch_tile_g<KV, D, PAIR, NC, 4>(a, ws, ctas, rows, s);
 }
 
-// Pairs of tiles where a request may have more rows than one tile; where they fill a half or a
-// quarter of one, that many copies of them (32 requests on up to 32 k keys, 24 and 40 rows: one
-// copy 0.221 and 0.225 ms, four and two 0.212 and 0.219, before the loads were two warps').
+// Pairs of tiles where a request may have more rows than one tile (96 rows, 32 requests on 1000 to
+// 16 k keys: one tile 0.108 ms, pairs 0.138; 4 on 4000 keys 28.6 and 27.9 us); where they fill a
+// half or a quarter of one, that many copies of them (40 rows, 32 on 1000 to 16 k: two copies 0.092
+// ms, one 0.104; 24 rows: four 0.0883, two 0.0890, one 0.100; on 100 to 600 keys, where an item's
+// ends weigh more, 26 us with copies and 23 to 24 with one).
 template <Kv8 KV, int D>
 cudaError_t launch_tile_d(AttnArgs &a, void *ws, int ctas, int64_t rows, cudaStream_t s) {
     return rows > tl::TR       ? launch_tile_f<KV, D, true, 1>(a, ws, ctas, rows, s)

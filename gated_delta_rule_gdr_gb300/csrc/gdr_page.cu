@@ -23,7 +23,7 @@
 // table holds: one CTA, or one cluster where the table is large, counts and places them.
 //
 // Bound: the launch and the scans' latency (300 requests of one token, 9 of them finished, 7.0 us,
-// 24 KB, 5.4 without a finished one; 60 prompts of some 250 k tokens together 7.4 us, 2.0 MB,
+// 24 KB, 5.4 without a finished one; 60 prompts of some 250 k tokens together 7.5 us, 2.0 MB,
 // of which the bytes are 0.3 us).
 
 #include "gdr_internal.h"
