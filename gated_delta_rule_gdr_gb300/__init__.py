@@ -31,13 +31,15 @@ __all__ = ["GdrError", "load", "chunk_fwd", "decode_step", "chunk_decay", "chunk
            "set_option", "get_option", "option", "mla_decode", "mla_decode_workspace_size",
            "chunk_bwd", "chunk_bwd_workspace_size", "chunk_saved_size", "chunk_fwd_train",
            "chunk_bwd_saved", "page_plan", "kv8_append", "kv8_attn", "kv8_attn_workspace_size",
-           "KV8"]
+           "KV8", "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_size", "NORM", "PAIRS"]
 
 DECAY = {"affine": 0, "log": 1}   # gdr_decay_t
 STATUS = {0: "GDR_OK", 1: "GDR_ERR_INVALID_ARG", 2: "GDR_ERR_UNSUPPORTED", 3: "GDR_ERR_RANGE",
           4: "GDR_ERR_CUDA", 5: "GDR_ERR_TIMEOUT"}
 DTYPE = {torch.float32: 0, torch.bfloat16: 1}
 KV8 = {torch.float8_e4m3fn: 0, torch.int8: 1}   # gdr_kv8_t
+NORM = {None: 0, "none": 0, "rms": 1, "l2": 2}  # gdr_norm_t
+PAIRS = {"half": 0, "adjacent": 1}              # gdr_rope_t
 # gdr_option_t
 OPTIONS = {"wait_limit_ns": 0, "fused_variant": 1, "chain_split": 2, "segments": 3,
            "bwd_variant": 4}
@@ -103,6 +105,9 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         "gdr_page_plan": [vp] * 11 + [i] * 5 + [vp],
         "gdr_page_plan_ex": [vp] * 13 + [i] * 5 + [vp],
         "gdr_kv8_append": [vp, vp, i64, i64, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp],
+        "gdr_qk_norm_rope": [vp, i64, vp, i64, vp, vp, f, i, vp, vp, i, i, vp, i64, vp, i64] + [i] * 5 + [vp],
+        "gdr_qk_norm_rope_bwd": [vp, i64, vp, i64, vp, vp, f, i, vp, vp, i, i, vp, i64, vp, i64, vp, i64, vp,
+                                 i64, vp, vp] + [i] * 5 + [vp, sz, vp],
         "gdr_kv8_attn": [vp, i64, vp, vp, vp, vp, vp, vp, vp, f, vp, vp] + [i] * 11 + [vp, sz, vp],
     }
     for name, args in sig.items():
@@ -119,6 +124,8 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.gdr_mla_decode_workspace_size.restype = sz
     lib.gdr_kv8_attn_workspace_size.argtypes = [i] * 7
     lib.gdr_kv8_attn_workspace_size.restype = sz
+    lib.gdr_qk_norm_rope_bwd_workspace_size.argtypes = [i]
+    lib.gdr_qk_norm_rope_bwd_workspace_size.restype = sz
     lib.gdr_get_option.argtypes = [i]
     lib.gdr_get_option.restype = ctypes.c_int64
     lib.gdr_status_string.restype = ctypes.c_char_p
@@ -719,3 +726,110 @@ def kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, scale: 
     if code:
         raise GdrError(code, "gdr_kv8_attn")
     return (out, lse) if want_lse else out
+
+
+# ---- norms of queries and keys with the rotation by position (checks as sparing as above)
+
+def _weights(t, name, D):
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous float32 CUDA tensor")
+    if t.shape != (D,):
+        raise ValueError(f"{name} must have shape ({D},)")
+    return t.data_ptr()
+
+
+def _norm_how(q, k, norm, q_weight, k_weight, positions, freq, pairs):
+    """What both directions check: T, heads, D, and the arguments from the weights to the pairs."""
+    T, Hq, D = q.shape
+    if k is not None and (k.dtype is not q.dtype or k.dim() != 3 or k.shape[0] != T or k.shape[2] != D):
+        raise ValueError(f"k must be [{T}, heads, {D}] of q's dtype")
+    if norm not in NORM or pairs not in PAIRS:
+        raise ValueError(f"unknown norm {norm!r} or pairs {pairs!r}")
+    rot, fp = 0, None
+    if freq is not None:
+        if positions is None:
+            raise ValueError("freq wants positions")
+        if freq.dtype is not torch.float64 or not freq.is_cuda or not freq.is_contiguous() or freq.dim() != 1:
+            raise TypeError("freq must be a contiguous float64 CUDA tensor [rot_dim / 2]")
+        rot, fp = 2 * freq.shape[0], freq.data_ptr()
+    return (T, Hq, 0 if k is None else k.shape[1], D, _weights(q_weight, "q_weight", D),
+            _weights(k_weight, "k_weight", D), NORM[norm],
+            None if positions is None else _int(positions, "positions", (T,)), fp, rot, PAIRS[pairs])
+
+
+def _like(t, out, name):
+    """A new tensor of t's shape, or `out`, checked: its pointer and token stride too."""
+    if out is None:
+        out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    elif out.shape != t.shape or out.dtype is not t.dtype:
+        raise ValueError(f"{name} must have its input's shape and dtype")
+    return (out, *_rows(out, name))
+
+
+def qk_norm_rope(q, k=None, *, norm="rms", q_weight=None, k_weight=None, eps: float = 1e-6, positions=None,
+                 freq=None, pairs="half", q_out=None, k_out=None):
+    """Norms of queries and keys for each head and the rotation by position, in one pass.  q [T,Hq,D]
+    and k [T,Hk,D] (or None) fp32 or bf16, tokens may be strided; norm "rms" (mean square), "l2" (unit
+    length) or "none"; q_weight, k_weight [D] fp32 or None; positions [T] int32 (negative: not a token,
+    its outputs are left as they were); freq [rot_dim / 2] fp64, radians a position (None: no
+    rotation); pairs "half" (i, i + rot_dim / 2) or "adjacent" (2 i, 2 i + 1).  q_out, k_out may be q and
+    k.  Returns (q_out, k_out)."""
+    lib = _lib or load()
+    qp, qst = _rows(q, "q")
+    kp, kst = (None, 0) if k is None else _rows(k, "k")
+    T, Hq, Hk, D, qw, kw, kind, pos, fp, rot, pr = _norm_how(q, k, norm, q_weight, k_weight, positions, freq, pairs)
+    q_out, qo, qos = _like(q, q_out, "q_out")
+    ko, kos = None, 0
+    if k is not None:
+        k_out, ko, kos = _like(k, k_out, "k_out")
+    code = lib.gdr_qk_norm_rope(qp, qst, kp, kst, qw, kw, eps, kind, pos, fp, rot, pr, qo, qos, ko, kos, T, Hq,
+                                Hk, D, DTYPE[q.dtype], _raw_stream(q.device.index))
+    if code:
+        raise GdrError(code, "gdr_qk_norm_rope")
+    return q_out, (None if k is None else k_out)
+
+
+def qk_norm_rope_bwd_workspace_size(D) -> int:
+    """Bytes of workspace qk_norm_rope_bwd needs on the current device where weights have gradients."""
+    return int(load().gdr_qk_norm_rope_bwd_workspace_size(int(D)))
+
+
+def qk_norm_rope_bwd(q, k, d_q_out, d_k_out, *, norm="rms", q_weight=None, k_weight=None, eps: float = 1e-6,
+                     positions=None, freq=None, pairs="half", d_q=None, d_k=None, workspace=None):
+    """Gradients through qk_norm_rope (the same arguments) given those of its outputs.  d_q, d_k may be
+    d_q_out and d_k_out (or q and k) themselves.  workspace: None (allocated here) or a uint8 CUDA tensor
+    of qk_norm_rope_bwd_workspace_size bytes.  Returns (d_q, d_k, d_q_weight, d_k_weight), the weights'
+    [D] fp32, None for weights that are None."""
+    lib = _lib or load()
+    qp, qst = _rows(q, "q")
+    kp, kst = (None, 0) if k is None else _rows(k, "k")
+    T, Hq, Hk, D, qw, kw, kind, pos, fp, rot, pr = _norm_how(q, k, norm, q_weight, k_weight, positions, freq, pairs)
+    if d_q_out.shape != q.shape or d_q_out.dtype is not q.dtype:
+        raise ValueError("d_q_out must have q's shape and dtype")
+    gp, gst = _rows(d_q_out, "d_q_out")
+    d_q, dp, dst = _like(q, d_q, "d_q")
+    hp, hst, ep, est = None, 0, None, 0
+    if k is not None:
+        if d_k_out.shape != k.shape or d_k_out.dtype is not k.dtype:
+            raise ValueError("d_k_out must have k's shape and dtype")
+        hp, hst = _rows(d_k_out, "d_k_out")
+        d_k, ep, est = _like(k, d_k, "d_k")
+    new = lambda w: None if w is None else torch.empty((D,), dtype=torch.float32, device=q.device)  # noqa: E731
+    dqw, dkw = new(q_weight), new(k_weight if k is not None else None)
+    wp, wn = None, 0
+    if dqw is not None or dkw is not None:
+        wn = lib.gdr_qk_norm_rope_bwd_workspace_size(D)
+        if workspace is None:
+            workspace = torch.empty(max(wn, 16), dtype=torch.uint8, device=q.device)
+        elif workspace.dtype is not torch.uint8 or not workspace.is_cuda or workspace.numel() < wn:
+            raise ValueError(f"workspace must be a uint8 CUDA tensor of at least {wn} bytes")
+        wp = workspace.data_ptr()
+    code = lib.gdr_qk_norm_rope_bwd(qp, qst, kp, kst, qw, kw, eps, kind, pos, fp, rot, pr, gp, gst, hp, hst, dp,
+                                    dst, ep, est, None if dqw is None else dqw.data_ptr(),
+                                    None if dkw is None else dkw.data_ptr(), T, Hq, Hk, D, DTYPE[q.dtype], wp, wn,
+                                    _raw_stream(q.device.index))
+    if code:
+        raise GdrError(code, "gdr_qk_norm_rope_bwd")
+    return d_q, (None if k is None else d_k), dqw, dkw

@@ -67,6 +67,40 @@ bool row_stride_ok(int64_t stride, int H, int D, int esz) {
     return stride >= (int64_t)H * D && stride < ((int64_t)1 << 40) && stride * esz % 16 == 0;
 }
 
+// ---- norms of queries and keys with the position rotation ----
+struct NormShape {
+    float eps;
+    gdr_norm_t norm;
+    const int *positions;
+    const double *freq;
+    int rot_dim;
+    gdr_rope_t pairs;
+    int T, Hq, Hk, D;
+    gdr_dtype_t dtype;
+};
+gdr_status_t check_norm(const NormShape &n) {
+    if (n.T < 0 || n.Hq < 0 || n.Hk < 0 || n.rot_dim < 0) return GDR_ERR_INVALID_ARG;
+    if (!(n.eps >= 0.0f) || !std::isfinite(n.eps)) return GDR_ERR_INVALID_ARG;
+    if (n.norm != GDR_NORM_NONE && n.norm != GDR_NORM_RMS && n.norm != GDR_NORM_L2) return GDR_ERR_INVALID_ARG;
+    if (n.pairs != GDR_ROPE_HALF && n.pairs != GDR_ROPE_ADJACENT) return GDR_ERR_INVALID_ARG;
+    if (!dtype_ok(n.dtype) || n.D < 16 || n.D > 512 || (n.D & (n.D - 1)) || n.Hq > 65536 || n.Hk > 65536)
+        return GDR_ERR_UNSUPPORTED;
+    if (n.rot_dim > n.D || n.rot_dim % 16) return GDR_ERR_UNSUPPORTED;
+    if (n.rot_dim > 0 && n.T > 0 && (!n.positions || !n.freq)) return GDR_ERR_INVALID_ARG;
+    return GDR_OK;
+}
+bool rows_ok(const void *p, int64_t stride, int H, const NormShape &n) {
+    return n.T == 0 || H == 0 ||
+           (p && aligned16(p) && row_stride_ok(stride, H, n.D, n.dtype == GDR_DTYPE_F32 ? 4 : 2));
+}
+gdr::NormCall norm_call(const NormShape &n) {
+    gdr::NormCall c{};
+    c.positions = n.positions, c.freq = n.freq, c.eps = n.eps;
+    c.norm = n.norm != GDR_NORM_NONE, c.mean = n.norm == GDR_NORM_RMS;
+    c.T = n.T, c.D = n.D, c.rot = n.rot_dim, c.pairs = n.pairs == GDR_ROPE_ADJACENT;
+    return c;
+}
+
 // Process-wide options (gdr_set_option).  Relaxed atomics: a value set before a
 // call is seen by that call's launches on any thread.
 std::atomic<uint64_t> g_wait_limit_ns{2000000000ull};
@@ -793,6 +827,57 @@ gdr_status_t gdr_kv8_attn(const void *q, int64_t q_stride, const void *k_cache, 
                                           kv_len, cu_q, scale, out, lse, S, max_q, total_q, Hq, Hkv, D,
                                           table_width, page, num_pages, elem_of(dtype), kv8_of(kv),
                                           workspace, static_cast<cudaStream_t>(stream)));
+}
+
+// ---- norms of queries and keys with the position rotation ----
+
+gdr_status_t gdr_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                              const float *q_weight, const float *k_weight, float eps, gdr_norm_t norm,
+                              const int *positions, const double *freq, int rot_dim, gdr_rope_t pairs,
+                              void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride, int T,
+                              int Hq, int Hk, int D, gdr_dtype_t dtype, void *stream) {
+    const NormShape n{eps, norm, positions, freq, rot_dim, pairs, T, Hq, Hk, D, dtype};
+    const gdr_status_t bad = check_norm(n);
+    if (bad != GDR_OK) return bad;
+    if (!rows_ok(q, q_stride, Hq, n) || !rows_ok(k, k_stride, Hk, n) || !rows_ok(q_out, q_out_stride, Hq, n) ||
+        !rows_ok(k_out, k_out_stride, Hk, n))
+        return GDR_ERR_INVALID_ARG;
+    if (T == 0 || Hq + Hk == 0) return GDR_OK;
+    gdr::NormCall c = norm_call(n);
+    c.t[0] = {q, nullptr, q_out, q_stride, 0, q_out_stride, q_weight, Hq};
+    c.t[1] = {k, nullptr, k_out, k_stride, 0, k_out_stride, k_weight, Hk};
+    return from_cuda(gdr::launch_norm_rope(c, false, nullptr, nullptr, nullptr, elem_of(dtype),
+                                           static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdr_qk_norm_rope_bwd_workspace_size(int D) {
+    return D < 16 || D > 512 || (D & (D - 1)) ? 0 : gdr::norm_rope_workspace_bytes(D);
+}
+
+gdr_status_t gdr_qk_norm_rope_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                  const float *q_weight, const float *k_weight, float eps, gdr_norm_t norm,
+                                  const int *positions, const double *freq, int rot_dim, gdr_rope_t pairs,
+                                  const void *d_q_out, int64_t d_q_out_stride, const void *d_k_out,
+                                  int64_t d_k_out_stride, void *d_q, int64_t d_q_stride, void *d_k,
+                                  int64_t d_k_stride, float *d_q_weight, float *d_k_weight, int T, int Hq,
+                                  int Hk, int D, gdr_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                                  void *stream) {
+    const NormShape n{eps, norm, positions, freq, rot_dim, pairs, T, Hq, Hk, D, dtype};
+    const gdr_status_t bad = check_norm(n);
+    if (bad != GDR_OK) return bad;
+    if (!rows_ok(q, q_stride, Hq, n) || !rows_ok(k, k_stride, Hk, n) || !rows_ok(d_q, d_q_stride, Hq, n) ||
+        !rows_ok(d_k, d_k_stride, Hk, n) || !rows_ok(d_q_out, d_q_out_stride, Hq, n) ||
+        !rows_ok(d_k_out, d_k_out_stride, Hk, n))
+        return GDR_ERR_INVALID_ARG;
+    const bool weights = d_q_weight || d_k_weight;
+    if (weights && (!workspace || workspace_bytes < gdr::norm_rope_workspace_bytes(D) || !aligned16(workspace)))
+        return GDR_ERR_INVALID_ARG;
+    if (!weights && (T == 0 || Hq + Hk == 0)) return GDR_OK;
+    gdr::NormCall c = norm_call(n);
+    c.t[0] = {q, d_q_out, d_q, q_stride, d_q_out_stride, d_q_stride, q_weight, Hq};
+    c.t[1] = {k, d_k_out, d_k, k_stride, d_k_out_stride, d_k_stride, k_weight, Hk};
+    return from_cuda(gdr::launch_norm_rope(c, true, d_q_weight, d_k_weight, workspace, elem_of(dtype),
+                                           static_cast<cudaStream_t>(stream)));
 }
 
 gdr_status_t gdr_last_device_error(void *stream) {

@@ -215,6 +215,25 @@ cudaError_t launch_kv8_tile(const void *q, int64_t q_stride, const void *k_cache
                             void *ws, cudaStream_t s);
 cudaError_t take_kv8_tile_error_word(unsigned *value);
 
+// ---- norms of queries and keys with the position rotation (gdr_norm_rope.cu) ----
+struct NormCall {
+    struct Tensor {
+        const void *x, *g;             // input; gradient of the output (backward)
+        void *y;                       // output; gradient of the input (backward)
+        int64_t x_stride, g_stride, y_stride;
+        const float *w;
+        int H;
+    } t[2];                            // queries, keys
+    const int *positions;
+    const double *freq;
+    float eps;
+    bool norm, mean;                   // a norm at all; of the mean square (else the sum)
+    int T, D, rot, pairs;              // pairs: 0 halves, 1 adjacent
+};
+size_t norm_rope_workspace_bytes(int D);
+// dwq, dwk: the weights' gradients or null (ws: norm_rope_workspace_bytes where one is wanted).
+cudaError_t launch_norm_rope(const NormCall &c, bool bwd, float *dwq, float *dwk, void *ws, Elem e, cudaStream_t s);
+
 // ---- the per-chunk gradients of the bf16 d = 128 chunk-64 backward on tcgen05
 // (gdr_bwd_tc.cu): Wt, Sb, dSb are the value-major bf16 tiles [BH][NC][128][64 / 128]
 // (W^T, the states, the state gradients), dR the fp32 [BH][T][128] rows of the reverse

@@ -16,11 +16,10 @@
 // merge kernel follows.  The order of the merge is that of the tokens, so results repeat.
 #pragma once
 
-#include "gdr_fused_common.cuh"
 #include "gdr_kv8.cuh"
+#include "gdr_launch.cuh"
 
 #include <algorithm>
-#include <atomic>
 
 namespace gdr {
 namespace {
@@ -450,39 +449,6 @@ __global__ void __launch_bounds__(256, kv8::kMergeResident) kv8_merge_kernel(con
     }
 }
 
-// SMs of the current device, asked once a device.
-int sm_count() {
-    static std::atomic<int> known[64];
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 152;
-    }
-    const bool in = dev >= 0 && dev < 64;
-    if (in && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
-        cudaGetLastError();
-        return 152;
-    }
-    if (in) known[dev].store(sms, std::memory_order_relaxed);
-    return sms;
-}
-// A launch that may start while the kernel before it in the stream ends (both wait before they
-// read what another kernel writes).
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A &...args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
 // CTAs for as many items as can be divided among the attention's `a.ctas` (each at most one, and
 // there are no more than the requests' blocks of rows), or for every entry where that is not
 // much more: looking for the item takes 1.5 us.  `rows` goes by max_q; where the lengths could be
@@ -513,19 +479,6 @@ void place_parts(AttnArgs &a, void *ws, int ctas, int RB) {
     a.entry = static_cast<int4 *>(ws);
     a.part_ml = reinterpret_cast<float *>(a.entry + ctas);
     a.part_o = a.part_ml + (size_t)ctas * 2 * RB * 2;
-}
-
-// The kernel's shared-memory limit, raised once a device (`done`: one flag a kernel).
-template <typename K>
-cudaError_t allow_smem(K kernel, size_t bytes, std::atomic<uint64_t> &done) {
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess) return e;
-    const uint64_t bit = dev >= 0 && dev < 64 ? (uint64_t)1 << dev : 0;
-    if (bit && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess && bit) done.fetch_or(bit, std::memory_order_release);
-    return e;
 }
 
 }  // namespace

@@ -644,6 +644,61 @@ gdr_status_t gdr_kv8_attn(const void *q, int64_t q_stride, const void *k_cache, 
                           int page, int num_pages, gdr_dtype_t dtype, gdr_kv8_t kv,
                           void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- norms of queries and keys for each head, with the rotation by position ----
+ *
+ * What stands between the projection and a layer: queries and keys of unit length for the
+ * incremental layers (gdr_chunk_fwd, gdr_decode_step), root-mean-square norms with weights and the
+ * rotation by the token's position for the exact ones (gdr_kv8_append, gdr_kv8_attn; gdr_page_plan
+ * gives the positions).  For every token and head of D values x, with p the token's position:
+ *     r = (|x|^2 / N + eps)^-1/2       (N = D for GDR_NORM_RMS, 1 for GDR_NORM_L2; r = 1 for NONE)
+ *     y = R(p) (w x r)                 (w: the tensor's weights, shared by its heads; NULL: ones)
+ * R(p) turns the pairs of the first rot_dim values, pair i by the angle p freq[i]:
+ *     (a, b) -> (a cos - b sin, a sin + b cos)
+ * and leaves the others.
+ */
+typedef enum { GDR_NORM_NONE = 0, GDR_NORM_RMS = 1, GDR_NORM_L2 = 2 } gdr_norm_t;
+typedef enum {
+    GDR_ROPE_HALF = 0,        /* pair i is the values i and i + rot_dim / 2 */
+    GDR_ROPE_ADJACENT = 1     /* pair i is the values 2 i and 2 i + 1       */
+} gdr_rope_t;
+/*
+ *   q, k      [T][Hq][D], [T][Hk][D] dtype, *_stride elements between tokens (at least H * D, rows
+ *             16-byte aligned: slices of a wider projection); Hk = 0: queries only (k, k_out and
+ *             k_weight are not looked at), and the same with Hq
+ *   q_weight, k_weight  fp32 [D] or NULL
+ *   positions [T] int32; a negative one is not a token: its rows of the outputs are left as they
+ *             were.  NULL (with rot_dim 0): all are tokens
+ *   freq      fp64 [rot_dim / 2], radians a position (for example theta^(-2 i / rot_dim)); may be
+ *             NULL with rot_dim 0
+ *   q_out, k_out  as q and k, strides of their own; may be q and k themselves (with their strides)
+ * D a power of two from 16 to 512, rot_dim a multiple of 16 up to D (GDR_ERR_UNSUPPORTED otherwise);
+ * eps finite, >= 0.  Angles are taken modulo a whole turn in 64-bit fixed point, so they are as good
+ * at position 2^31 - 1 as at 1.  Arithmetic in fp32 (|x|^2 overflows where |x| passes 1.8e19),
+ * rounded once.  One launch, no workspace.
+ *
+ * gdr_qk_norm_rope_bwd: the gradients, given those of the outputs (d_q_out, d_k_out, laid out as
+ *   the outputs): with g = R(p)^T dy,  dx = r (w g - x r^2 <w g, x> / N),  dw = the sum of g x r over
+ *   tokens and heads (fp32, in an order that depends on the sizes and the device only).
+ *   d_q, d_k are overwritten (rows of negative positions with zeros); they may be d_q_out and d_k_out,
+ *   or q and k, themselves.  d_q_weight, d_k_weight fp32 [D], overwritten, or NULL: not wanted (then one
+ *   launch and no workspace; else two, and `workspace`: gdr_qk_norm_rope_bwd_workspace_size bytes on the
+ *   current device, 16-byte aligned, scratch on entry and exit).
+ */
+gdr_status_t gdr_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                              const float *q_weight, const float *k_weight, float eps, gdr_norm_t norm,
+                              const int *positions, const double *freq, int rot_dim, gdr_rope_t pairs,
+                              void *q_out, int64_t q_out_stride, void *k_out, int64_t k_out_stride, int T,
+                              int Hq, int Hk, int D, gdr_dtype_t dtype, void *stream);
+size_t gdr_qk_norm_rope_bwd_workspace_size(int D);
+gdr_status_t gdr_qk_norm_rope_bwd(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                  const float *q_weight, const float *k_weight, float eps, gdr_norm_t norm,
+                                  const int *positions, const double *freq, int rot_dim, gdr_rope_t pairs,
+                                  const void *d_q_out, int64_t d_q_out_stride, const void *d_k_out,
+                                  int64_t d_k_out_stride, void *d_q, int64_t d_q_stride, void *d_k,
+                                  int64_t d_k_stride, float *d_q_weight, float *d_k_weight, int T, int Hq,
+                                  int Hk, int D, gdr_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+
 /*
  * Process-wide options, for tests and tuning.  Each takes effect for calls made
  * after it is set, on every thread; the defaults suit production use.
