@@ -762,8 +762,10 @@ def _norm_how(q, k, norm, q_weight, k_weight, positions, freq, pairs):
 def _like(t, out, name):
     """A new tensor of t's shape, or `out`, checked: its pointer and token stride too."""
     if out is None:
-        out = torch.empty(t.shape, dtype=t.dtype, device=t.device)
-    elif out.shape != t.shape or out.dtype is not t.dtype:
+        shape = t.shape
+        out = t.new_empty(shape)
+        return out, out.data_ptr(), shape[1] * shape[2]
+    if out.shape != t.shape or out.dtype is not t.dtype:
         raise ValueError(f"{name} must have its input's shape and dtype")
     return (out, *_rows(out, name))
 

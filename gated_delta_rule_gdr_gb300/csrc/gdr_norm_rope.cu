@@ -14,11 +14,17 @@
 //
 // Work.  A head's values are taken by D / 16 lanes, 16 values each in two pieces of 8: pieces
 // that a pair lies across (or within), so that no value changes lanes but in the row's sums.
-// A warp takes 32 / (D / 16) heads at once, U times over for loads in flight: a unit.  The units of
-// a tensor, tokens in order, are divided evenly among the warps of the CTAs that the tensor
-// got, queries and keys in proportion.
+// A warp takes 32 / (D / 16) heads of a token at once: a pass.  The passes of a tensor, tokens in
+// order, are divided evenly among the warps of the CTAs that the tensor got, queries and keys by
+// their cost.  A lane copies its pieces asynchronously to a place of its own in shared memory, ST - 1
+// passes ahead, so that no registers wait for memory and nothing synchronises.
 //
-// Bound: bytes (forward 2, backward 3 times the tensors).
+// Bound: bytes (forward 2, backward 3 times the tensors).  Measured, 16384 tokens, 32 + 8 heads of
+// 128 bf16 values out of one projection, weights and rotation: forward (336 MB, 50 us at the
+// measured copy rate) 56 us, backward with the weights' gradients (503 MB, 75 us) 84 us; 65536 tokens of
+// 64 heads to unit length (2147 MB, 322 us) 325 us.  With the pieces in registers, four passes'
+// (forward) or two (backward) in flight: 60 and 98 us, since the backward's registers then spill;
+// rings of 4 passes 62 and 88, of 8 forward 65 us.
 
 #include "gdr_launch.cuh"
 
@@ -27,6 +33,11 @@ namespace {
 
 namespace nr {
 constexpr int NT = 256, NW = NT / 32;
+constexpr int CPS = 2;                                            // CTAs an SM
+template <bool BWD> constexpr int ST = 3;                          // passes of a warp's ring
+template <typename E> constexpr uint32_t PIECE = 256 * sizeof(E); // bytes of a warp's pieces of 8 values
+template <typename E, bool BWD> constexpr uint32_t STAGE = (BWD ? 4 : 2) * PIECE<E>;
+constexpr int RUN = 4;         // passes of a warp where there are few
 }
 
 struct NormTensor {
@@ -46,42 +57,49 @@ struct NormArgs {
     bool norm;
 };
 
-// 8 values of a piece, as they come and as floats.
+// 8 values of a piece: brought to the lane's place in shared memory (none: zeros), taken from there as
+// four packed pairs of floats, stored.
 template <typename E> struct Piece;
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool has) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(has ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void lds128(uint32_t src, uint64_t &a, uint64_t &b) {
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(src) : "memory");
+}
 template <> struct Piece<float> {
-    uint4 u[2];
-    __device__ __forceinline__ void load(const float *p) {
-        u[0] = *reinterpret_cast<const uint4 *>(p);
-        u[1] = *reinterpret_cast<const uint4 *>(p + 4);
+    static __device__ __forceinline__ void bring(uint32_t dst, const float *src, bool has) {
+        copy16(dst, src, has);
+        copy16(dst + 512, src + 4, has);
     }
-    __device__ __forceinline__ void zero() { u[0] = u[1] = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float *f) const {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            f[4 * i] = __uint_as_float(u[i].x), f[4 * i + 1] = __uint_as_float(u[i].y);
-            f[4 * i + 2] = __uint_as_float(u[i].z), f[4 * i + 3] = __uint_as_float(u[i].w);
-        }
+    static __device__ __forceinline__ void get(uint32_t src, uint64_t *f) {
+        lds128(src, f[0], f[1]);
+        lds128(src + 512, f[2], f[3]);
     }
-    static __device__ __forceinline__ void store(float *p, const float *f) {
-        *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<float4 *>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+    static __device__ __forceinline__ void store(float *p, const uint64_t *f) {
+        *reinterpret_cast<ulonglong2 *>(p) = make_ulonglong2(f[0], f[1]);
+        *reinterpret_cast<ulonglong2 *>(p + 4) = make_ulonglong2(f[2], f[3]);
     }
 };
 template <> struct Piece<__nv_bfloat16> {
-    uint4 u;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { u = *reinterpret_cast<const uint4 *>(p); }
-    __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float *f) const {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    static __device__ __forceinline__ void bring(uint32_t dst, const __nv_bfloat16 *src, bool has) { copy16(dst, src, has); }
+    static __device__ __forceinline__ void get(uint32_t src, uint64_t *f) {
+        uint64_t u[2];
+        lds128(src, u[0], u[1]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            f[2 * i] = __uint_as_float(w[i] << 16);
-            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            const uint32_t w = (uint32_t)(u[i >> 1] >> (32 * (i & 1)));
+            f[i] = f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
         }
     }
-    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float *f) {
-        *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                                   pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const uint64_t *f) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            f2_unpack(f[i], a, b);
+            w[i] = pack_bf16x2(a, b);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
 };
 
@@ -115,169 +133,254 @@ __device__ __forceinline__ float inverse_root(float x) {
     return rsqrtf(x);
 }
 
-// ROT: 0 no rotation, 1 pairs (i, i + rot / 2), 2 pairs (2 i, 2 i + 1).
+// The rotation of a lane's pairs by its pieces p0 and p1.  ROT 1: pairs (i, i + rot / 2), a piece's values
+// with the other's, two pairs an instruction; ROT 2: pairs (2 i, 2 i + 1) within a piece.
 template <int ROT>
-__device__ __forceinline__ void rotate(float (&f)[16], const float (&cs)[8], const float (&sn)[8], float sign, bool turned) {
-    if (ROT == 0 || !turned) return;
+struct Turn {
+    float c[8], s[8];
+    bool on[2];           // whether the pieces are turned (ROT 1: both or none)
+    __device__ __forceinline__ Turn(int p0, int p1, int rot) { on[0] = 8 * p0 < rot, on[1] = 8 * p1 < rot; }
+    template <typename E>
+    __device__ __forceinline__ void set(const uint64_t *f, int p0, int p1, uint32_t p) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int ia = ROT == 1 ? i : 2 * i, ib = ROT == 1 ? i + 8 : 2 * i + 1;
-        const float a = f[ia], b = f[ib], s = sn[i] * sign;
-        f[ia] = fmaf(a, cs[i], -b * s);
-        f[ib] = fmaf(a, s, b * cs[i]);
+        for (int e = 0; e < 8; ++e)
+            if (on[ROT == 1 ? 0 : e >> 2]) {
+                const uint64_t turns = f[ROT == 1 ? 8 * p0 + e : 4 * (e < 4 ? p0 : p1) + (e & 3)];
+                turn_sincos<E>((uint32_t)((turns * (uint64_t)p) >> 32), s[e], c[e]);
+            }
     }
+    template <bool BACK>
+    __device__ __forceinline__ void apply(uint64_t (&f)[8]) const {
+        if constexpr (ROT == 1) {
+            if (on[0])
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint64_t a = f[e], b = f[e + 4], minus = 0x8000000080000000ull;
+                    const uint64_t c2 = f2_pack(c[2 * e], c[2 * e + 1]), s2 = f2_pack(s[2 * e], s[2 * e + 1]);
+                    f[e] = f2_fma(BACK ? b : b ^ minus, s2, f2_mul(a, c2));
+                    f[e + 4] = f2_fma(BACK ? a ^ minus : a, s2, f2_mul(b, c2));
+                }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (on[e >> 2]) {
+                    float a, b;
+                    f2_unpack(f[e], a, b);
+                    const float sn = BACK ? -s[e] : s[e];
+                    f[e] = f2_pack(fmaf(-b, sn, a * c[e]), fmaf(a, sn, b * c[e]));
+                }
+        }
+    }
+};
+template <> struct Turn<0> {
+    __device__ __forceinline__ Turn(int, int, int) {}
+};
+
+// The sum of a packed pair over the lanes of a head.  LOG: log2 of these lanes, or -1: `log`.
+template <int LOG>
+__device__ __forceinline__ float head_sum(uint64_t v, int log) {
+    float a, b;
+    f2_unpack(v, a, b);
+    a += b;
+    if constexpr (LOG >= 0) {
+#pragma unroll
+        for (int off = 1; off < (1 << LOG); off <<= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
+    } else {
+        for (int off = 1; off < (1 << log); off <<= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
+    }
+    return a;
+}
+__device__ __forceinline__ uint64_t dot8(const uint64_t (&a)[8], const uint64_t (&b)[8]) {
+    uint64_t v = f2_mul(a[0], b[0]);
+#pragma unroll
+    for (int e = 1; e < 8; ++e) v = f2_fma(a[e], b[e], v);
+    return v;
 }
 
-// U: passes of a unit, whose loads are in flight together.  BWD: the backward; DW: and the weights'
-// gradients.
-template <typename E, int ROT, bool BWD, bool DW, int U>
-__global__ void __launch_bounds__(nr::NT, 2) norm_rope_kernel(const NormArgs a) {
+// ROT: 0 no rotation, 1 pairs (i, i + rot / 2), 2 pairs (2 i, 2 i + 1).  LOG: log2 of D / 16, or -1:
+// any.  BWD: the backward; DW: and the weights' gradients.
+template <typename E, int ROT, int LOG, bool BWD, bool DW>
+__global__ void __launch_bounds__(nr::NT, nr::CPS) norm_rope_kernel(const NormArgs a) {
     using nr::NT, nr::NW;
+    constexpr uint32_t PIECE = nr::PIECE<E>, STAGE = nr::STAGE<E, BWD>;
+    constexpr int ST = nr::ST<BWD>;
+    constexpr bool WSM = BWD && DW && ROT != 0;      // the weights in shared memory: registers are short
+    extern __shared__ __align__(16) uint8_t sm[];
     __shared__ uint64_t s_f[ROT ? 256 : 1];
-    __shared__ float s_dw[DW ? NW : 1][DW ? 512 : 1];
+    __shared__ __align__(16) float s_w[WSM ? 512 : 4];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int which = (int)blockIdx.x >= a.split;
     const int cta = which ? blockIdx.x - a.split : blockIdx.x, ctas = which ? gridDim.x - a.split : a.split;
     const NormTensor t = a.t[which];
-    const int plog2 = a.dlog2 - 4, j = lane & ((1 << plog2) - 1), grp = lane >> plog2, HB = 32 >> plog2;
-    // the two pieces; a lane's pairs are 8 j .. 8 j + 7
-    const int lanes_turned = a.rot >> 4;
-    const bool turned = ROT != 0 && j < lanes_turned;
-    const int p0 = ROT == 1 ? (turned ? j : 2 * j) : 2 * j, p1 = ROT == 1 && turned ? j + lanes_turned : p0 + 1;
+    const int plog2 = LOG >= 0 ? LOG : a.dlog2 - 4, D = 16 << plog2;
+    const int j = lane & ((1 << plog2) - 1), grp = lane >> plog2, HB = 32 >> plog2;
+    // the lane's pieces: j and the one that holds the other values of its pairs (ROT 1) or half the head's
+    // on, so that neighbouring lanes have neighbouring pieces; likewise of those that are not turned
+    const int half = ROT == 1 ? a.rot >> 4 : 1 << plog2;
+    const int p0 = j < half ? j : j + half, p1 = p0 + (j < half ? half : (1 << plog2) - half);
+
+    // passes of the tensor in order (token, heads): a warp's run of them
+    const int passes = (t.H + HB - 1) / HB;
+    const int64_t all = (int64_t)a.T * passes, nw = (int64_t)ctas * NW, gw = (int64_t)cta * NW + warp;
+    const int64_t first = all * gw / nw;
+    const int left = (int)(all * (gw + 1) / nw - first);
+    int64_t tok = passes ? first / passes : 0;
+    int c = (int)(first - tok * passes);
+    // this lane's first piece of the pass that is brought next, and of the one that is stored next
+    const int64_t at0 = (c * HB + grp) * D + 8 * p0;
+    const E *xr = static_cast<const E *>(t.x) + tok * t.xs + at0;
+    const E *gr = BWD ? static_cast<const E *>(t.g) + tok * t.gs + at0 : nullptr;
+    E *yr = static_cast<E *>(t.y) + tok * t.ys + at0;
+    const int step = HB * D, back = (passes - 1) * step, p01 = 8 * (p1 - p0);
+    const bool in_last = (passes - 1) * HB + grp < t.H;      // this lane has a head in a token's last pass
+    const uint32_t ring = smem_u32(sm) + (uint32_t)warp * ST * STAGE + 16u * lane;
+    int cl = c, brought = 0;
+    uint32_t fill = 0;
+    auto bring = [&]() {
+        if (brought < left) {
+            const bool has = cl < passes - 1 || in_last;
+            const E *x = has ? xr : static_cast<const E *>(t.x);
+            Piece<E>::bring(ring + fill, x, has);
+            Piece<E>::bring(ring + fill + PIECE, x + (has ? p01 : 0), has);
+            if constexpr (BWD) {
+                const E *g = has ? gr : static_cast<const E *>(t.g);
+                Piece<E>::bring(ring + fill + 2 * PIECE, g, has);
+                Piece<E>::bring(ring + fill + 3 * PIECE, g + (has ? p01 : 0), has);
+            }
+            if (++cl == passes) {
+                cl = 0;
+                xr += t.xs - back;
+                if (BWD) gr += t.gs - back;
+            } else {
+                xr += step;
+                if (BWD) gr += step;
+            }
+            ++brought;
+        }
+        fill = fill == (ST - 1) * STAGE ? 0 : fill + STAGE;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
 
     grid_dependency_wait();
-    if constexpr (ROT != 0) {
-        for (int i = tid; i < a.rot / 2; i += NT) s_f[i] = turn_fraction(a.freq[i]);
-        __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < ST - 1; ++i) bring();
+    // the position of the token at hand and of the next one
+    int p = 0, p_next = 0;
+    if (a.positions && left > 0) {
+        p = a.positions[tok];
+        if (tok + 1 < a.T) p_next = a.positions[tok + 1];
     }
-    float w[16];
+    if constexpr (ROT != 0)
+        for (int i = tid; i < a.rot / 2; i += NT) s_f[i] = turn_fraction(a.freq[i]);
+    uint64_t w[8];
+    if constexpr (WSM) {
+        for (int i = tid; i < D; i += NT) s_w[i] = t.w ? t.w[i] : 1.f;
+    } else {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = t.w ? t.w[8 * (i < 8 ? p0 : p1) + (i & 7)] : 1.f;
-    float dw[DW ? 16 : 1];
+        for (int e = 0; e < 8; ++e) {
+            const int at = 8 * (e < 4 ? p0 : p1) + 2 * (e & 3);
+            w[e] = t.w ? f2_pack(t.w[at], t.w[at + 1]) : f2_pack(1.f, 1.f);
+        }
+    }
+    if constexpr (ROT != 0) __syncthreads();
+    uint64_t dw[DW ? 8 : 1];
     if constexpr (DW)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) dw[i] = 0.f;
+        for (int e = 0; e < 8; ++e) dw[e] = 0;
 
-    const int passes = (t.H + HB - 1) / HB, chunks = (passes + U - 1) / U;
-    const int64_t units = (int64_t)a.T * chunks, nw = (int64_t)ctas * NW, gw = (int64_t)cta * NW + warp;
-    const int64_t u0 = units * gw / nw, u1 = units * (gw + 1) / nw;
-    int64_t tok = chunks ? u0 / chunks : 0;
-    int c = (int)(u0 - tok * chunks);
-    float cs[8] = {}, sn[8] = {};
-    int p = 0;
+    Turn<ROT> turn(p0, p1, a.rot);
     bool fresh = true;
+    uint32_t stage = 0;
 #pragma unroll 1
-    for (int64_t u = u0; u < u1; ++u) {
-        Piece<E> x[U][2], g[BWD ? U : 1][2];
-        const E *xr = static_cast<const E *>(t.x) + tok * t.xs;
-        const E *gr = BWD ? static_cast<const E *>(t.g) + tok * t.gs : nullptr;
+    for (int k = 0; k < left; ++k) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
+        uint64_t f[8], d[BWD ? 8 : 1];
+        Piece<E>::get(ring + stage, f), Piece<E>::get(ring + stage + PIECE, f + 4);
+        if constexpr (BWD) Piece<E>::get(ring + stage + 2 * PIECE, d), Piece<E>::get(ring + stage + 3 * PIECE, d + 4);
+        stage = stage == (ST - 1) * STAGE ? 0 : stage + STAGE;
+        bring();          // into the place that was read in the pass before
+        const bool has = c < passes - 1 || in_last;
+        if (p < 0) {      // not a token: no output, and a gradient of zero (the warp's lanes agree)
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int h = (c * U + i) * HB + grp;
-            if (h < t.H) {
-                const int at = h << a.dlog2;
-                x[i][0].load(xr + at + 8 * p0);
-                x[i][1].load(xr + at + 8 * p1);
-                if constexpr (BWD) {
-                    g[i][0].load(gr + at + 8 * p0);
-                    g[i][1].load(gr + at + 8 * p1);
-                }
-            } else {
-                x[i][0].zero(), x[i][1].zero();
-                if constexpr (BWD) g[i][0].zero(), g[i][1].zero();
-            }
-        }
-        if (fresh && a.positions) {
-            p = a.positions[tok];
-            if constexpr (ROT != 0) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    if (turned) turn_sincos<E>((uint32_t)((s_f[8 * j + i] * (uint64_t)(uint32_t)p) >> 32), sn[i], cs[i]);
-                }
-            }
-        }
-        fresh = false;
-        E *yr = static_cast<E *>(t.y) + tok * t.ys;
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const int h = (c * U + i) * HB + grp, at = h << a.dlog2;
-            float f[16];
-            if (p < 0) {          // not a token: no output, and a gradient of zero (the warp's lanes agree)
-                if (BWD && h < t.H) {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = 0.f;
-                    Piece<E>::store(yr + at + 8 * p0, f);
-                    Piece<E>::store(yr + at + 8 * p1, f);
-                }
-                continue;
-            }
-            x[i][0].get(f), x[i][1].get(f + 8);
+            for (int e = 0; e < 8; ++e) f[e] = 0;
+        } else {
+            if constexpr (ROT != 0)
+                if (fresh) turn.template set<E>(s_f, p0, p1, (uint32_t)p);
+            fresh = false;
             float r = 1.f;
-            if (a.norm) {
-                float ss = 0.f;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) ss = fmaf(f[e], f[e], ss);
-                for (int off = 1; off < (1 << plog2); off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-                r = inverse_root<E>(fmaf(ss, a.inv_n, a.eps));
-            }
+            if (a.norm) r = inverse_root<E>(fmaf(head_sum<LOG>(dot8(f, f), plog2), a.inv_n, a.eps));
+            const uint64_t r2 = f2_pack(r, r);
             if constexpr (!BWD) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) f[e] *= r * w[e];
-                rotate<ROT>(f, cs, sn, 1.f, turned);
+                for (int e = 0; e < 8; ++e) f[e] = f2_mul(f2_mul(f[e], r2), w[e]);
+                if constexpr (ROT != 0) turn.template apply<false>(f);
             } else {
-                float d[16];
-                g[i][0].get(d), g[i][1].get(d + 8);
-                rotate<ROT>(d, cs, sn, -1.f, turned);
-                if constexpr (DW)
-                    if (h < t.H)
+                if constexpr (ROT != 0) turn.template apply<true>(d);
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) dw[e] = fmaf(d[e], f[e] * r, dw[e]);
+                for (int e = 0; e < 8; ++e) f[e] = f2_mul(f[e], r2);          // x r
+                if constexpr (DW)      // a lane without a head has zeros, and r may be infinite
+                    if (has)
 #pragma unroll
-                for (int e = 0; e < 16; ++e) d[e] *= w[e];
+                        for (int e = 0; e < 8; ++e) dw[e] = f2_fma(d[e], f[e], dw[e]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if constexpr (WSM)
+                        lds128(smem_u32(s_w + 8 * (e < 2 ? p0 : p1) + 4 * (e & 1)), w[2 * e], w[2 * e + 1]);
+                    d[2 * e] = f2_mul(d[2 * e], w[2 * e]), d[2 * e + 1] = f2_mul(d[2 * e + 1], w[2 * e + 1]);
+                }
                 if (a.norm) {
-                    float dot = 0.f;
+                    const float dot = -head_sum<LOG>(dot8(d, f), plog2) * a.inv_n;
+                    const uint64_t k2 = f2_pack(dot, dot);
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) dot = fmaf(d[e], f[e], dot);
-                    for (int off = 1; off < (1 << plog2); off <<= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
-                    const float k = -dot * a.inv_n * r * r;
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] = r * fmaf(f[e], k, d[e]);
+                    for (int e = 0; e < 8; ++e) f[e] = f2_mul(r2, f2_fma(f[e], k2, d[e]));
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) f[e] = d[e];
+                    for (int e = 0; e < 8; ++e) f[e] = d[e];
                 }
             }
-            if (h < t.H) {
-                Piece<E>::store(yr + at + 8 * p0, f);
-                Piece<E>::store(yr + at + 8 * p1, f + 8);
-            }
         }
-        if (++c == chunks) c = 0, ++tok, fresh = true;
+        if (has && (BWD || p >= 0)) Piece<E>::store(yr, f), Piece<E>::store(yr + p01, f + 4);
+        if (++c == passes) {
+            c = 0;
+            yr += t.ys - back;
+            p = p_next, fresh = true;
+            ++tok;
+            if (a.positions && tok + 1 < a.T) p_next = a.positions[tok + 1];
+        } else {
+            yr += step;
+        }
     }
     if constexpr (DW) {
         // lanes with the same values, then the warps, in a fixed order
+        float d[16];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f2_unpack(dw[e], d[2 * e], d[2 * e + 1]);
 #pragma unroll
         for (int e = 0; e < 16; ++e)
-            for (int off = 1 << plog2; off < 32; off <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], off);
+            for (int off = 1 << plog2; off < 32; off <<= 1) d[e] += __shfl_xor_sync(0xffffffffu, d[e], off);
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+        static_assert(ST * STAGE >= 512 * sizeof(float) && ST >= 2, "");
+        float *s_dw = reinterpret_cast<float *>(sm);      // [NW][D], over the rings
         if (grp == 0)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s_dw[warp][8 * (e < 8 ? p0 : p1) + (e & 7)] = dw[e];
+            for (int e = 0; e < 16; ++e) s_dw[warp * D + 8 * (e < 8 ? p0 : p1) + (e & 7)] = d[e];
         __syncthreads();
-        for (int i = tid; i < 1 << a.dlog2; i += NT) {
+        for (int i = tid; i < D; i += NT) {
             float s = 0.f;
 #pragma unroll
-            for (int k = 0; k < NW; ++k) s += s_dw[k][i];
-            if (t.part) t.part[((int64_t)cta << a.dlog2) + i] = s;
+            for (int k = 0; k < NW; ++k) s += s_dw[k * D + i];
+            if (t.part) t.part[(int64_t)cta * D + i] = s;
         }
     }
     grid_launch_dependents();
 }
 
-// The weights' gradients from the CTAs' sums: a CTA for queries and one for keys.
-constexpr int SUM_NT = 1024;
-__global__ void __launch_bounds__(SUM_NT) norm_weight_grad_kernel(const NormArgs a, int ctas, float *dwq, float *dwk) {
-    __shared__ float s_sum[SUM_NT];
-    const int D = 1 << a.dlog2, i = threadIdx.x & (D - 1), s = threadIdx.x >> a.dlog2, ns = SUM_NT >> a.dlog2;
+// The weights' gradients from the CTAs' sums, of queries (blockIdx.x 0) and keys: a CTA for 32 of the
+// D values, a lane for one, the 32 warps for every 32nd CTA's each.
+__global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const NormArgs a, int ctas, float *dwq, float *dwk) {
+    __shared__ float s_sum[32][33];
+    const int D = 1 << a.dlog2, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = 32 * blockIdx.y + lane;
     grid_dependency_wait();
     float *dst = blockIdx.x ? dwk : dwq;
     const float *part = a.t[blockIdx.x].part;
@@ -285,64 +388,70 @@ __global__ void __launch_bounds__(SUM_NT) norm_weight_grad_kernel(const NormArgs
     if (dst) {
         float sum = 0.f;
 #pragma unroll 4
-        for (int c = s; c < n; c += ns) sum += part[((int64_t)c << a.dlog2) + i];
-        s_sum[threadIdx.x] = sum;
+        for (int c = warp; c < n; c += 32) sum += col < D ? part[((int64_t)c << a.dlog2) + col] : 0.f;
+        s_sum[warp][lane] = sum;
         __syncthreads();
-        if (s == 0) {
-            for (int k = 1; k < ns; ++k) sum += s_sum[k * D + i];
-            dst[i] = sum;
-        }
+        sum = s_sum[lane][warp];           // value 32 blockIdx.y + warp, lane's part
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (lane == 0 && 32 * blockIdx.y + warp < D) dst[32 * blockIdx.y + warp] = sum;
     }
     grid_launch_dependents();
 }
 
-constexpr int CTAS_PER_SM = 2;
-int most_ctas() { return CTAS_PER_SM * sm_count(); }
-
-// CTAs of both tensors: a warp for every unit while the device has them, else all that are resident,
-// in proportion to the passes.
-template <int U>
-int divide(NormArgs &a) {
+// CTAs of both tensors: a warp for every RUN passes while the device has them, else all that are
+// resident, in proportion to the passes and (a token's sines and cosines) half a pass a token.
+int divide(NormArgs &a, int per_sm) {
     const int HB = 32 >> (a.dlog2 - 4);
-    int64_t units[2], passes[2];
+    int64_t passes[2], want[2];
     for (int i = 0; i < 2; ++i) {
-        passes[i] = (a.t[i].H + HB - 1) / HB;
-        units[i] = (passes[i] + U - 1) / U * a.T;
+        passes[i] = (int64_t)((a.t[i].H + HB - 1) / HB) * a.T;
+        want[i] = (passes[i] + nr::RUN * nr::NW - 1) / (nr::RUN * nr::NW);
     }
-    const int most = most_ctas();
-    const int64_t want[2] = {(units[0] + nr::NW - 1) / nr::NW, (units[1] + nr::NW - 1) / nr::NW};
+    const int most = per_sm * sm_count();
     if (want[0] + want[1] <= most) {
         a.split = (int)want[0];
         return (int)(want[0] + want[1]);
     }
-    int q = (int)((most * passes[0] + (passes[0] + passes[1]) / 2) / (passes[0] + passes[1]));
+    int64_t cost[2];      // without the half pass 59 us for the forward above
+    for (int i = 0; i < 2; ++i) cost[i] = 2 * passes[i] + (a.rot && passes[i] ? a.T : 0);
+    int q = (int)((most * cost[0] + (cost[0] + cost[1]) / 2) / (cost[0] + cost[1]));
     if (passes[0] && q < 1) q = 1;
     if (passes[1] && q > most - 1) q = most - 1;
     a.split = q;
     return most;
 }
 
-template <typename E, int ROT, bool BWD, bool DW, int U>
-cudaError_t launch_norm_u(NormArgs &a, float *dwq, float *dwk, float *ws, cudaStream_t s) {
-    const int ctas = divide<U>(a);
+template <typename E, int ROT, int LOG, bool BWD, bool DW>
+cudaError_t launch_norm_k(NormArgs &a, float *dwq, float *dwk, float *ws, cudaStream_t s) {
+    const int ctas = divide(a, nr::CPS);
     if (DW) {
         a.t[0].part = ws;
         a.t[1].part = ws + ((size_t)a.split << a.dlog2);
     }
     if (ctas > 0) {
-        cudaError_t e = launch_after(norm_rope_kernel<E, ROT, BWD, DW, U>, dim3((unsigned)ctas), nr::NT, 0, s, a);
+        constexpr size_t smem = (size_t)nr::NW * nr::ST<BWD> * nr::STAGE<E, BWD>;
+        auto kernel = norm_rope_kernel<E, ROT, LOG, BWD, DW>;
+        static std::atomic<uint64_t> allowed{0};
+        cudaError_t e = allow_smem(kernel, smem, allowed);
         if (e != cudaSuccess) return e;
+        if ((e = launch_after(kernel, dim3((unsigned)ctas), nr::NT, smem, s, a)) != cudaSuccess) return e;
     }
     if constexpr (DW)
-        return launch_after(norm_weight_grad_kernel, dim3(2), SUM_NT, 0, s, a, ctas, dwq, dwk);
+        return launch_after(norm_weight_grad_kernel, dim3(2, ((1u << a.dlog2) + 31) / 32), 1024, 0, s, a, ctas, dwq, dwk);
     return cudaSuccess;
+}
+template <typename E, int ROT, int LOG>
+cudaError_t launch_norm_d(NormArgs &a, bool bwd, float *dwq, float *dwk, float *ws, cudaStream_t s) {
+    if (!bwd) return launch_norm_k<E, ROT, LOG, false, false>(a, nullptr, nullptr, nullptr, s);
+    if (dwq || dwk) return launch_norm_k<E, ROT, LOG, true, true>(a, dwq, dwk, ws, s);
+    return launch_norm_k<E, ROT, LOG, true, false>(a, nullptr, nullptr, nullptr, s);
 }
 template <typename E, int ROT>
 cudaError_t launch_norm_r(NormArgs &a, bool bwd, float *dwq, float *dwk, float *ws, cudaStream_t s) {
-    constexpr int U = sizeof(E) == 4 ? 2 : 4;
-    if (!bwd) return launch_norm_u<E, ROT, false, false, U>(a, nullptr, nullptr, nullptr, s);
-    if (dwq || dwk) return launch_norm_u<E, ROT, true, true, U / 2>(a, dwq, dwk, ws, s);
-    return launch_norm_u<E, ROT, true, false, U / 2>(a, nullptr, nullptr, nullptr, s);
+    return a.dlog2 == 7   ? launch_norm_d<E, ROT, 3>(a, bwd, dwq, dwk, ws, s)
+           : a.dlog2 == 6 ? launch_norm_d<E, ROT, 2>(a, bwd, dwq, dwk, ws, s)
+                          : launch_norm_d<E, ROT, -1>(a, bwd, dwq, dwk, ws, s);
 }
 template <typename E>
 cudaError_t launch_norm_e(NormArgs &a, int pairs, bool bwd, float *dwq, float *dwk, float *ws, cudaStream_t s) {
@@ -364,7 +473,7 @@ NormArgs norm_args(const NormCall &c) {
 
 }  // namespace
 
-size_t norm_rope_workspace_bytes(int D) { return (size_t)most_ctas() * D * sizeof(float); }
+size_t norm_rope_workspace_bytes(int D) { return (size_t)nr::CPS * sm_count() * D * sizeof(float); }
 
 cudaError_t launch_norm_rope(const NormCall &c, bool bwd, float *dwq, float *dwk, void *ws, Elem e, cudaStream_t s) {
     NormArgs a = norm_args(c);
