@@ -31,7 +31,7 @@ __all__ = ["GdrError", "load", "chunk_fwd", "decode_step", "chunk_decay", "chunk
            "set_option", "get_option", "option", "mla_decode", "mla_decode_workspace_size",
            "chunk_bwd", "chunk_bwd_workspace_size", "chunk_saved_size", "chunk_fwd_train",
            "chunk_bwd_saved", "page_plan", "kv8_append", "kv8_attn", "kv8_attn_workspace_size",
-           "KV8", "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_size", "NORM", "PAIRS"]
+           "KV8", "kv8_shared_plan", "kv8_attn_shared", "kv8_attn_shared_workspace_size", "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_size", "NORM", "PAIRS"]
 
 DECAY = {"affine": 0, "log": 1}   # gdr_decay_t
 STATUS = {0: "GDR_OK", 1: "GDR_ERR_INVALID_ARG", 2: "GDR_ERR_UNSUPPORTED", 3: "GDR_ERR_RANGE",
@@ -105,6 +105,8 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
         "gdr_page_plan": [vp] * 11 + [i] * 5 + [vp],
         "gdr_page_plan_ex": [vp] * 13 + [i] * 5 + [vp],
         "gdr_kv8_append": [vp, vp, i64, i64, vp, vp, vp, vp, vp, i, i, i, i, i, i, i, vp],
+        "gdr_kv8_shared_plan": [vp] * 6 + [i] * 4 + [vp],
+        "gdr_kv8_attn_shared": [vp, i64] + [vp] * 10 + [f, vp, vp] + [i] * 13 + [vp, sz, vp],
         "gdr_qk_norm_rope": [vp, i64, vp, i64, vp, vp, f, i, vp, vp, i, i, vp, i64, vp, i64] + [i] * 5 + [vp],
         "gdr_qk_norm_rope_bwd": [vp, i64, vp, i64, vp, vp, f, i, vp, vp, i, i, vp, i64, vp, i64, vp, i64, vp,
                                  i64, vp, vp] + [i] * 5 + [vp, sz, vp],
@@ -124,6 +126,8 @@ def load(build_if_missing: bool = False) -> ctypes.CDLL:
     lib.gdr_mla_decode_workspace_size.restype = sz
     lib.gdr_kv8_attn_workspace_size.argtypes = [i] * 7
     lib.gdr_kv8_attn_workspace_size.restype = sz
+    lib.gdr_kv8_attn_shared_workspace_size.argtypes = [i] * 9
+    lib.gdr_kv8_attn_shared_workspace_size.restype = sz
     lib.gdr_qk_norm_rope_bwd_workspace_size.argtypes = [i]
     lib.gdr_qk_norm_rope_bwd_workspace_size.restype = sz
     lib.gdr_get_option.argtypes = [i]
@@ -725,6 +729,74 @@ def kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, scale: 
                             _raw_stream(dev.index))
     if code:
         raise GdrError(code, "gdr_kv8_attn")
+    return (out, lse) if want_lse else out
+
+
+def kv8_shared_plan(block_table, kv_len, cu_group, page: int, *, cu_q=None):
+    """What the requests of each group have in common, for kv8_attn_shared (once a step for all
+    layers).  block_table [S,W], kv_len [S], cu_group [groups + 1] (group g: the requests cu_group[g]
+    up to cu_group[g + 1]) and cu_q [S+1] (None: one query a request) int32.  Returns int32 (shared [S]:
+    tokens of the pages in common, lead [groups]: the request whose row they are read by, -1: none)."""
+    lib = _lib or load()
+    S, W = block_table.shape
+    groups, dev = cu_group.numel() - 1, block_table.device
+    shared = torch.empty(S, dtype=torch.int32, device=dev)
+    lead = torch.empty(max(groups, 0), dtype=torch.int32, device=dev)
+    code = lib.gdr_kv8_shared_plan(_int(block_table, "block_table"), _int(kv_len, "kv_len", (S,)),
+                                   None if cu_q is None else _int(cu_q, "cu_q", (S + 1,)),
+                                   _int(cu_group, "cu_group"), shared.data_ptr(), lead.data_ptr(), S, groups, W, page,
+                                   _raw_stream(dev.index))
+    if code:
+        raise GdrError(code, "gdr_kv8_shared_plan")
+    return shared, lead
+
+
+def kv8_attn_shared_workspace_size(S, max_q, groups, max_group_q, total_q, Hq, Hkv, D, dtype=torch.bfloat16) -> int:
+    """Bytes of workspace kv8_attn_shared needs."""
+    return int(load().gdr_kv8_attn_shared_workspace_size(S, max_q, groups, max_group_q, total_q, Hq, Hkv, D, DTYPE[dtype]))
+
+
+def kv8_attn_shared(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, scale: float, cu_group, shared, lead, *,
+                    cu_q=None, max_q: int = None, max_group_q: int, out=None, want_lse: bool = False, workspace=None):
+    """kv8_attn for requests that share prefixes: the pages that the requests of a group have in common
+    are read once for all of them.  cu_group, shared, lead: kv8_shared_plan's, for these tables and
+    lengths; max_group_q: the most queries that the requests of a group have together; the rest as
+    kv8_attn.  workspace: None (allocated here) or a uint8 CUDA tensor of kv8_attn_shared_workspace_size
+    bytes.  Returns out, or (out, lse) if want_lse."""
+    lib = _lib or load()
+    kv, (N, Hkv, P, D) = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
+    qp, qst = _rows(q, "q")
+    T, Hq, dq = q.shape
+    S, W = block_table.shape
+    groups = cu_group.numel() - 1
+    dtype, dev = q.dtype, k_cache.device
+    if dq != D:
+        raise ValueError(f"q must be [total_q, Hq, {D}]")
+    if out is None:
+        out = torch.empty((T, Hq, D), dtype=dtype, device=dev)
+    elif out.dtype is not dtype or out.shape != q.shape or not out.is_cuda or not out.is_contiguous():
+        raise ValueError("out must be a contiguous CUDA tensor of q's shape and dtype")
+    lse = torch.empty((T, Hq), dtype=torch.float32, device=dev) if want_lse else None
+    if max_q is None:
+        if cu_q is not None:
+            raise ValueError("cu_q wants max_q, the most queries of a request")
+        max_q = 1
+    # 0 as a small one: what the lengths say is computed
+    max_q, max_group_q = max_q or 1, max_group_q or 1
+    el = DTYPE[dtype]
+    need = lib.gdr_kv8_attn_shared_workspace_size(S, max_q, groups, max_group_q, T, Hq, Hkv, D, el)
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+    elif workspace.dtype is not torch.uint8 or not workspace.is_cuda or workspace.numel() < need:
+        raise ValueError(f"workspace must be a uint8 CUDA tensor of at least {need} bytes")
+    code = lib.gdr_kv8_attn_shared(qp, qst, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                                   v_scale.data_ptr(), _int(block_table, "block_table"), _int(kv_len, "kv_len", (S,)),
+                                   None if cu_q is None else _int(cu_q, "cu_q", (S + 1,)), _int(cu_group, "cu_group"),
+                                   _int(shared, "shared", (S,)), _int(lead, "lead", (groups,)), scale, out.data_ptr(),
+                                   None if lse is None else lse.data_ptr(), S, max_q, groups, max_group_q, T, Hq, Hkv,
+                                   D, W, P, N, el, kv, workspace.data_ptr(), need, _raw_stream(dev.index))
+    if code:
+        raise GdrError(code, "gdr_kv8_attn_shared")
     return (out, lse) if want_lse else out
 
 

@@ -32,7 +32,8 @@ def _nvcc() -> str:
 
 
 def sources():
-    return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    # the attention kernels of the 8-bit cache take longest: they begin first
+    return sorted(glob.glob(os.path.join(CSRC, "*.cu")), key=lambda p: ("kv8" not in os.path.basename(p), p))
 
 
 def _deps():

@@ -829,6 +829,60 @@ gdr_status_t gdr_kv8_attn(const void *q, int64_t q_stride, const void *k_cache, 
                                           workspace, static_cast<cudaStream_t>(stream)));
 }
 
+gdr_status_t gdr_kv8_shared_plan(const int *block_table, const int *kv_len, const int *cu_q, const int *cu_group,
+                                 int *shared, int *lead, int S, int num_groups, int table_width, int page, void *stream) {
+    if (S < 0 || num_groups < 0 || table_width < 0) return GDR_ERR_INVALID_ARG;
+    if (!page_ok(page) || S > gdr::kMaxRequests || num_groups > gdr::kMaxRequests ||
+        (int64_t)table_width * page > 0x7fffff00)
+        return GDR_ERR_UNSUPPORTED;
+    if (S == 0 && num_groups == 0) return GDR_OK;
+    if (S == 0 || num_groups == 0 || table_width == 0) return GDR_ERR_INVALID_ARG;
+    if (!block_table || !kv_len || !cu_group || !shared || !lead) return GDR_ERR_INVALID_ARG;
+    if (shared == kv_len || lead == shared || shared == cu_group || lead == cu_group || shared == cu_q || lead == cu_q ||
+        lead == kv_len || shared == block_table || lead == block_table)
+        return GDR_ERR_INVALID_ARG;
+    return from_cuda(gdr::launch_kv8_shared_plan(block_table, kv_len, cu_q, cu_group, shared, lead, S, num_groups,
+                                                 table_width, page, static_cast<cudaStream_t>(stream)));
+}
+
+size_t gdr_kv8_attn_shared_workspace_size(int S, int max_q, int num_groups, int max_group_q, int total_q, int Hq,
+                                          int Hkv, int D, gdr_dtype_t dtype) {
+    if (S <= 0 || max_q <= 0 || num_groups <= 0 || max_group_q <= 0 || total_q <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv)
+        return 0;
+    if (!kv8_shape_ok(Hkv, D, 16, 1, dtype, GDR_KV8_E4M3) || !kv8_heads_ok(Hq, Hkv, total_q, S)) return 0;
+    return gdr::kv8_shared_workspace_bytes(max_q, max_group_q, total_q, Hq, Hkv, D, elem_of(dtype));
+}
+
+gdr_status_t gdr_kv8_attn_shared(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                                 const float *k_scale, const float *v_scale, const int *block_table, const int *kv_len,
+                                 const int *cu_q, const int *cu_group, const int *shared, const int *lead, float scale,
+                                 void *out, float *lse, int S, int max_q, int num_groups, int max_group_q, int total_q,
+                                 int Hq, int Hkv, int D, int table_width, int page, int num_pages, gdr_dtype_t dtype,
+                                 gdr_kv8_t kv, void *workspace, size_t workspace_bytes, void *stream) {
+    if (S < 0 || max_q < 0 || total_q < 0 || Hq < 0 || Hkv < 0 || table_width < 0 || num_pages < 0 || num_groups < 0 ||
+        max_group_q < 0)
+        return GDR_ERR_INVALID_ARG;
+    if (!std::isfinite(scale)) return GDR_ERR_INVALID_ARG;
+    if (!kv8_shape_ok(Hkv, D, page, num_pages, dtype, kv) || num_groups > gdr::kMaxRequests) return GDR_ERR_UNSUPPORTED;
+    if (S == 0 || total_q == 0 || Hq == 0 || max_q == 0) return GDR_OK;
+    if (Hkv == 0 || Hq % Hkv != 0 || table_width == 0 || num_pages == 0 || num_groups == 0 || max_group_q == 0)
+        return GDR_ERR_INVALID_ARG;
+    if (!cu_q && (total_q != S || max_q != 1)) return GDR_ERR_INVALID_ARG;
+    // a unit of keys ends up to 255 tokens past the last one
+    if (!kv8_heads_ok(Hq, Hkv, total_q, S) || (int64_t)table_width * page > 0x7fffff00) return GDR_ERR_UNSUPPORTED;
+    if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !kv_len || !cu_group || !shared || !lead || !out)
+        return GDR_ERR_INVALID_ARG;
+    if (!row_stride_ok(q_stride, Hq, D, dtype == GDR_DTYPE_F32 ? 4 : 2)) return GDR_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out))
+        return GDR_ERR_INVALID_ARG;
+    const size_t need = gdr::kv8_shared_workspace_bytes(max_q, max_group_q, total_q, Hq, Hkv, D, elem_of(dtype));
+    if (!workspace || workspace_bytes < need || !aligned16(workspace)) return GDR_ERR_INVALID_ARG;
+    const gdr::KvSharedCall c{q, q_stride, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, cu_q, cu_group, shared,
+                              lead, scale, out, lse, S, max_q, num_groups, max_group_q, total_q, Hq, Hkv, D, table_width,
+                              page, num_pages, elem_of(dtype), kv8_of(kv)};
+    return from_cuda(gdr::launch_kv8_shared(c, workspace, static_cast<cudaStream_t>(stream)));
+}
+
 // ---- norms of queries and keys with the position rotation ----
 
 gdr_status_t gdr_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,

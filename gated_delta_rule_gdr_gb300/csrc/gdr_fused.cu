@@ -645,7 +645,11 @@ cudaError_t read_and_clear_device_error(cudaStream_t s, unsigned *value) {
     unsigned x = 0, y = 0;
     if (e == cudaSuccess) e = take_kv8_split_error_word(&x);
     if (e == cudaSuccess) e = take_kv8_tile_error_word(&y);
-    *value = a | b | c | d | f | m | t | r | x | y;
+    unsigned z = 0, v = 0, w = 0;
+    if (e == cudaSuccess) e = take_kv8_shared_error_word(&z);
+    if (e == cudaSuccess) e = take_kv8_shared_e4m3_error_word(&v);
+    if (e == cudaSuccess) e = take_kv8_shared_int8_error_word(&w);
+    *value = a | b | c | d | f | m | t | r | x | y | z | v | w;
     return e;
 }
 

@@ -187,7 +187,7 @@ cudaError_t launch_mla_decode(const void *q_abs, const void *ckv, const int *seq
 cudaError_t take_mla_error_word(unsigned *value);
 
 // ---- the 8-bit paged cache: plan (gdr_page.cu), append (gdr_kv8_append.cu), attention
-// (gdr_kv8_attn.cu); arguments as in include/gdr.h, N = num_pages, W = table_width ----
+// (gdr_kv8_attn.cu, gdr_kv8_shared.cu); arguments as in include/gdr.h, N = num_pages, W = table_width ----
 constexpr int kMaxRequests = 8192;
 size_t page_plan_smem(int S);
 cudaError_t launch_page_plan(const int *kv_len, const int *q_len, const int *held, int *table, int *ring,
@@ -214,6 +214,30 @@ cudaError_t launch_kv8_tile(const void *q, int64_t q_stride, const void *k_cache
                             int max_q, int total_q, int Hq, int Hkv, int D, int W, int page, int N, Kv8 kv,
                             void *ws, cudaStream_t s);
 cudaError_t take_kv8_tile_error_word(unsigned *value);
+// Attention of requests that share a prefix (gdr_kv8_shared*.cu).
+struct KvSharedCall {
+    const void *q;
+    int64_t q_stride;
+    const void *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    const int *table, *kv_len, *cu_q, *cu_group, *shared, *lead;
+    float scale;
+    void *out;
+    float *lse;
+    int S, max_q, groups, max_group_q, total_q, Hq, Hkv, D, W, page, N;
+    Elem e;
+    Kv8 kv;
+};
+cudaError_t launch_kv8_shared_plan(const int *table, const int *kv_len, const int *cu_q, const int *cu_group, int *shared,
+                                   int *lead, int S, int groups, int W, int page, cudaStream_t s);
+size_t kv8_shared_workspace_bytes(int max_q, int max_group_q, int total_q, int Hq, int Hkv, int D, Elem e);
+cudaError_t launch_kv8_shared(const KvSharedCall &c, void *ws, cudaStream_t s);
+// One pass in the kernel for many rows; pre_o, pre_ml: the first pass's sums (SharedArgs).
+cudaError_t launch_kv8_shared_e4m3(const KvSharedCall &c, bool first, float *pre_o, float2 *pre_ml, void *parts, cudaStream_t s);
+cudaError_t launch_kv8_shared_int8(const KvSharedCall &c, bool first, float *pre_o, float2 *pre_ml, void *parts, cudaStream_t s);
+cudaError_t take_kv8_shared_error_word(unsigned *value);
+cudaError_t take_kv8_shared_e4m3_error_word(unsigned *value);
+cudaError_t take_kv8_shared_int8_error_word(unsigned *value);
 
 // ---- norms of queries and keys with the position rotation (gdr_norm_rope.cu) ----
 struct NormCall {

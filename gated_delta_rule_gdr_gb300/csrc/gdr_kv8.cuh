@@ -1,5 +1,5 @@
 // gdr_kv8.cuh -- the 8-bit paged cache: codes, scales and addressing shared by the kernels
-// that write it (gdr_kv8_append.cu) and read it (gdr_kv8_attn.cu).
+// that write it (gdr_kv8_append.cu) and read it (gdr_kv8_split.cuh, gdr_kv8_tile.cuh).
 //
 // Keys and values are two arrays of codes [num_pages][Hkv][page][D] (e4m3 or int8) with fp32
 // scales [num_pages][Hkv]: value = code * scale.  A (page, head) block of page * D bytes is

@@ -20,6 +20,7 @@
 #include "gdr_launch.cuh"
 
 #include <algorithm>
+#include <cmath>
 
 namespace gdr {
 namespace {
@@ -36,7 +37,18 @@ constexpr float kVsMin = 9.094947017729282e-13f, kVsMax = 1.099511627776e12f;   
 constexpr int kMergeResident = 4;
 }  // namespace kv8
 
+// One request, as every kernel reads it: offsets and lengths are clamped to the tensors.
+struct Request {
+    int q0, n, kv;
+};
+// A row of an item: its place in q and out, and how many keys it sees.
+struct TileRow {
+    int qrow, hq, lim;
+    bool live;
+};
 struct AttnArgs {
+    using Req = Request;
+    using Row = TileRow;
     const void *q;
     int64_t q_stride;
     const float *ks, *vs;
@@ -55,10 +67,6 @@ struct AttnArgs {
     uint64_t limit_ns;
 };
 
-// One request, as every kernel reads it: offsets and lengths are clamped to the tensors.
-struct Request {
-    int q0, n, kv;
-};
 __device__ __forceinline__ Request request_of(const AttnArgs &a, int s) {
     Request r;
     r.kv = (int)min((int64_t)max(a.kv_len[s], 0), (int64_t)a.W << a.page_log2);
@@ -71,18 +79,103 @@ __device__ __forceinline__ Request request_of(const AttnArgs &a, int s) {
     }
     return r;
 }
+// Where the request's pages begin in the block table.
+__device__ __forceinline__ int64_t table_at(const AttnArgs &a, const Request &, int s) { return (int64_t)s * a.W; }
 // Keys that query i sees, and those that block b of RB rows does (its last row sees the most).
 __device__ __forceinline__ int seen_by(const Request &r, int i) { return max(0, min(r.kv, r.kv - r.n + i + 1)); }
-template <int RB>
-__device__ __forceinline__ int block_end(const AttnArgs &a, const Request &r, int b) {
+
+// Requests that share a prefix (gdr_kv8_attn_shared), in two passes over the same kernels.  The first
+// takes groups for requests: a group's queries stand together in q, and all of them see all of the
+// pages that its requests have in common, which are read by the table row of one of them.  It leaves
+// every row's sums in pre_o, pre_ml.  The second takes the requests without these pages, and joins the
+// first one's sums to a row's own where it is complete.
+struct SharedRequest : Request {
+    int row, skip;               // of the block table: the request's, the entries left out
+    bool all, pre;               // every query sees every key; there are sums of the first pass
+};
+struct SharedRow : TileRow {
+    bool pre;
+};
+struct SharedArgs : AttnArgs {
+    using Req = SharedRequest;
+    using Row = SharedRow;
+    const int *group, *shared, *lead;
+    float *pre_o;                // [total_q][Hq][D]
+    float2 *pre_ml;              // [total_q][Hq]: reference exponent M, weight sum
+    int requests;                // (S: groups in the first pass)
+    bool first;                  // the first pass
+};
+__device__ __forceinline__ int shared_pages(const SharedArgs &a, int s, int kv) {
+    return min(max(a.shared[s], 0), kv) >> a.page_log2;
+}
+__device__ __forceinline__ SharedRequest request_of(const SharedArgs &a, int s) {
+    SharedRequest r;
+    r.row = s, r.skip = 0;
+    r.all = a.first;
+    r.pre = false;
+    const int most = (int)((int64_t)a.W << a.page_log2);
+    auto begin_of = [&](int i) { return a.cu_q ? min(max(a.cu_q[i], 0), a.total_q) : min(i, a.total_q); };
+    if (a.first) {
+        r.row = a.lead[s];
+        r.q0 = r.n = r.kv = 0;
+        if (r.row < 0 || r.row >= a.requests) return r;
+        r.kv = shared_pages(a, r.row, most) << a.page_log2;
+        r.q0 = begin_of(min(max(a.group[s], 0), a.requests));
+        r.n = r.kv > 0 ? max(begin_of(min(max(a.group[s + 1], 0), a.requests)) - r.q0, 0) : 0;
+        return r;
+    }
+    r.kv = min(max(a.kv_len[s], 0), most);
+    r.skip = shared_pages(a, s, r.kv);
+    r.pre = r.skip > 0;
+    r.kv -= r.skip << a.page_log2;
+    r.q0 = begin_of(s);
+    r.n = max(begin_of(s + 1) - r.q0, 0);
+    return r;
+}
+__device__ __forceinline__ int64_t table_at(const SharedArgs &a, const SharedRequest &r, int) { return (int64_t)r.row * a.W + r.skip; }
+__device__ __forceinline__ int seen_by(const SharedRequest &r, int i) {
+    return r.all ? r.kv : max(0, min(r.kv, r.kv - r.n + i + 1));
+}
+
+// Weight 2^(m - ref) of a part whose exponent m is at most the joint one.
+__device__ __forceinline__ float join_weight(float m, float ref);
+// A row's complete sums (o: some of its values, `at` on): true if they are to be written out.  In the
+// passes over shared prefixes they are left for the second one, or joined with the first one's.
+template <int D, int N>
+__device__ __forceinline__ bool complete_row(const AttnArgs &, const Request &, int64_t, int, bool, float (&)[N], float &, float &) {
+    return true;
+}
+template <int D, int N>
+__device__ __forceinline__ bool complete_row(const SharedArgs &a, const SharedRequest &r, int64_t row, int at, bool one, float (&o)[N], float &M,
+                                             float &l) {
+    float *po = a.pre_o + row * D + at;
+    if (a.first) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) po[e] = o[e];
+        if (one) a.pre_ml[row] = make_float2(M, l);
+        return false;
+    }
+    if (r.pre) {
+        const float2 x = a.pre_ml[row];
+        const float top = fmaxf(M, x.x), w = join_weight(M, top), wx = join_weight(x.x, top);
+#pragma unroll
+        for (int e = 0; e < N; ++e) o[e] = fmaf(wx, po[e], o[e] * w);
+        l = fmaf(wx, x.y, l * w);
+        M = top;
+    }
+    return true;
+}
+
+template <int RB, class A>
+__device__ __forceinline__ int block_end(const A &a, const typename A::Req &r, int b) {
     return seen_by(r, (min(r.n * a.G, (b + 1) * RB) - 1) / a.G);
 }
-template <int RB>
-__device__ __forceinline__ int blocks_of(const AttnArgs &a, const Request &r) { return (r.n * a.G + RB - 1) / RB; }
+template <int RB, class A>
+__device__ __forceinline__ int blocks_of(const A &a, const typename A::Req &r) { return (r.n * a.G + RB - 1) / RB; }
 template <int UT>
 __device__ __forceinline__ int units_of(int end) { return max(1, (end + UT - 1) / UT); }
-template <int RB, int UT>
-__device__ __forceinline__ int64_t units_of_head(const AttnArgs &a, const Request &r) {
+template <int RB, int UT, class A>
+__device__ __forceinline__ int64_t units_of_head(const A &a, const typename A::Req &r) {
     const int nb = blocks_of<RB>(a, r);
     int64_t u = 0;
     for (int b = 0; b < nb; ++b) u += units_of<UT>(block_end<RB>(a, r, b));
@@ -100,8 +193,8 @@ struct Place {      // a unit: request, head, block of rows, unit of the block's
 // and its end, as much as E more; what is divided evenly is the sum of both (the units of an
 // item follow its E), or the units alone where a CTA's share would be no more than E.  All NT
 // threads call it; `place` is in shared memory and valid after it returns.
-template <int RB, int UT, int NT, int E>
-__device__ __forceinline__ void find_place(const AttnArgs &a, Place *place, int64_t *s_scan) {
+template <int RB, int UT, int NT, int E, class A>
+__device__ __forceinline__ void find_place(const A &a, Place *place, int64_t *s_scan) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int NW = NT / 32;
     struct Sum {
@@ -113,7 +206,7 @@ __device__ __forceinline__ void find_place(const AttnArgs &a, Place *place, int6
         const int s = base + tid;
         mine = Sum{0, 0};
         if (s < a.S) {
-            const Request r = request_of(a, s);
+            const typename A::Req r = request_of(a, s);
             mine.u = units_of_head<RB, UT>(a, r) * a.Hkv;
             mine.i = (int64_t)blocks_of<RB>(a, r) * a.Hkv;
         }
@@ -164,7 +257,7 @@ __device__ __forceinline__ void find_place(const AttnArgs &a, Place *place, int6
             for (int k = 0; k < 2; ++k) {            // the first unit at or after w0, and after w1
                 const int64_t w = k ? w1 : w0;
                 if (w < at || w >= end) continue;
-                const Request r = request_of(a, base + tid);
+                const typename A::Req r = request_of(a, base + tid);
                 const int64_t per_u = mine.u / a.Hkv, per_i = mine.i / a.Hkv, h = (w - at) / (per_u + e * per_i);
                 int64_t rem = w - at - h * (per_u + e * per_i), u = run.u + before.u + h * per_u;
                 int b = 0;
@@ -195,8 +288,8 @@ __device__ __forceinline__ int cta_of(const Place &p, int64_t u, int64_t i) {
 }
 
 // Moves to the next item: next block, head, request with queries.
-template <int RB>
-__device__ __forceinline__ void next_item(const AttnArgs &a, int &s, int &h, int &b, Request &r) {
+template <int RB, class A>
+__device__ __forceinline__ void next_item(const A &a, int &s, int &h, int &b, typename A::Req &r) {
     if (++b < blocks_of<RB>(a, r)) return;
     b = 0;
     if (++h < a.Hkv) return;
@@ -208,25 +301,25 @@ __device__ __forceinline__ void next_item(const AttnArgs &a, int &s, int &h, int
 }
 
 // A role's way through this CTA's units.
-template <int RB, int UT>
+template <int RB, int UT, class A>
 struct Cursor {
     int s, h, b, t, nt, end;     // item, unit, the item's units and keys
-    Request r;
-    __device__ __forceinline__ void enter(const AttnArgs &a) {
+    typename A::Req r;
+    __device__ __forceinline__ void enter(const A &a) {
         end = block_end<RB>(a, r, b);
         nt = units_of<UT>(end);
     }
-    __device__ __forceinline__ void start(const AttnArgs &a, const Place &p) {
+    __device__ __forceinline__ void start(const A &a, const Place &p) {
         s = p.s, h = p.h, b = p.b, t = p.t;
         r = request_of(a, s);
         enter(a);
     }
-    __device__ __forceinline__ void next_of_item(const AttnArgs &a) {   // past the last item: s = S
+    __device__ __forceinline__ void next_of_item(const A &a) {   // past the last item: s = S
         t = 0;
         next_item<RB>(a, s, h, b, r);
         if (s < a.S) enter(a);
     }
-    __device__ __forceinline__ void next_unit(const AttnArgs &a) {
+    __device__ __forceinline__ void next_unit(const A &a) {
         if (++t == nt) next_of_item(a);
     }
 };
@@ -270,6 +363,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 // 2^(m - ref) for exponents of partial results; 0 for a part that saw nothing.
 __device__ __forceinline__ float part_weight(float m, float ref) { return m == -INFINITY ? 0.f : ex2(m - ref); }
+__device__ __forceinline__ float join_weight(float m, float ref) { return m == ref ? 1.f : part_weight(m, ref); }
 
 // The power of two that brings a row of largest magnitude amax below 2^15, where a half
 // keeps 11 bits of everything that counts (bf16 values exactly, down to 2^-29 of the
@@ -294,8 +388,8 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
 // values: eight loads are in flight at once, since each is a trip to the L2.
 // ROUND: the grid may be too small for the items and rows that there are (max_q says less than
 // the lengths do), and goes round; the loops cost up to 1 us (7 ragged fp32 requests: 22.1 and 23.4 us).
-template <typename E, int D, int RB, int WPR, int RPW, bool ROUND>
-__global__ void __launch_bounds__(256, kv8::kMergeResident) kv8_merge_kernel(const AttnArgs a) {
+template <typename E, int D, int RB, int WPR, int RPW, bool ROUND, class A>
+__global__ void __launch_bounds__(256, kv8::kMergeResident) kv8_merge_kernel(const A a) {
     static_assert(WPR == 1 ? !ROUND : RPW == 1, "");
     constexpr int VL = D / 32;
     __shared__ float s_o[WPR > 1 ? 8 : 1][D];
@@ -308,7 +402,7 @@ __global__ void __launch_bounds__(256, kv8::kMergeResident) kv8_merge_kernel(con
     auto item = [&](int c0) {
         const int4 en = a.entry[c0];
         if (en.x < 0) return;
-        const Request r = request_of(a, en.y);
+        const typename A::Req r = request_of(a, en.y);
         const int rows = min(RB, r.n * a.G - en.w * RB), parts = en.x - c0 + 1;
         constexpr int STEP = 8 / WPR * RPW;
 #pragma unroll 1
@@ -394,8 +488,9 @@ __global__ void __launch_bounds__(256, kv8::kMergeResident) kv8_merge_kernel(con
             for (int rr = 0; rr < RPW; ++rr) {
                 const int row = row0 + rr, at = en.w * RB + row;
                 if (row >= rows) break;
-                const float inv = l[rr] == 0.f ? 0.f : 1.f / l[rr];
                 const int64_t orow = (int64_t)(r.q0 + at / a.G) * a.Hq + en.z * a.G + at % a.G;
+                if (!complete_row<D>(a, r, orow, lane * VL, lane == 0, o[rr], ref[rr], l[rr])) continue;
+                const float inv = l[rr] == 0.f ? 0.f : 1.f / l[rr];
 #pragma unroll
                 for (int e = 0; e < VL; ++e) {
                     if constexpr (sizeof(E) == 4)
@@ -404,7 +499,7 @@ __global__ void __launch_bounds__(256, kv8::kMergeResident) kv8_merge_kernel(con
                         static_cast<__nv_bfloat16 *>(a.out)[orow * D + lane * VL + e] = __float2bfloat16_rn(o[rr][e] * inv);
                 }
                 if (a.lse && lane == 0)
-                    a.lse[orow] = l[rr] == 0.f ? -INFINITY : (M[rr] - kv8::kOff + log2f(l[rr])) * 0.693147180559945f;
+                    a.lse[orow] = l[rr] == 0.f ? -INFINITY : ((ref[rr] == -INFINITY ? 0.f : ref[rr]) - kv8::kOff + log2f(l[rr])) * 0.693147180559945f;
             }
             if constexpr (!ROUND) return;
         }
@@ -453,8 +548,8 @@ __global__ void __launch_bounds__(256, kv8::kMergeResident) kv8_merge_kernel(con
 // there are no more than the requests' blocks of rows), or for every entry where that is not
 // much more: looking for the item takes 1.5 us.  `rows` goes by max_q; where the lengths could be
 // more than that, the wide form goes round and the other has CTAs for what they could be.
-template <typename E, int D, int RB>
-cudaError_t launch_merge(const AttnArgs &a, int64_t rows, cudaStream_t s) {
+template <typename E, int D, int RB, class A>
+cudaError_t launch_merge(const A &a, int64_t rows, cudaStream_t s) {
     constexpr int RPW = RB >= 16 ? 2 : 1;
     const int64_t all = (int64_t)a.total_q * a.G;      // rows of all requests
     const int64_t most = std::min(rows, (int64_t)RB), could = std::min(all, (int64_t)RB);
@@ -464,10 +559,26 @@ cudaError_t launch_merge(const AttnArgs &a, int64_t rows, cudaStream_t s) {
     const unsigned x = (unsigned)items, all_x = (unsigned)std::min(limit * a.Hkv, (int64_t)a.ctas);
     const unsigned wide = (unsigned)most, y = (unsigned)((could + 8 * RPW - 1) / (8 * RPW));
     if (items * most <= kv8::kMergeResident * sm_count()) {
-        if (every && most == could) return launch_after(kv8_merge_kernel<E, D, RB, 8, 1, false>, dim3(x, wide), 256, 0, s, a);
-        return launch_after(kv8_merge_kernel<E, D, RB, 8, 1, true>, dim3(x, wide), 256, 0, s, a);
+        if (every && most == could) return launch_after(kv8_merge_kernel<E, D, RB, 8, 1, false, A>, dim3(x, wide), 256, 0, s, a);
+        return launch_after(kv8_merge_kernel<E, D, RB, 8, 1, true, A>, dim3(x, wide), 256, 0, s, a);
     }
-    return launch_after(kv8_merge_kernel<E, D, RB, 1, RPW, false>, dim3(every ? x : all_x, y), 256, 0, s, a);
+    return launch_after(kv8_merge_kernel<E, D, RB, 1, RPW, false, A>, dim3(every ? x : all_x, y), 256, 0, s, a);
+}
+
+// The arguments of a pass over shared prefixes.
+SharedArgs shared_args(const KvSharedCall &c, bool first, float *pre_o, float2 *pre_ml) {
+    SharedArgs a{};
+    a.q = c.q, a.q_stride = c.q_stride, a.ks = c.k_scale, a.vs = c.v_scale, a.table = c.table, a.kv_len = c.kv_len;
+    a.kc = static_cast<const uint8_t *>(c.k_cache), a.vc = static_cast<const uint8_t *>(c.v_cache);
+    a.cu_q = c.cu_q, a.scale_log2 = fabsf(c.scale) * 1.4426950408889634f, a.sign = c.scale < 0.f ? -1.f : 1.f;
+    a.out = c.out, a.lse = c.lse;
+    a.S = first ? c.groups : c.S, a.requests = c.S;
+    a.total_q = c.total_q, a.Hq = c.Hq, a.Hkv = c.Hkv, a.G = c.Hq / c.Hkv, a.W = c.W, a.N = c.N;
+    a.page_log2 = c.page == 16 ? 4 : c.page == 32 ? 5 : c.page == 64 ? 6 : 7;
+    a.limit_ns = wait_limit_ns();
+    a.group = c.cu_group, a.shared = c.shared, a.lead = c.lead;
+    a.pre_o = pre_o, a.pre_ml = pre_ml, a.first = first;
+    return a;
 }
 
 // Entries, then {M, l}, then the sums.

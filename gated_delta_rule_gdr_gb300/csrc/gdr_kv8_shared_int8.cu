@@ -1,0 +1,15 @@
+// gdr_kv8_shared_int8.cu -- attention of requests that share a prefix (gdr_kv8_attn_shared): its passes in
+// the kernel for many query rows a cached head, int8 codes (a file for each type, to compile side by side).
+
+#include "gdr_kv8_tile.cuh"
+
+namespace gdr {
+
+cudaError_t launch_kv8_shared_int8(const KvSharedCall &c, bool first, float *pre_o, float2 *pre_ml, void *parts, cudaStream_t s) {
+    SharedArgs a = shared_args(c, first, pre_o, pre_ml);
+    return launch_tile_kv<Kv8::INT8>(a, c.D, parts, (int64_t)(first ? c.max_group_q : c.max_q) * a.G, s);
+}
+
+cudaError_t take_kv8_shared_int8_error_word(unsigned *value) { return take_error_word(value); }
+
+}  // namespace gdr

@@ -644,6 +644,47 @@ gdr_status_t gdr_kv8_attn(const void *q, int64_t q_stride, const void *k_cache, 
                           int page, int num_pages, gdr_dtype_t dtype, gdr_kv8_t kv,
                           void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * The same attention for requests that share a prefix: a system prompt, a document that many requests
+ * ask about, samples of one prompt.  Their rows of the block table begin with the same pages (the
+ * prefix's own entries, copied; page_plan then counts them as the request's, so set them to -1 before a
+ * request ends, or the prefix's pages return to the free ring).  gdr_kv8_attn_shared reads such pages
+ * once for all queries of a group of requests instead of once a request; its result is gdr_kv8_attn's
+ * but for rounding.
+ *
+ * gdr_kv8_shared_plan finds what there is to share, once a step for all layers:
+ *   cu_group  [num_groups + 1] int32, ascending: group g is the requests cu_group[g] .. cu_group[g + 1] - 1,
+ *             which stand together in the batch; requests outside every group share nothing
+ *   cu_q      [S+1] or NULL (one query a request), kv_len [S], block_table: as gdr_kv8_attn
+ *   shared    [S] out: tokens of the first pages that the request has in common with all requests of its
+ *             group that have queries: whole pages, equal entries in all these rows, and seen by every
+ *             query of them; 0 where there are none, for a request without queries, or alone with them
+ *   lead      [num_groups] out: the request whose row the group's pages are read by, -1: none
+ * Two launches, no workspace; the outputs must be no inputs.  Errors: S, num_groups or table_width
+ * negative, one of them 0 where the others are not, null pointers: GDR_ERR_INVALID_ARG; S or num_groups
+ * > 8192, another page size, table_width * page > 2^31 - 256: GDR_ERR_UNSUPPORTED.
+ *
+ * gdr_kv8_attn_shared: the arguments of gdr_kv8_attn, the plan's cu_group, and its shared and lead
+ *   for these block_table, kv_len and cu_q (others give wrong results, but read nothing outside the
+ *   tensors).
+ *   max_group_q  the most queries that the requests of a group have together: it chooses a kernel, as
+ *             max_q does
+ *   workspace  16-byte aligned, gdr_kv8_attn_shared_workspace_size bytes: the sums over the common pages
+ *             (fp32, Hq * (D + 2) values a query) and partial results; scratch on entry and exit
+ * Two passes of one to two launches each.  Worth its second pass where the prefix is long beside a
+ * request's own tokens and requests are several (8 requests on 2048 common tokens already).
+ */
+gdr_status_t gdr_kv8_shared_plan(const int *block_table, const int *kv_len, const int *cu_q, const int *cu_group,
+                                 int *shared, int *lead, int S, int num_groups, int table_width, int page, void *stream);
+size_t gdr_kv8_attn_shared_workspace_size(int S, int max_q, int num_groups, int max_group_q, int total_q, int Hq,
+                                          int Hkv, int D, gdr_dtype_t dtype);
+gdr_status_t gdr_kv8_attn_shared(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                                 const float *k_scale, const float *v_scale, const int *block_table, const int *kv_len,
+                                 const int *cu_q, const int *cu_group, const int *shared, const int *lead, float scale,
+                                 void *out, float *lse, int S, int max_q, int num_groups, int max_group_q, int total_q,
+                                 int Hq, int Hkv, int D, int table_width, int page, int num_pages, gdr_dtype_t dtype,
+                                 gdr_kv8_t kv, void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- norms of queries and keys for each head, with the rotation by position ----
  *
  * What stands between the projection and a layer: queries and keys of unit length for the
