@@ -42,7 +42,7 @@ NORM = {None: 0, "none": 0, "rms": 1, "l2": 2}  # gdr_norm_t
 PAIRS = {"half": 0, "adjacent": 1}              # gdr_rope_t
 # gdr_option_t
 OPTIONS = {"wait_limit_ns": 0, "fused_variant": 1, "chain_split": 2, "segments": 3,
-           "bwd_variant": 4}
+           "bwd_variant": 4, "shared_least": 5}
 
 _lib = None
 
@@ -150,7 +150,8 @@ def set_option(name: str, value: int) -> None:
     """Set a process-wide option of the library (gdr_set_option): "wait_limit_ns"
     (0 = every device-side wait gives up at once), "fused_variant" (0 auto, 1 one CTA
     per head, 2 cluster pair), "chain_split" (0 auto, 1, 2), "segments" (0 auto, else
-    the sequence segments of the two-kernel path)."""
+    the sequence segments of the two-kernel path), "shared_least" (common tokens from which
+    kv8_attn_shared reads them in a pass of their own; 0 by a cost model)."""
     _check(load().gdr_set_option(OPTIONS[name], int(value)), "gdr_set_option")
 
 

@@ -108,6 +108,7 @@ std::atomic<int> g_fused_variant{0};
 std::atomic<int> g_chain_split{0};
 std::atomic<int> g_segments{0};
 std::atomic<int> g_bwd_variant{0};
+std::atomic<int> g_shared_least{0};
 
 }  // namespace
 
@@ -117,6 +118,7 @@ int opt_fused_variant() { return g_fused_variant.load(std::memory_order_relaxed)
 int opt_chain_split() { return g_chain_split.load(std::memory_order_relaxed); }
 int opt_segments() { return g_segments.load(std::memory_order_relaxed); }
 int opt_bwd_variant() { return g_bwd_variant.load(std::memory_order_relaxed); }
+int opt_shared_least() { return g_shared_least.load(std::memory_order_relaxed); }
 }  // namespace gdr
 
 extern "C" {
@@ -143,6 +145,10 @@ gdr_status_t gdr_set_option(gdr_option_t option, int64_t value) {
             if (value < 0 || value > 2) return GDR_ERR_INVALID_ARG;
             g_bwd_variant.store((int)value, std::memory_order_relaxed);
             return GDR_OK;
+        case GDR_OPT_SHARED_LEAST:
+            if (value < 0 || value > 0x7fffffff) return GDR_ERR_INVALID_ARG;
+            g_shared_least.store((int)value, std::memory_order_relaxed);
+            return GDR_OK;
     }
     return GDR_ERR_INVALID_ARG;
 }
@@ -153,6 +159,7 @@ int64_t gdr_get_option(gdr_option_t option) {
         case GDR_OPT_FUSED_VARIANT: return gdr::opt_fused_variant();
         case GDR_OPT_CHAIN_SPLIT: return gdr::opt_chain_split();
         case GDR_OPT_SEGMENTS: return gdr::opt_segments();
+        case GDR_OPT_SHARED_LEAST: return gdr::opt_shared_least();
         case GDR_OPT_BWD_VARIANT: return gdr::opt_bwd_variant();
     }
     return -1;
@@ -879,7 +886,7 @@ gdr_status_t gdr_kv8_attn_shared(const void *q, int64_t q_stride, const void *k_
     if (!workspace || workspace_bytes < need || !aligned16(workspace)) return GDR_ERR_INVALID_ARG;
     const gdr::KvSharedCall c{q, q_stride, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, cu_q, cu_group, shared,
                               lead, scale, out, lse, S, max_q, num_groups, max_group_q, total_q, Hq, Hkv, D, table_width,
-                              page, num_pages, elem_of(dtype), kv8_of(kv)};
+                              page, num_pages, elem_of(dtype), kv8_of(kv), 0};
     return from_cuda(gdr::launch_kv8_shared(c, workspace, static_cast<cudaStream_t>(stream)));
 }
 

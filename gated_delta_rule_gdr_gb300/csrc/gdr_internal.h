@@ -62,6 +62,8 @@ int opt_chain_split();
 // most the sequence's chunk count).
 int opt_segments();
 int opt_bwd_variant();
+// Common tokens from which gdr_kv8_attn_shared takes a pass of its own for them: 0 by a cost model.
+int opt_shared_least();
 
 // ---- backward of the chunked form (gdr_bwd.cu) ----
 bool bwd_supported(int dk, int dv, int C);
@@ -227,6 +229,7 @@ struct KvSharedCall {
     int S, max_q, groups, max_group_q, total_q, Hq, Hkv, D, W, page, N;
     Elem e;
     Kv8 kv;
+    int least;      // common tokens that are worth the first pass (set by launch_kv8_shared)
 };
 cudaError_t launch_kv8_shared_plan(const int *table, const int *kv_len, const int *cu_q, const int *cu_group, int *shared,
                                    int *lead, int S, int groups, int W, int page, cudaStream_t s);

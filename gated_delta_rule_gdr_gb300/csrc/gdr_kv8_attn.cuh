@@ -103,10 +103,12 @@ struct SharedArgs : AttnArgs {
     float *pre_o;                // [total_q][Hq][D]
     float2 *pre_ml;              // [total_q][Hq]: reference exponent M, weight sum
     int requests;                // (S: groups in the first pass)
+    int least;                   // common tokens below which a request attends to all of its own alone
     bool first;                  // the first pass
 };
 __device__ __forceinline__ int shared_pages(const SharedArgs &a, int s, int kv) {
-    return min(max(a.shared[s], 0), kv) >> a.page_log2;
+    const int n = a.shared[s];
+    return n < a.least ? 0 : min(max(n, 0), kv) >> a.page_log2;
 }
 __device__ __forceinline__ SharedRequest request_of(const SharedArgs &a, int s) {
     SharedRequest r;
@@ -577,7 +579,7 @@ SharedArgs shared_args(const KvSharedCall &c, bool first, float *pre_o, float2 *
     a.page_log2 = c.page == 16 ? 4 : c.page == 32 ? 5 : c.page == 64 ? 6 : 7;
     a.limit_ns = wait_limit_ns();
     a.group = c.cu_group, a.shared = c.shared, a.lead = c.lead;
-    a.pre_o = pre_o, a.pre_ml = pre_ml, a.first = first;
+    a.pre_o = pre_o, a.pre_ml = pre_ml, a.least = c.least, a.first = first;
     return a;
 }
 

@@ -130,6 +130,42 @@ __global__ void __launch_bounds__(PT) shared_groups_kernel(const PlanArgs a) {
 size_t align32(size_t n) { return (n + 31) & ~(size_t)31; }
 size_t pre_bytes(int total_q, int Hq, int D) { return align32((size_t)total_q * Hq * (D + 2) * sizeof(float)); }
 
+// Common tokens from which on the first pass is worth its time, by the sizes that the host knows.
+//
+// What 128 common tokens of a cached head cost one SM, in us: the split kernel's blocks of 8 or 16 rows
+// (measured: 128 decodes of 8 heads a cached head on 32 k common keys, from the L2 mostly, 502 us = 0.58 a
+// block; fp32 1.0 and 1.6 at D = 128, 0.63 and 1.0 at 64), the tile kernel's copies, tile or pair of
+// tiles (24 x 5 drafted tokens on 16 k 110 us = 1.3; 2.4 a pair).
+// A pass of its own costs 17 us (8 decodes on 4096 common tokens 34 us against 20 in one), 27 where it
+// takes pairs, the sums' way through memory, and the ends of items that are twice as many.
+// Where the two are even: measured / by this rule, 8, 16, 32, 64 decodes with 4 cached heads: 30 / 25, 12 /
+// 11, 7.5 / 8.1, 3.6 / 4.1 thousand common tokens; 24 x 5 drafted 7 / 7.6; prompts of 64 or 300 tokens: none
+// up to 16 k / none, 20.
+// (`rows` of one request or group on average, at most `most`; alike: all have that many, else the last
+// block of each is half full; ends: what the ends of its items cost in units)
+double keys_cost(int64_t most, double rows, bool alike, int D, Elem e, double *ends) {
+    const double narrow = D == 64 ? 0.63 : 1.0;
+    auto blocks = [&](int n) { return alike ? std::ceil(rows / n) : rows / n + 0.5; };
+    *ends = sp::ITEM;
+    if (e == Elem::F32) return most <= 8 ? narrow : 1.6 * narrow * blocks(16);
+    if (most <= 16) return (most <= 8 ? 0.58 : 0.8) * narrow;
+    *ends = most > 128 ? 3 : 8;
+    return most <= 64 ? 1.3 : most <= 128 ? 1.7 : 2.4 * blocks(kKv8TileRows);
+}
+int least_worth(const KvSharedCall &c) {
+    if (opt_shared_least() > 0) return opt_shared_least();
+    const int64_t G = c.Hq / c.Hkv, most = c.max_q * G, gmost = c.max_group_q * G;
+    const double requests = std::min(c.S, c.total_q), sms = sm_count();
+    double ends, gends;
+    const double one = keys_cost(most, c.total_q * G / requests, (int64_t)c.S * c.max_q == c.total_q, c.D, c.e, &ends);
+    const double group = keys_cost(gmost, (double)c.total_q * G / c.groups, c.groups == 1, c.D, c.e, &gends);
+    const double gain = requests * one - c.groups * group;
+    if (gain <= 0) return 0x7fffffff;
+    const double pass = (c.e == Elem::BF16 && gmost > 128 ? 27 : 17) + (double)c.total_q * c.Hq * (8 * c.D + 16) / 3e6 +
+                        requests * c.Hkv * one * ends / sms;
+    return (int)std::min(pass * sms / (gain * c.Hkv) * 128, 2147483647.0);
+}
+
 cudaError_t launch_pass(const KvSharedCall &c, bool first, float *pre_o, float2 *pre_ml, void *parts, cudaStream_t s) {
     const int max_q = first ? c.max_group_q : c.max_q;
     const Shape sh = shape_of(max_q, c.Hq / c.Hkv, c.e);
@@ -156,7 +192,13 @@ size_t kv8_shared_workspace_bytes(int max_q, int max_group_q, int total_q, int H
                                                 shape_workspace_bytes(shape_of(max_q, G, e), D));
 }
 
-cudaError_t launch_kv8_shared(const KvSharedCall &c, void *ws, cudaStream_t s) {
+cudaError_t launch_kv8_shared(const KvSharedCall &call, void *ws, cudaStream_t s) {
+    KvSharedCall c = call;
+    c.least = least_worth(c);
+    if ((int64_t)c.least > (int64_t)c.W * c.page)      // no request can have that many: one pass
+        return launch_kv8_attn(c.q, c.q_stride, c.k_cache, c.v_cache, c.k_scale, c.v_scale, c.table, c.kv_len, c.cu_q,
+                               c.scale, c.out, c.lse, c.S, c.max_q, c.total_q, c.Hq, c.Hkv, c.D, c.W, c.page, c.N, c.e,
+                               c.kv, ws, s);
     float *pre_o = static_cast<float *>(ws);
     float2 *pre_ml = reinterpret_cast<float2 *>(pre_o + (size_t)c.total_q * c.Hq * c.D);
     void *parts = static_cast<uint8_t *>(ws) + pre_bytes(c.total_q, c.Hq, c.D);

@@ -671,8 +671,9 @@ gdr_status_t gdr_kv8_attn(const void *q, int64_t q_stride, const void *k_cache, 
  *             max_q does
  *   workspace  16-byte aligned, gdr_kv8_attn_shared_workspace_size bytes: the sums over the common pages
  *             (fp32, Hq * (D + 2) values a query) and partial results; scratch on entry and exit
- * Two passes of one to two launches each.  Worth its second pass where the prefix is long beside a
- * request's own tokens and requests are several (8 requests on 2048 common tokens already).
+ * Two passes of two launches each, or gdr_kv8_attn's one where the sizes say that a pass of its own costs
+ * more than the common pages (by a cost model; GDR_OPT_SHARED_LEAST forces either): with 32 query and 4
+ * cached heads 8 single tokens want some 25 thousand common tokens, 64 some 4 thousand.
  */
 gdr_status_t gdr_kv8_shared_plan(const int *block_table, const int *kv_len, const int *cu_q, const int *cu_group,
                                  int *shared, int *lead, int S, int num_groups, int table_width, int page, void *stream);
@@ -760,6 +761,9 @@ gdr_status_t gdr_qk_norm_rope_bwd(const void *q, int64_t q_stride, const void *k
  *                          per-chunk gradients on tensor cores), 1 the backward's own
  *                          recomputation with the warp-level-MMA per-chunk kernel,
  *                          2 the same with the tensor-core per-chunk kernel.
+ *   GDR_OPT_SHARED_LEAST   common tokens from which gdr_kv8_attn_shared reads them in a
+ *                          pass of their own: 0 chosen by a cost model of the batch's
+ *                          sizes (default), else that many (1: always).
  * gdr_set_option returns GDR_ERR_INVALID_ARG for an unknown option or a value
  * out of its range; gdr_get_option returns the current value (-1 if unknown).
  * The library reads no environment variable.
@@ -769,7 +773,8 @@ typedef enum {
     GDR_OPT_FUSED_VARIANT = 1,
     GDR_OPT_CHAIN_SPLIT = 2,
     GDR_OPT_SEGMENTS = 3,
-    GDR_OPT_BWD_VARIANT = 4
+    GDR_OPT_BWD_VARIANT = 4,
+    GDR_OPT_SHARED_LEAST = 5
 } gdr_option_t;
 gdr_status_t gdr_set_option(gdr_option_t option, int64_t value);
 int64_t gdr_get_option(gdr_option_t option);

@@ -28,7 +28,8 @@ def _lib():
     if not torch.cuda.is_available():
         pytest.skip("no CUDA device")
     gdr.load(build_if_missing=True)
-    yield
+    with gdr.option(shared_least=1):        # both passes, however little there is to share
+        yield
     torch.cuda.synchronize()
     assert gdr.last_device_error() == 0
 
@@ -295,3 +296,22 @@ def test_waits_give_up(qs, rows):
         assert gdr.last_device_error() == 5
     check(x, attend(x, d, plan=plan, packed=True))
     assert gdr.last_device_error() == 0
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_chosen_by_sizes(dtype):
+    """By the cost model, and with a bound between two groups' prefixes: in one pass, in two, mixed."""
+    for groups in ([(4, [(9, 1)] * 5)], [(400, [(20, 1)] * 30), (2, [(7, 1)] * 4)],
+                   [(90, [(9, 2), (40, 3)]), (20, [(9, 1)] * 6)]):
+        x = case(groups, 16, 2, 128, 16, dtype, "e4m3", seed=16)
+        for least in (0, 500, 2 ** 31 - 1):
+            with gdr.option(shared_least=least):
+                check(x)
+
+
+def test_option():
+    for bad in (-1, 2 ** 31):
+        with pytest.raises(gdr.GdrError):
+            gdr.set_option("shared_least", bad)
+    with gdr.option(shared_least=77):
+        assert gdr.get_option("shared_least") == 77
