@@ -82,7 +82,7 @@ __device__ __forceinline__ Request request_of(const AttnArgs &a, int s) {
 // Where the request's pages begin in the block table.
 __device__ __forceinline__ int64_t table_at(const AttnArgs &a, const Request &, int s) { return (int64_t)s * a.W; }
 // Keys that query i sees, and those that block b of RB rows does (its last row sees the most).
-__device__ __forceinline__ int seen_by(const Request &r, int i) { return max(0, min(r.kv, r.kv - r.n + i + 1)); }
+__device__ __forceinline__ int seen_by(const AttnArgs &, const Request &r, int i) { return max(0, min(r.kv, r.kv - r.n + i + 1)); }
 
 // Requests that share a prefix (gdr_kv8_attn_shared), in two passes over the same kernels.  The first
 // takes groups for requests: a group's queries stand together in q, and all of them see all of the
@@ -90,13 +90,14 @@ __device__ __forceinline__ int seen_by(const Request &r, int i) { return max(0, 
 // every row's sums in pre_o, pre_ml.  The second takes the requests without these pages, and joins the
 // first one's sums to a row's own where it is complete.
 struct SharedRequest : Request {
-    int row, skip;               // of the block table: the request's, the entries left out
-    bool all, pre;               // every query sees every key; there are sums of the first pass
+    int row, skip;               // of the block table: the request's, the entries left out (the first pass's)
 };
 struct SharedRow : TileRow {
     bool pre;
 };
+template <bool FIRST>            // the first pass
 struct SharedArgs : AttnArgs {
+    static constexpr bool first = FIRST;
     using Req = SharedRequest;
     using Row = SharedRow;
     const int *group, *shared, *lead;
@@ -104,20 +105,19 @@ struct SharedArgs : AttnArgs {
     float2 *pre_ml;              // [total_q][Hq]: reference exponent M, weight sum
     int requests;                // (S: groups in the first pass)
     int least;                   // common tokens below which a request attends to all of its own alone
-    bool first;                  // the first pass
 };
-__device__ __forceinline__ int shared_pages(const SharedArgs &a, int s, int kv) {
+template <bool F>
+__device__ __forceinline__ int shared_pages(const SharedArgs<F> &a, int s, int kv) {
     const int n = a.shared[s];
     return n < a.least ? 0 : min(max(n, 0), kv) >> a.page_log2;
 }
-__device__ __forceinline__ SharedRequest request_of(const SharedArgs &a, int s) {
+template <bool F>
+__device__ __forceinline__ SharedRequest request_of(const SharedArgs<F> &a, int s) {
     SharedRequest r;
     r.row = s, r.skip = 0;
-    r.all = a.first;
-    r.pre = false;
     const int most = (int)((int64_t)a.W << a.page_log2);
     auto begin_of = [&](int i) { return a.cu_q ? min(max(a.cu_q[i], 0), a.total_q) : min(i, a.total_q); };
-    if (a.first) {
+    if constexpr (F) {
         r.row = a.lead[s];
         r.q0 = r.n = r.kv = 0;
         if (r.row < 0 || r.row >= a.requests) return r;
@@ -125,18 +125,20 @@ __device__ __forceinline__ SharedRequest request_of(const SharedArgs &a, int s) 
         r.q0 = begin_of(min(max(a.group[s], 0), a.requests));
         r.n = r.kv > 0 ? max(begin_of(min(max(a.group[s + 1], 0), a.requests)) - r.q0, 0) : 0;
         return r;
+    } else {
+        r.kv = min(max(a.kv_len[s], 0), most);
+        r.skip = shared_pages(a, s, r.kv);
+        r.kv -= r.skip << a.page_log2;
+        r.q0 = begin_of(s);
+        r.n = max(begin_of(s + 1) - r.q0, 0);
+        return r;
     }
-    r.kv = min(max(a.kv_len[s], 0), most);
-    r.skip = shared_pages(a, s, r.kv);
-    r.pre = r.skip > 0;
-    r.kv -= r.skip << a.page_log2;
-    r.q0 = begin_of(s);
-    r.n = max(begin_of(s + 1) - r.q0, 0);
-    return r;
 }
-__device__ __forceinline__ int64_t table_at(const SharedArgs &a, const SharedRequest &r, int) { return (int64_t)r.row * a.W + r.skip; }
-__device__ __forceinline__ int seen_by(const SharedRequest &r, int i) {
-    return r.all ? r.kv : max(0, min(r.kv, r.kv - r.n + i + 1));
+template <bool F>
+__device__ __forceinline__ int64_t table_at(const SharedArgs<F> &a, const SharedRequest &r, int) { return (int64_t)r.row * a.W + r.skip; }
+template <bool F>
+__device__ __forceinline__ int seen_by(const SharedArgs<F> &a, const SharedRequest &r, int i) {
+    return F ? r.kv : max(0, min(r.kv, r.kv - r.n + i + 1));
 }
 
 // Weight 2^(m - ref) of a part whose exponent m is at most the joint one.
@@ -147,17 +149,16 @@ template <int D, int N>
 __device__ __forceinline__ bool complete_row(const AttnArgs &, const Request &, int64_t, int, bool, float (&)[N], float &, float &) {
     return true;
 }
-template <int D, int N>
-__device__ __forceinline__ bool complete_row(const SharedArgs &a, const SharedRequest &r, int64_t row, int at, bool one, float (&o)[N], float &M,
+template <int D, int N, bool F>
+__device__ __forceinline__ bool complete_row(const SharedArgs<F> &a, const SharedRequest &r, int64_t row, int at, bool one, float (&o)[N], float &M,
                                              float &l) {
     float *po = a.pre_o + row * D + at;
-    if (a.first) {
+    if constexpr (F) {
 #pragma unroll
         for (int e = 0; e < N; ++e) po[e] = o[e];
         if (one) a.pre_ml[row] = make_float2(M, l);
         return false;
-    }
-    if (r.pre) {
+    } else if (r.skip > 0) {
         const float2 x = a.pre_ml[row];
         const float top = fmaxf(M, x.x), w = join_weight(M, top), wx = join_weight(x.x, top);
 #pragma unroll
@@ -170,7 +171,7 @@ __device__ __forceinline__ bool complete_row(const SharedArgs &a, const SharedRe
 
 template <int RB, class A>
 __device__ __forceinline__ int block_end(const A &a, const typename A::Req &r, int b) {
-    return seen_by(r, (min(r.n * a.G, (b + 1) * RB) - 1) / a.G);
+    return seen_by(a, r, (min(r.n * a.G, (b + 1) * RB) - 1) / a.G);
 }
 template <int RB, class A>
 __device__ __forceinline__ int blocks_of(const A &a, const typename A::Req &r) { return (r.n * a.G + RB - 1) / RB; }
@@ -568,18 +569,19 @@ cudaError_t launch_merge(const A &a, int64_t rows, cudaStream_t s) {
 }
 
 // The arguments of a pass over shared prefixes.
-SharedArgs shared_args(const KvSharedCall &c, bool first, float *pre_o, float2 *pre_ml) {
-    SharedArgs a{};
+template <bool FIRST>
+SharedArgs<FIRST> shared_args(const KvSharedCall &c, float *pre_o, float2 *pre_ml) {
+    SharedArgs<FIRST> a{};
     a.q = c.q, a.q_stride = c.q_stride, a.ks = c.k_scale, a.vs = c.v_scale, a.table = c.table, a.kv_len = c.kv_len;
     a.kc = static_cast<const uint8_t *>(c.k_cache), a.vc = static_cast<const uint8_t *>(c.v_cache);
     a.cu_q = c.cu_q, a.scale_log2 = fabsf(c.scale) * 1.4426950408889634f, a.sign = c.scale < 0.f ? -1.f : 1.f;
     a.out = c.out, a.lse = c.lse;
-    a.S = first ? c.groups : c.S, a.requests = c.S;
+    a.S = FIRST ? c.groups : c.S, a.requests = c.S;
     a.total_q = c.total_q, a.Hq = c.Hq, a.Hkv = c.Hkv, a.G = c.Hq / c.Hkv, a.W = c.W, a.N = c.N;
     a.page_log2 = c.page == 16 ? 4 : c.page == 32 ? 5 : c.page == 64 ? 6 : 7;
     a.limit_ns = wait_limit_ns();
     a.group = c.cu_group, a.shared = c.shared, a.lead = c.lead;
-    a.pre_o = pre_o, a.pre_ml = pre_ml, a.least = c.least, a.first = first;
+    a.pre_o = pre_o, a.pre_ml = pre_ml, a.least = c.least;
     return a;
 }
 

@@ -166,13 +166,14 @@ int least_worth(const KvSharedCall &c) {
     return (int)std::min(pass * sms / (gain * c.Hkv) * 128, 2147483647.0);
 }
 
-cudaError_t launch_pass(const KvSharedCall &c, bool first, float *pre_o, float2 *pre_ml, void *parts, cudaStream_t s) {
-    const int max_q = first ? c.max_group_q : c.max_q;
+template <bool FIRST>
+cudaError_t launch_pass(const KvSharedCall &c, float *pre_o, float2 *pre_ml, void *parts, cudaStream_t s) {
+    const int max_q = FIRST ? c.max_group_q : c.max_q;
     const Shape sh = shape_of(max_q, c.Hq / c.Hkv, c.e);
     if (sh == Shape::TILE)
-        return c.kv == Kv8::E4M3 ? launch_kv8_shared_e4m3(c, first, pre_o, pre_ml, parts, s)
-                                 : launch_kv8_shared_int8(c, first, pre_o, pre_ml, parts, s);
-    SharedArgs a = shared_args(c, first, pre_o, pre_ml);
+        return c.kv == Kv8::E4M3 ? launch_kv8_shared_e4m3(c, FIRST, pre_o, pre_ml, parts, s)
+                                 : launch_kv8_shared_int8(c, FIRST, pre_o, pre_ml, parts, s);
+    SharedArgs<FIRST> a = shared_args<FIRST>(c, pre_o, pre_ml);
     return launch_split_any(a, sh, c.k_cache, c.v_cache, c.D, c.e, c.kv, parts, (int64_t)max_q * a.G, s);
 }
 
@@ -202,9 +203,9 @@ cudaError_t launch_kv8_shared(const KvSharedCall &call, void *ws, cudaStream_t s
     float *pre_o = static_cast<float *>(ws);
     float2 *pre_ml = reinterpret_cast<float2 *>(pre_o + (size_t)c.total_q * c.Hq * c.D);
     void *parts = static_cast<uint8_t *>(ws) + pre_bytes(c.total_q, c.Hq, c.D);
-    cudaError_t e = launch_pass(c, true, pre_o, pre_ml, parts, s);
+    cudaError_t e = launch_pass<true>(c, pre_o, pre_ml, parts, s);
     if (e != cudaSuccess) return e;
-    return launch_pass(c, false, pre_o, pre_ml, parts, s);
+    return launch_pass<false>(c, pre_o, pre_ml, parts, s);
 }
 
 cudaError_t take_kv8_shared_error_word(unsigned *value) { return take_error_word(value); }

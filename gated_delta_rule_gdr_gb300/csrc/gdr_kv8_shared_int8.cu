@@ -6,8 +6,12 @@
 namespace gdr {
 
 cudaError_t launch_kv8_shared_int8(const KvSharedCall &c, bool first, float *pre_o, float2 *pre_ml, void *parts, cudaStream_t s) {
-    SharedArgs a = shared_args(c, first, pre_o, pre_ml);
-    return launch_tile_kv<Kv8::INT8>(a, c.D, parts, (int64_t)(first ? c.max_group_q : c.max_q) * a.G, s);
+    if (first) {
+        SharedArgs<true> a = shared_args<true>(c, pre_o, pre_ml);
+        return launch_tile_kv<Kv8::INT8>(a, c.D, parts, (int64_t)c.max_group_q * a.G, s);
+    }
+    SharedArgs<false> a = shared_args<false>(c, pre_o, pre_ml);
+    return launch_tile_kv<Kv8::INT8>(a, c.D, parts, (int64_t)c.max_q * a.G, s);
 }
 
 cudaError_t take_kv8_shared_int8_error_word(unsigned *value) { return take_error_word(value); }

@@ -253,13 +253,13 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
             for (int e = 0; e < 2; ++e) {
                 const int r2 = 8 * n + 2 * t4 + e;
                 cs[n][e] = __shfl_sync(0xffffffffu, csg, 4 * (2 * t4 + e));
-                lim[n][e] = r2 < rows ? seen_by(c.r, (row0 + r2) / a.G) : 0;
+                lim[n][e] = r2 < rows ? seen_by(a, c.r, (row0 + r2) / a.G) : 0;
                 M[n][e] = -INFINITY;
                 l[n][e] = 0.f;
             }
         }
         // the fewest keys that a row of the item sees: below them no mask is needed
-        const int lim_all = seen_by(c.r, row0 / a.G);
+        const int lim_all = seen_by(a, c.r, row0 / a.G);
         float o[R][NVT][4];     // value LO g + 2 j + (k >> 1) of row 8 n + 2 t4 + (k & 1)
 #pragma unroll
         for (int n = 0; n < R; ++n)

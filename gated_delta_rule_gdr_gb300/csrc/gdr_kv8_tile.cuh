@@ -151,7 +151,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
 
 // A query row of the item that block b of RB rows is.
 __device__ __forceinline__ void note_prefix(TileRow &, const Request &) {}
-__device__ __forceinline__ void note_prefix(SharedRow &t, const SharedRequest &r) { t.pre = r.pre; }
+__device__ __forceinline__ void note_prefix(SharedRow &t, const SharedRequest &r) { t.pre = r.skip > 0; }
 template <int RB, class A>
 __device__ __forceinline__ typename A::Row tile_row(const A &a, const Cursor<RB, tl::UT, A> &c, int lr) {
     typename A::Row t;
@@ -161,7 +161,7 @@ __device__ __forceinline__ typename A::Row tile_row(const A &a, const Cursor<RB,
     const int i = t.live ? at / a.G : 0;
     t.qrow = c.r.q0 + i;
     t.hq = c.h * a.G + (t.live ? at - i * a.G : 0);
-    t.lim = t.live ? seen_by(c.r, i) : 0x3fffffff;   // a row that is not there needs no mask
+    t.lim = t.live ? seen_by(a, c.r, i) : 0x3fffffff;   // a row that is not there needs no mask
     return t;
 }
 
@@ -530,46 +530,50 @@ __device__ __forceinline__ void store32(void *p, const uint32_t *w, bool wide) {
         reinterpret_cast<uint4 *>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
     }
 }
-// How a row ends: what its sums are multiplied with; of the passes over a shared prefix also where they
-// go in the first one, and in the second the first one's, with their factor.
+// How a row ends: what its sums are multiplied with, and in the second pass over a shared prefix also the
+// first one's sums with their factor.
 struct RowEnd {
     float f;
 };
 struct SharedEnd {
     float f, fx;
-    float *pre;              // null: there is no first pass
+    const float *pre;        // null: there are none
 };
 template <int D>
 __device__ __forceinline__ RowEnd end_row(const AttnArgs &, const TileRow &, bool, float, float &l) {
     return RowEnd{l == 0.f ? 0.f : 1.f / l};
 }
 template <int D>
-__device__ __forceinline__ SharedEnd end_row(const SharedArgs &a, const SharedRow &t, bool whole, float &M, float &l) {
+__device__ __forceinline__ RowEnd end_row(const SharedArgs<true> &, const TileRow &, bool, float, float &) { return RowEnd{1.f}; }
+template <int D>
+__device__ __forceinline__ SharedEnd end_row(const SharedArgs<false> &a, const SharedRow &t, bool whole, float &M, float &l) {
     SharedEnd x{1.f, 0.f, nullptr};
-    if (!t.live) return x;
-    const int64_t row = (int64_t)t.qrow * a.Hq + t.hq;
-    if (a.first || (whole && t.pre)) x.pre = a.pre_o + row * D;
-    if (x.pre && !a.first) {
+    if (whole && t.live && t.pre) {
+        const int64_t row = (int64_t)t.qrow * a.Hq + t.hq;
         const float2 m = a.pre_ml[row];
         const float top = fmaxf(M, m.x);
         x.f = join_weight(M, top), x.fx = join_weight(m.x, top);
+        x.pre = a.pre_o + row * D;
         l = fmaf(x.fx, m.y, l * x.f);
         M = top;
     }
-    const float inv = a.first ? 1.f : l == 0.f ? 0.f : 1.f / l;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
     x.f *= inv, x.fx *= inv;
     return x;
 }
-__device__ __forceinline__ float *first_pass(const RowEnd &) { return nullptr; }
-__device__ __forceinline__ float *first_pass(const SharedEnd &x) { return x.pre; }
-__device__ __forceinline__ bool left_for_second(const AttnArgs &) { return false; }
-__device__ __forceinline__ bool left_for_second(const SharedArgs &a) { return a.first; }
-__device__ __forceinline__ void join_chunk(const RowEnd &, int, float (&)[32]) {}
-__device__ __forceinline__ void join_chunk(const SharedEnd &x, int cb, float (&o)[32]) {
+// Where a row's complete sums stay, null: they are written out.
+template <int D> __device__ __forceinline__ float *left_at(const AttnArgs &, const TileRow &) { return nullptr; }
+template <int D> __device__ __forceinline__ float *left_at(const SharedArgs<true> &a, const TileRow &t) {
+    return a.pre_o + ((int64_t)t.qrow * a.Hq + t.hq) * D;
+}
+// 16 values from `at` on (a store's: the memory clobber between two keeps the second's loads behind the
+// first, and registers are short here).
+__device__ __forceinline__ void join_values(const RowEnd &, int, float *) {}
+__device__ __forceinline__ void join_values(const SharedEnd &x, int at, float *o) {
     if (!x.pre) return;
 #pragma unroll
-    for (int e = 0; e < 32; e += 4) {
-        const float4 p = *reinterpret_cast<const float4 *>(x.pre + 32 * cb + e);
+    for (int e = 0; e < 16; e += 4) {
+        const float4 p = *reinterpret_cast<const float4 *>(x.pre + at + e);
         o[e] = fmaf(x.fx, p.x, o[e]), o[e + 1] = fmaf(x.fx, p.y, o[e + 1]);
         o[e + 2] = fmaf(x.fx, p.z, o[e + 2]), o[e + 3] = fmaf(x.fx, p.w, o[e + 3]);
     }
@@ -579,34 +583,38 @@ __device__ __forceinline__ void write_chunk(const A &a, const typename A::Row &t
                                             const End &end, float (&o)[32]) {
     if (!t.live) return;
     uint32_t w[32];
-    if (whole && !left_for_second(a)) {
+    float *left = left_at<D>(a, t);
+    if (whole && !left) {
         __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(a.out) + ((int64_t)t.qrow * a.Hq + t.hq) * D + 32 * cb;
 #pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] *= end.f;
-        join_chunk(end, cb, o);
+        for (int h = 0; h < 2; ++h) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+            for (int e = 0; e < 16; ++e) o[16 * h + e] *= end.f;
+            join_values(end, 32 * cb + 16 * h, o + 16 * h);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) store32(dst + 16 * e, w + 8 * e, a.wide);
+            for (int e = 0; e < 8; ++e) w[e] = pack_bf16x2(o[16 * h + 2 * e], o[16 * h + 2 * e + 1]);
+            store32(dst + 16 * h, w, a.wide);
+        }
     } else {
-        float *dst = (whole ? first_pass(end) : a.part_o + slot * D) + 32 * cb;
+        float *dst = (whole ? left : a.part_o + slot * D) + 32 * cb;
 #pragma unroll
         for (int e = 0; e < 32; ++e) w[e] = __float_as_uint(o[e]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) store32(dst + 8 * e, w + 8 * e, a.wide);
     }
 }
-__device__ __forceinline__ void leave_stats(const AttnArgs &, int64_t, float, float) {}
-__device__ __forceinline__ void leave_stats(const SharedArgs &a, int64_t row, float M, float l) { a.pre_ml[row] = make_float2(M, l); }
+__device__ __forceinline__ bool leave_stats(const AttnArgs &, int64_t, float, float) { return false; }
+__device__ __forceinline__ bool leave_stats(const SharedArgs<true> &a, int64_t row, float M, float l) {
+    a.pre_ml[row] = make_float2(M, l);
+    return true;
+}
 template <class A>
 __device__ __forceinline__ void write_stats(const A &a, const typename A::Row &t, bool whole, int64_t slot, float M, float l) {
     if (!t.live) return;
     const int64_t row = (int64_t)t.qrow * a.Hq + t.hq;
     if (!whole)
         *reinterpret_cast<float2 *>(a.part_ml + 2 * slot) = make_float2(M, l);
-    else if (left_for_second(a))
-        leave_stats(a, row, M, l);
-    else if (a.lse)
+    else if (!leave_stats(a, row, M, l) && a.lse)
         a.lse[row] = l == 0.f ? -INFINITY : ((M == -INFINITY ? 0.f : M) - kv8::kOff + log2f(l)) * 0.693147180559945f;
 }
 
@@ -1226,7 +1234,8 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const A a) {
 
 // What the rows' 32-byte stores go to.
 uintptr_t stored_at(const AttnArgs &a) { return reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.part_o); }
-uintptr_t stored_at(const SharedArgs &a) { return stored_at(static_cast<const AttnArgs &>(a)) | reinterpret_cast<uintptr_t>(a.pre_o); }
+template <bool F>
+uintptr_t stored_at(const SharedArgs<F> &a) { return stored_at(static_cast<const AttnArgs &>(a)) | reinterpret_cast<uintptr_t>(a.pre_o); }
 template <Kv8 KV, int D, bool PAIR, int NC, int GR, class A>
 cudaError_t launch_tile_g(A &a, void *ws, int ctas, int64_t rows, cudaStream_t s) {
     using L = tl::Lay<D, PAIR, NC>;
