@@ -6,8 +6,14 @@ state of every incremental layer and its sequence length.  A step takes each slo
 tokens (a prompt, a chunk of one, one decoded token, none, or "finished") and runs
 
     page_plan                                   places for the new tokens, once a step
-    incremental layer:  chunk_fwd_varlen, or decode_step where every slot has one token
-    exact layer:        kv8_append, kv8_attn
+    incremental layer:  qk_norm_rope (unit length), chunk_fwd_varlen, or decode_step where every slot has
+                        one token
+    exact layer:        qk_norm_rope (with --theta: root-mean-square norms and the rotation by the plan's
+                        positions), kv8_append, kv8_attn
+
+With a common prefix (share(), --prefix) its tokens run once: every request's row of the block table begins
+with the prefix's pages and its states with the prefix's, and the exact layers read these pages once for
+all slots (kv8_shared_plan once a step, kv8_attn_shared).
 
 Weights are random; the linear maps around the layers are plain matrix products.
 
@@ -35,7 +41,7 @@ class HybridDecoder:
     """Blocks of one incremental and one exact-attention layer each, with their caches."""
 
     def __init__(self, slots, pages, table_width, *, blocks=2, vocab=1000, width=512, heads=4,
-                 q_heads=8, kv_heads=2, page=32, codes=torch.float8_e4m3fn, device="cuda", seed=0):
+                 q_heads=8, kv_heads=2, page=32, codes=torch.float8_e4m3fn, theta=None, device="cuda", seed=0):
         self.slots, self.pages, self.page, self.blocks = slots, pages, page, blocks
         self.heads, self.q_heads, self.kv_heads = heads, q_heads, kv_heads
         self.device = device
@@ -51,6 +57,13 @@ class HybridDecoder:
         self.w_qkv = [matrix(width, (q_heads + 2 * kv_heads) * D) for _ in range(blocks)]
         self.w_attn_out = [matrix(q_heads * D, width) for _ in range(blocks)]
 
+        # norms and rotation of the exact layers' queries and keys (theta None: neither)
+        self.freq = self.q_norm = self.k_norm = None
+        if theta:
+            self.freq = (theta ** (-2 * torch.arange(D // 2, dtype=torch.float64) / D)).to(device)
+            self.q_norm, self.k_norm = ([(1 + 0.1 * torch.randn(D, generator=g)).to(device) for _ in range(blocks)]
+                                        for _ in range(2))
+
         # what a request leaves behind between steps
         self.state = [torch.zeros((slots, heads, D, D), device=device) for _ in range(blocks)]
         shape = (pages, kv_heads, page, D)
@@ -60,6 +73,10 @@ class HybridDecoder:
         self.ring = torch.arange(pages, dtype=torch.int32, device=device)
         self.ring_state = torch.tensor([0, pages], dtype=torch.int32, device=device)
         self.kv_len = torch.zeros(slots, dtype=torch.int32, device=device)
+        # the prefix that requests begin with: its tokens (whole pages), pages, states; which slots have it
+        self.prefix, self.prefix_pages, self.prefix_state = 0, None, None
+        self.begun = [False] * slots
+        self.group = torch.tensor([0, slots], dtype=torch.int32, device=device)
         # one workspace for every exact layer of any step up to this size, kept by the caller
         self.workspace = torch.empty(0, dtype=torch.uint8, device=device)
 
@@ -69,7 +86,7 @@ class HybridDecoder:
         T, H = x.shape[0], self.heads
         q, k, v = (t.view(T, H, D) for t in y[:, :3 * H * D].split(H * D, 1))
         gate, beta = y[:, 3 * H * D:].float().split(H, 1)
-        q, k = F.normalize(q.float(), dim=-1).bfloat16(), F.normalize(k.float(), dim=-1).bfloat16()
+        q, k = gdr.qk_norm_rope(q, k, norm="l2", eps=1e-24)
         args = (q, k, v.contiguous(), gate.contiguous(), beta.sigmoid(), A_MIN)
         if single:
             out = gdr.decode_step(*args, self.state[b])
@@ -77,14 +94,57 @@ class HybridDecoder:
             out, self.state[b] = gdr.chunk_fwd_varlen(*args, cu, self.state[b])
         return out.view(T, H * D) @ self.w_delta_out[b]
 
-    def _attention(self, b, x, cu, slots, kv_len, longest, single):
-        """The exact layer: the new keys and values into the cache, then attention over it."""
+    def _attention(self, b, x, cu, slots, positions, kv_len, longest, shared):
+        """The exact layer: the new keys and values into the cache, then attention over it.  cu: None
+        where every slot has one token; shared: the plan of what the slots have in common, or None."""
         y = (x @ self.w_qkv[b]).view(x.shape[0], -1, D)      # q, k, v stay where the product put them
         q, k, v = y.split([self.q_heads, self.kv_heads, self.kv_heads], 1)
+        if self.freq is not None:
+            gdr.qk_norm_rope(q, k, q_weight=self.q_norm[b], k_weight=self.k_norm[b], positions=positions,
+                             freq=self.freq, q_out=q, k_out=k)
         gdr.kv8_append(k, v, slots, *self.cache[b], *self.scale[b])
-        out = gdr.kv8_attn(q, *self.cache[b], *self.scale[b], self.table, kv_len, 1 / math.sqrt(D),
-                           cu_q=None if single else cu, max_q=longest, workspace=self.workspace)
+        cache = *self.cache[b], *self.scale[b], self.table, kv_len, 1 / math.sqrt(D)
+        if shared is None:
+            out = gdr.kv8_attn(q, *cache, cu_q=cu, max_q=longest, workspace=self.workspace)
+        else:
+            out = gdr.kv8_attn_shared(q, *cache, self.group, *shared, cu_q=cu, max_q=longest,
+                                      max_group_q=x.shape[0], workspace=self.workspace)
         return out.view(x.shape[0], -1) @ self.w_attn_out[b]
+
+    def share(self, tokens):
+        """Runs the tokens once (whole pages of them; the rest is left off) and lets every later request
+        begin with them.  No request may be under way."""
+        if any(self.begun) or self.prefix:
+            raise RuntimeError("a prefix is set once, before any request")
+        tokens = tokens[:len(tokens) // self.page * self.page]
+        if not tokens:
+            return
+        self.step([tokens] + [[]] * (self.slots - 1))
+        n = len(tokens) // self.page
+        self.prefix, self.prefix_pages = len(tokens), self.table[0, :n].clone()
+        self.prefix_state = [state[0].clone() for state in self.state]
+        # the slot is free again; the pages are the prefix's, not the ring's
+        self.table[0, :n] = -1
+        self.kv_len[0] = 0
+        for state in self.state:
+            state[0].zero_()
+        self.begun[0] = False
+
+    def _begin_and_end(self, tokens):
+        """Slots whose request begins get the prefix; those whose request ends let go of it."""
+        n = self.prefix // self.page
+        for s, t in enumerate(tokens):
+            if t is None:
+                if n:
+                    self.table[s, :n] = -1          # these pages do not return to the ring
+                self.begun[s] = False
+            elif t and not self.begun[s]:
+                self.begun[s] = True
+                if n:
+                    self.table[s, :n] = self.prefix_pages
+                    self.kv_len[s] = self.prefix
+                    for state, first in zip(self.state, self.prefix_state):
+                        state[s] = first
 
     def step(self, tokens):
         """tokens: per slot the new token ids (a list), [] for none, None where the request is
@@ -93,8 +153,9 @@ class HybridDecoder:
         n = [-1 if t is None else len(t) for t in tokens]
         flat = [i for t in tokens if t for i in t]
         total, longest = len(flat), max(n)
+        self._begin_and_end(tokens)
         q_len = torch.tensor(n, dtype=torch.int32, device=self.device)
-        kv_len, cu, slots, _, granted, ring_state = gdr.page_plan(
+        kv_len, cu, slots, positions, granted, ring_state = gdr.page_plan(
             self.kv_len, q_len, self.table, self.ring, self.ring_state, self.page, total)
         self.kv_len, self.ring_state = kv_len, ring_state
         for s, t in enumerate(tokens):
@@ -106,13 +167,19 @@ class HybridDecoder:
         if not bool(granted.all()):
             raise RuntimeError("no pages left: admit fewer requests")
         single = longest == 1 and min(n) == 1
-        size = gdr.kv8_attn_workspace_size(self.slots, longest, total, self.q_heads, self.kv_heads, D)
+        cu_q = None if single else cu
+        heads = self.q_heads, self.kv_heads, D
+        if self.prefix:
+            shared = gdr.kv8_shared_plan(self.table, kv_len, self.group, self.page, cu_q=cu_q)
+            size = gdr.kv8_attn_shared_workspace_size(self.slots, longest, 1, total, total, *heads)
+        else:
+            shared, size = None, gdr.kv8_attn_workspace_size(self.slots, longest, total, *heads)
         if self.workspace.numel() < size:
             self.workspace = torch.empty(size, dtype=torch.uint8, device=self.device)
         x = self.embedding[torch.tensor(flat, device=self.device)]
         for b in range(self.blocks):
             x = x + self._delta(b, F.rms_norm(x, x.shape[-1:]), cu, single)
-            x = x + self._attention(b, F.rms_norm(x, x.shape[-1:]), cu, slots, kv_len, longest, single)
+            x = x + self._attention(b, F.rms_norm(x, x.shape[-1:]), cu_q, slots, positions, kv_len, longest, shared)
         last = (cu[1:] - 1).clamp_min(0).long()
         return F.rms_norm(x[last], x.shape[-1:]) @ self.unembedding
 
@@ -162,14 +229,18 @@ def main(argv=None):
     p.add_argument("--prompt", type=int, default=2000, help="longest prompt")
     p.add_argument("--new", type=int, default=64, help="tokens to decode per request")
     p.add_argument("--chunk", type=int, default=512, help="most prompt tokens of a request in a step")
+    p.add_argument("--theta", type=float, help="base of the rotation's frequencies (none: no rotation)")
+    p.add_argument("--prefix", type=int, default=0, help="tokens that all prompts begin with")
     p.add_argument("--codes", choices=["e4m3", "int8"], default="e4m3")
     a = p.parse_args(argv)
     gdr.load(build_if_missing=True)
     page = 32
     width = -(-(a.prompt + a.new) // page)
-    model = HybridDecoder(a.slots, 2 * a.slots * width, width, page=page,
-                          codes=torch.float8_e4m3fn if a.codes == "e4m3" else torch.int8)
+    model = HybridDecoder(a.slots, 2 * a.slots * width + a.prefix // page, width + a.prefix // page, page=page,
+                          codes=torch.float8_e4m3fn if a.codes == "e4m3" else torch.int8, theta=a.theta)
     g = torch.Generator().manual_seed(1)
+    if a.prefix:
+        model.share(torch.randint(0, 1000, (a.prefix,), generator=g).tolist())
     lengths = torch.randint(1, a.prompt + 1, (a.requests,), generator=g).tolist()
     prompts = [torch.randint(0, 1000, (n,), generator=g).tolist() for n in lengths]
     torch.cuda.synchronize()
