@@ -592,6 +592,15 @@ def _raw_stream(index):
     return torch._C._cuda_getCurrentRawStream(index)
 
 
+def _all_here(*tensors):
+    """The tensors (None: none) are on the current device, where the kernels are launched."""
+    here = torch._C._cuda_getDevice()
+    for t in tensors:
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{here}")
+    return here
+
+
 def _int(t, name, shape=None):
     """Device pointer of a contiguous int32 CUDA tensor."""
     if t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous():
@@ -743,10 +752,10 @@ def kv8_shared_plan(block_table, kv_len, cu_group, page: int, *, cu_q=None):
     groups, dev = cu_group.numel() - 1, block_table.device
     shared = torch.empty(S, dtype=torch.int32, device=dev)
     lead = torch.empty(max(groups, 0), dtype=torch.int32, device=dev)
-    code = lib.gdr_kv8_shared_plan(_int(block_table, "block_table"), _int(kv_len, "kv_len", (S,)),
-                                   None if cu_q is None else _int(cu_q, "cu_q", (S + 1,)),
-                                   _int(cu_group, "cu_group"), shared.data_ptr(), lead.data_ptr(), S, groups, W, page,
-                                   _raw_stream(dev.index))
+    args = (_int(block_table, "block_table"), _int(kv_len, "kv_len", (S,)),
+            None if cu_q is None else _int(cu_q, "cu_q", (S + 1,)), _int(cu_group, "cu_group"))
+    here = _all_here(block_table, kv_len, cu_q, cu_group)
+    code = lib.gdr_kv8_shared_plan(*args, shared.data_ptr(), lead.data_ptr(), S, groups, W, page, _raw_stream(here))
     if code:
         raise GdrError(code, "gdr_kv8_shared_plan")
     return shared, lead
@@ -790,12 +799,14 @@ def kv8_attn_shared(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, 
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
     elif workspace.dtype is not torch.uint8 or not workspace.is_cuda or workspace.numel() < need:
         raise ValueError(f"workspace must be a uint8 CUDA tensor of at least {need} bytes")
+    here = _all_here(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, cu_q, cu_group, shared, lead, out,
+                     workspace)
     code = lib.gdr_kv8_attn_shared(qp, qst, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                                    v_scale.data_ptr(), _int(block_table, "block_table"), _int(kv_len, "kv_len", (S,)),
                                    None if cu_q is None else _int(cu_q, "cu_q", (S + 1,)), _int(cu_group, "cu_group"),
                                    _int(shared, "shared", (S,)), _int(lead, "lead", (groups,)), scale, out.data_ptr(),
                                    None if lse is None else lse.data_ptr(), S, max_q, groups, max_group_q, T, Hq, Hkv,
-                                   D, W, P, N, el, kv, workspace.data_ptr(), need, _raw_stream(dev.index))
+                                   D, W, P, N, el, kv, workspace.data_ptr(), need, _raw_stream(here))
     if code:
         raise GdrError(code, "gdr_kv8_attn_shared")
     return (out, lse) if want_lse else out
@@ -836,7 +847,7 @@ def _like(t, out, name):
     """A new tensor of t's shape, or `out`, checked: its pointer and token stride too."""
     if out is None:
         shape = t.shape
-        out = t.new_empty(shape)
+        out = torch.empty(shape, dtype=t.dtype, device=t.device)
         return out, out.data_ptr(), shape[1] * shape[2]
     if out.shape != t.shape or out.dtype is not t.dtype:
         raise ValueError(f"{name} must have its input's shape and dtype")
@@ -859,8 +870,9 @@ def qk_norm_rope(q, k=None, *, norm="rms", q_weight=None, k_weight=None, eps: fl
     ko, kos = None, 0
     if k is not None:
         k_out, ko, kos = _like(k, k_out, "k_out")
+    here = _all_here(q, k, q_weight, k_weight, positions, freq, q_out, k_out if k is not None else None)
     code = lib.gdr_qk_norm_rope(qp, qst, kp, kst, qw, kw, eps, kind, pos, fp, rot, pr, qo, qos, ko, kos, T, Hq,
-                                Hk, D, DTYPE[q.dtype], _raw_stream(q.device.index))
+                                Hk, D, DTYPE[q.dtype], _raw_stream(here))
     if code:
         raise GdrError(code, "gdr_qk_norm_rope")
     return q_out, (None if k is None else k_out)
@@ -901,10 +913,12 @@ def qk_norm_rope_bwd(q, k, d_q_out, d_k_out, *, norm="rms", q_weight=None, k_wei
         elif workspace.dtype is not torch.uint8 or not workspace.is_cuda or workspace.numel() < wn:
             raise ValueError(f"workspace must be a uint8 CUDA tensor of at least {wn} bytes")
         wp = workspace.data_ptr()
+    here = _all_here(q, k, q_weight, k_weight, positions, freq, d_q_out, d_k_out if k is not None else None, d_q,
+                     d_k if k is not None else None, workspace if wp is not None else None)
     code = lib.gdr_qk_norm_rope_bwd(qp, qst, kp, kst, qw, kw, eps, kind, pos, fp, rot, pr, gp, gst, hp, hst, dp,
                                     dst, ep, est, None if dqw is None else dqw.data_ptr(),
                                     None if dkw is None else dkw.data_ptr(), T, Hq, Hk, D, DTYPE[q.dtype], wp, wn,
-                                    _raw_stream(q.device.index))
+                                    _raw_stream(here))
     if code:
         raise GdrError(code, "gdr_qk_norm_rope_bwd")
     return d_q, (None if k is None else d_k), dqw, dkw

@@ -670,7 +670,8 @@ gdr_status_t gdr_kv8_attn(const void *q, int64_t q_stride, const void *k_cache, 
  *   max_group_q  the most queries that the requests of a group have together: it chooses a kernel, as
  *             max_q does
  *   workspace  16-byte aligned, gdr_kv8_attn_shared_workspace_size bytes: the sums over the common pages
- *             (fp32, Hq * (D + 2) values a query) and partial results; scratch on entry and exit
+ *             (fp32, Hq * (D + 2) values a query) and partial results; scratch on entry and exit, not
+ *             shared with a call still running on another stream
  * Two passes of two launches each, or gdr_kv8_attn's one where the sizes say that a pass of its own costs
  * more than the common pages (by a cost model; GDR_OPT_SHARED_LEAST forces either): with 32 query and 4
  * cached heads 8 single tokens want some 25 thousand common tokens, 64 some 4 thousand.
@@ -724,7 +725,8 @@ typedef enum {
  *   d_q, d_k are overwritten (rows of negative positions with zeros); they may be d_q_out and d_k_out,
  *   or q and k, themselves.  d_q_weight, d_k_weight fp32 [D], overwritten, or NULL: not wanted (then one
  *   launch and no workspace; else two, and `workspace`: gdr_qk_norm_rope_bwd_workspace_size bytes on the
- *   current device, 16-byte aligned, scratch on entry and exit).
+ *   current device, 16-byte aligned, scratch on entry and exit, not shared with a call still running on
+ *   another stream).
  */
 gdr_status_t gdr_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
                               const float *q_weight, const float *k_weight, float eps, gdr_norm_t norm,

@@ -315,3 +315,15 @@ def test_option():
             gdr.set_option("shared_least", bad)
     with gdr.option(shared_least=77):
         assert gdr.get_option("shared_least") == 77
+
+
+def test_another_device(monkeypatch):
+    """Tensors that are not on the current device are refused (the current one is made out to be another)."""
+    x = case([(2, [(9, 1)] * 3)], 2, 2, 64, 16, BF16, "int8")
+    d = on_gpu(x)
+    plan = gdr.kv8_shared_plan(d["table"], d["kv_len"], d["group"], 16)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        gdr.kv8_shared_plan(d["table"], d["kv_len"], d["group"], 16)
+    with pytest.raises(ValueError, match="current device"):
+        attend(x, d, plan=plan)

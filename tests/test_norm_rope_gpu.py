@@ -301,3 +301,16 @@ def test_repeats_streams_and_graphs():
             ws.fill_(255)
             g.replay()
             assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+def test_another_device(monkeypatch):
+    """Tensors that are not on the current device are refused (the current one is made out to be another)."""
+    q, k, wq, wk, gq, gk = make(5, 2, 1, 64, "bf16")
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    with pytest.raises(ValueError, match="current device"):
+        gdr.qk_norm_rope(q, k)
+    with pytest.raises(ValueError, match="current device"):
+        gdr.qk_norm_rope_bwd(q, k, gq, gk)
+    monkeypatch.undo()
+    with pytest.raises(TypeError):
+        gdr.qk_norm_rope(q, k, q_weight=wq.cpu())
