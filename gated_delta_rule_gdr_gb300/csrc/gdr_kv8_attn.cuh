@@ -21,6 +21,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 namespace gdr {
 namespace {
@@ -394,6 +395,7 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
 template <typename E, int D, int RB, int WPR, int RPW, bool ROUND, class A>
 __global__ void __launch_bounds__(256, kv8::kMergeResident) kv8_merge_kernel(const A a) {
     static_assert(WPR == 1 ? !ROUND : RPW == 1, "");
+    static_assert(WPR == 8 || !ROUND, "");
     constexpr int VL = D / 32;
     __shared__ float s_o[WPR > 1 ? 8 : 1][D];
     __shared__ float s_l[8];
@@ -469,10 +471,15 @@ __global__ void __launch_bounds__(256, kv8::kMergeResident) kv8_merge_kernel(con
             if constexpr (WPR > 1) {
                 if (ROUND && again) __syncthreads();
                 again = true;
+                // the row's warps; a row that is not there has none here
+                auto meet = [&]() {
+                    if constexpr (WPR == 8) __syncthreads();
+                    else asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / WPR), "n"(32 * WPR) : "memory");
+                };
                 if (lane == 0) s_l[warp] = l[0];
 #pragma unroll
                 for (int e = 0; e < VL; ++e) s_o[warp][lane * VL + e] = o[0][e];
-                __syncthreads();
+                meet();
                 if (warp != w0) {
                     if constexpr (ROUND) continue;
                     return;
@@ -565,6 +572,13 @@ cudaError_t launch_merge(const A &a, int64_t rows, cudaStream_t s) {
         if (every && most == could) return launch_after(kv8_merge_kernel<E, D, RB, 8, 1, false, A>, dim3(x, wide), 256, 0, s, a);
         return launch_after(kv8_merge_kernel<E, D, RB, 8, 1, true, A>, dim3(x, wide), 256, 0, s, a);
     }
+    // Groups with a long prefix: few items of many parts and more rows than there are warps for eight each
+    // (32 decodes of 8 rows on 32 k common keys, 1024 rows of 38 parts: the whole call 50 us with four warps
+    // a row, 59 with one for two; 64, of 19 parts: 69 and 70; 128, of 9: 110 and 105).
+    if constexpr (!std::is_same_v<A, AttnArgs>)
+        if (a.ctas >= 16 * items)
+            return launch_after(kv8_merge_kernel<E, D, RB, 4, 1, false, A>, dim3(every ? x : all_x, (unsigned)((could + 1) / 2)),
+                                256, 0, s, a);
     return launch_after(kv8_merge_kernel<E, D, RB, 1, RPW, false, A>, dim3(every ? x : all_x, y), 256, 0, s, a);
 }
 

@@ -183,6 +183,8 @@ CASES = [
     ([(10, [(300, 200), (180, 150), (90, 1)]), (2, [(130, 129), (140, 140)])], 8, 2, 128, 64),
     ([(70, [(1, 1), (40, 17), (33, 33), (900, 2)])], 5, 1, 128, 16),
     ([(1, [(16, 1)] * 2)], 64, 1, 128, 16),
+    ([(75, [(3, 1)] * 33)], 28, 4, 64, 16),                                        # 231 rows of many parts
+    ([(19, [(1, 1)] * 37), (4, [(3, 1)] * 2)], 21, 3, 128, 64),                    # 259
 ]
 
 
