@@ -13,8 +13,8 @@
 //
 // Bound: the common pages' codes once a group and the others' once, or, with many rows, the products.
 // Measured: 256 single tokens of 8 heads a cached head, four groups with 17 to 32 k common tokens and up to
-// 2000 of their own (372 MB, 107 GFLOP: 56 us either way) 244 us, gdr_kv8_attn 928: the tile kernel 159 (a
-// third of the groups' last pairs of tiles is empty; 2.4 us a pair and 128 keys as in gdr_kv8_attn), its
+// 2000 of their own (372 MB, 107 GFLOP: 56 us either way) 244 us, gdr_kv8_attn 928: the tile kernel 159 (four
+// of eleven blocks of 256 rows are half empty; 2.4 us a block and 128 keys as in gdr_kv8_attn), its
 // merge 11, the own tokens 75 (270 MB, 1000 keys an item: its ends weigh), their merge 8.  24 questions of up
 // to 200 tokens of 4 heads a cached head on 20 k (595 GFLOP, 310 us) 667 us, gdr_kv8_attn 800: 985
 // TFLOP/s in the first pass (580 us), the rest the questions' own tiles and 60 MB of sums on their way.

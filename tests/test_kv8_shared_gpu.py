@@ -329,3 +329,30 @@ def test_another_device(monkeypatch):
         gdr.kv8_shared_plan(d["table"], d["kv_len"], d["group"], 16)
     with pytest.raises(ValueError, match="current device"):
         attend(x, d, plan=plan)
+
+
+@pytest.mark.parametrize("size", [2, 3, 1024])
+def test_the_most_requests(size):
+    """8192 requests in groups of two, of three (some left over, outside every group) and of 1024."""
+    S, page, D, Hkv, Hq = 8192, 16, 64, 1, 2
+    groups = S // size
+    g = torch.Generator().manual_seed(size)
+    N = 3 * groups + S
+    order = torch.randperm(N, generator=g).to(torch.int32)
+    r = torch.arange(S)
+    table = torch.stack([order[(r // size).clamp(max=groups - 1) * 3 + c] for c in range(3)]
+                        + [order[3 * groups + r]], 1)
+    kv = torch.randint(3 * page + 1, 4 * page + 1, (S,), generator=g, dtype=torch.int32)
+    cache = [torch.randint(-127, 128, (N, Hkv, page, D), generator=g, dtype=torch.int8).cuda() for _ in range(2)]
+    scale = [torch.exp2(torch.randint(-8, -4, (N, Hkv), generator=g).float()).cuda() for _ in range(2)]
+    q = torch.randn((S, Hq, D), generator=g).bfloat16().cuda()
+    group = torch.arange(groups + 1, dtype=torch.int32).cuda() * size
+    shared, lead = gdr.kv8_shared_plan(table.cuda(), kv.cuda(), group, page)
+    inside = groups * size
+    assert (shared[:inside] == 48).all() and (shared[inside:] == 0).all()
+    assert torch.equal(lead.cpu(), torch.arange(groups, dtype=torch.int32) * size)
+    a, la = gdr.kv8_attn_shared(q, *cache, *scale, table.cuda(), kv.cuda(), 0.125, group, shared, lead, max_group_q=size,
+                                want_lse=True)
+    b, lb = gdr.kv8_attn(q, *cache, *scale, table.cuda(), kv.cuda(), 0.125, want_lse=True)
+    assert oracle.rel_l2(a.cpu(), b.cpu()) <= 2 * TOL[BF16]
+    assert (la - lb).abs().max() <= 2 * LSE_TOL * max(1.0, float(lb.abs().max()))

@@ -314,3 +314,23 @@ def test_another_device(monkeypatch):
     monkeypatch.undo()
     with pytest.raises(TypeError):
         gdr.qk_norm_rope(q, k, q_weight=wq.cpu())
+
+
+def test_offsets_past_32_bits():
+    """A tensor of more than 2^31 values, in place: its last tokens as they are alone."""
+    H, D, extra = 32, 128, 70
+    T = 2 ** 31 // (H * D) + extra
+    x = torch.zeros((T, H, D), dtype=torch.bfloat16, device="cuda")
+    x[-extra:] = torch.randn((extra, H, D), device="cuda")
+    x[:extra] = torch.randn((extra, H, D), device="cuda")
+    pos, freq = torch.arange(T, dtype=torch.int32, device="cuda"), freq_of(D)
+    ends = [gdr.qk_norm_rope(x[s].clone(), positions=pos[s].clone(), freq=freq)[0] for s in (slice(0, extra), slice(T - extra, T))]
+    g = [torch.randn((extra, H, D), device="cuda").bfloat16() for _ in range(2)]
+    dx = [gdr.qk_norm_rope_bwd(x[s].clone(), None, y, None, positions=pos[s].clone(), freq=freq)[0]
+          for s, y in zip((slice(0, extra), slice(T - extra, T)), g)]
+    d = torch.zeros_like(x)
+    d[:extra], d[-extra:] = g
+    gdr.qk_norm_rope_bwd(x, None, d, None, positions=pos, freq=freq, d_q=d)
+    assert torch.equal(d[:extra], dx[0]) and torch.equal(d[-extra:], dx[1]) and (d[extra:-extra] == 0).all()
+    gdr.qk_norm_rope(x, positions=pos, freq=freq, q_out=x)
+    assert torch.equal(x[:extra], ends[0]) and torch.equal(x[-extra:], ends[1]) and (x[extra:-extra] == 0).all()
