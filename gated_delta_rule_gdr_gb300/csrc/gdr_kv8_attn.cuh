@@ -193,24 +193,35 @@ struct Place {      // a unit: request, head, block of rows, unit of the block's
     int64_t total;           // what is shared: all units, and `extra` for each item
 };
 
+// And the request, as every role needs it: in the passes over shared prefixes reading it again is several
+// trips to memory in turn (244 -> 237 us for 256 decodes, 667 -> 648 for 24 questions; in gdr_kv8_attn, where
+// it is one trip, 32 x 5 drafted tokens went from 156 to 162 us with it).
+template <class A> constexpr bool kKeepsRequest = !std::is_same_v<A, AttnArgs>;
+template <class A> struct FirstPlace : Place {
+    typename A::Req r;
+};
+template <> struct FirstPlace<AttnArgs> : Place {};
+
 // This CTA's units and the place of the first one.  An item costs its units and, for its queries
 // and its end, as much as E more; what is divided evenly is the sum of both (the units of an
 // item follow its E), or the units alone where a CTA's share would be no more than E.  All NT
 // threads call it; `place` is in shared memory and valid after it returns.
 template <int RB, int UT, int NT, int E, class A>
-__device__ __forceinline__ void find_place(const A &a, Place *place, int64_t *s_scan) {
+__device__ __forceinline__ void find_place(const A &a, FirstPlace<A> *place, int64_t *s_scan) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int NW = NT / 32;
     struct Sum {
         int64_t u, i;        // units, items
     };
     Sum mine{}, before{}, sum{};
+    typename A::Req kept{};
     // what comes before each request of a chunk of NT requests; the last chunk stays in registers
     auto scan = [&](int base) {
         const int s = base + tid;
         mine = Sum{0, 0};
         if (s < a.S) {
             const typename A::Req r = request_of(a, s);
+            if constexpr (kKeepsRequest<A>) kept = r;
             mine.u = units_of_head<RB, UT>(a, r) * a.Hkv;
             mine.i = (int64_t)blocks_of<RB>(a, r) * a.Hkv;
         }
@@ -261,7 +272,9 @@ __device__ __forceinline__ void find_place(const A &a, Place *place, int64_t *s_
             for (int k = 0; k < 2; ++k) {            // the first unit at or after w0, and after w1
                 const int64_t w = k ? w1 : w0;
                 if (w < at || w >= end) continue;
-                const typename A::Req r = request_of(a, base + tid);
+                typename A::Req r;
+                if constexpr (kKeepsRequest<A>) r = kept;
+                else r = request_of(a, base + tid);
                 const int64_t per_u = mine.u / a.Hkv, per_i = mine.i / a.Hkv, h = (w - at) / (per_u + e * per_i);
                 int64_t rem = w - at - h * (per_u + e * per_i), u = run.u + before.u + h * per_u;
                 int b = 0;
@@ -278,6 +291,7 @@ __device__ __forceinline__ void find_place(const A &a, Place *place, int64_t *s_
                     place->u0 = u + t;
                     place->i0 = run.i + before.i + h * per_i + b;
                     place->s = base + tid, place->h = (int)h, place->b = b, place->t = t;
+                    if constexpr (kKeepsRequest<A>) place->r = r;
                 }
             }
             run.u += sum.u, run.i += sum.i;
@@ -313,9 +327,10 @@ struct Cursor {
         end = block_end<RB>(a, r, b);
         nt = units_of<UT>(end);
     }
-    __device__ __forceinline__ void start(const A &a, const Place &p) {
+    __device__ __forceinline__ void start(const A &a, const FirstPlace<A> &p) {
         s = p.s, h = p.h, b = p.b, t = p.t;
-        r = request_of(a, s);
+        if constexpr (kKeepsRequest<A>) r = p.r;
+        else r = request_of(a, s);
         enter(a);
     }
     __device__ __forceinline__ void next_of_item(const A &a) {   // past the last item: s = S

@@ -115,7 +115,7 @@ kv8_split_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant
     constexpr int LD = D / 4, LO = D / 8;        // values of a query, of an output row that a lane holds
     extern __shared__ __align__(1024) uint8_t sm[];
     __shared__ __align__(8) uint64_t s_bar[NW * ST];
-    __shared__ Place s_place;
+    __shared__ FirstPlace<A> s_place;
     __shared__ int64_t s_scan[2 * NW];
     __shared__ float s_stat[2][NW][RB];          // M, l of each warp at an item's end
     __shared__ volatile int s_abort;

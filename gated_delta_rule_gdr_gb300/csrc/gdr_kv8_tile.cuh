@@ -627,7 +627,7 @@ __global__ void __launch_bounds__(tl::NT, 1) kv8_tile_kernel(const A a) {
     extern __shared__ __align__(1024) uint8_t sm[];
     const uint32_t sb = smem_u32(sm);
     __shared__ __align__(8) uint64_t s_bar[NUM_BARS];
-    __shared__ Place s_place;
+    __shared__ FirstPlace<A> s_place;
     __shared__ int64_t s_scan[2 * NT / 32];
     __shared__ uint32_t s_tmem;
     __shared__ int s_gone[NSC];
