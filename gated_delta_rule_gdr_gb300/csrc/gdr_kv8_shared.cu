@@ -13,11 +13,11 @@
 //
 // Bound: the common pages' codes once a group and the others' once, or, with many rows, the products.
 // Measured: 256 single tokens of 8 heads a cached head, four groups with 17 to 32 k common tokens and up to
-// 2000 of their own (372 MB, 107 GFLOP: 56 us either way) 244 us, gdr_kv8_attn 928: the tile kernel 159 (four
-// of eleven blocks of 256 rows are half empty; 2.4 us a block and 128 keys as in gdr_kv8_attn), its
-// merge 11, the own tokens 75 (270 MB, 1000 keys an item: its ends weigh), their merge 8.  24 questions of up
-// to 200 tokens of 4 heads a cached head on 20 k (595 GFLOP, 310 us) 667 us, gdr_kv8_attn 800: 985
-// TFLOP/s in the first pass (580 us), the rest the questions' own tiles and 60 MB of sums on their way.
+// 2000 of their own (372 MB, 107 GFLOP: 56 us either way) 237 us, gdr_kv8_attn 928: the tile kernel 154 (four
+// of eleven blocks of 256 rows are half empty; 2.6 us a block and 128 keys), its merge 10, the own tokens 72
+// (270 MB, 1000 keys an item: its ends weigh), their merge 7.  24 questions of up to 200 tokens of 4 heads a
+// cached head on 20 k (595 GFLOP, 310 us) 647 us, gdr_kv8_attn 800: 1000 TFLOP/s in the first pass (570 us),
+// the rest the questions' own tiles and 60 MB of sums on their way.
 // The plan: 256 requests in 8 groups 3.5 us, 1000 rows of 4096 entries (16.4 MB) 7.4 us, two launches.
 
 #include "gdr_kv8_split.cuh"
@@ -143,11 +143,11 @@ size_t pre_bytes(int total_q, int Hq, int D) { return align32((size_t)total_q * 
 // (measured: 128 decodes of 8 heads a cached head on 32 k common keys, from the L2 mostly, 502 us = 0.58 a
 // block; fp32 1.0 and 1.6 at D = 128, 0.63 and 1.0 at 64), the tile kernel's copies, tile or pair of
 // tiles (24 x 5 drafted tokens on 16 k 110 us = 1.3; 2.4 a pair).
-// A pass of its own costs 17 us (8 decodes on 4096 common tokens 34 us against 20 in one), 27 where it
+// A pass of its own costs 15 us (16 decodes on 4096 common tokens 31 us against 21 in one), 19 where it
 // takes pairs, the sums' way through memory, and the ends of items that are twice as many.
-// Where the two are even: measured / by this rule, 8, 16, 32, 64 decodes with 4 cached heads: 30 / 25, 12 /
-// 11, 7.5 / 8.1, 3.6 / 4.1 thousand common tokens; 24 x 5 drafted 7 / 7.6; prompts of 64 or 300 tokens: none
-// up to 16 k / none, 20.
+// Where the two are even, measured / by this rule, with 4 cached heads of 8 query heads: 8, 16, 32, 64 decodes
+// 22 / 22, 9 / 10, 5.2 / 5.7, 2.9 / 2.9 thousand common tokens; 24 x 5 drafted 6 / 6; prompts of 64 or 300
+// tokens: none up to 16 k / none, 20.
 // (`rows` of one request or group on average, at most `most`; alike: all have that many, else the last
 // block of each is half full; ends: what the ends of its items cost in units)
 double keys_cost(int64_t most, double rows, bool alike, int D, Elem e, double *ends) {
@@ -168,7 +168,7 @@ int least_worth(const KvSharedCall &c) {
     const double group = keys_cost(gmost, (double)c.total_q * G / c.groups, c.groups == 1, c.D, c.e, &gends);
     const double gain = requests * one - c.groups * group;
     if (gain <= 0) return 0x7fffffff;
-    const double pass = (c.e == Elem::BF16 && gmost > 128 ? 27 : 17) + (double)c.total_q * c.Hq * (8 * c.D + 16) / 3e6 +
+    const double pass = (c.e == Elem::BF16 && gmost > 128 ? 19 : 15) + (double)c.total_q * c.Hq * (8 * c.D + 16) / 3e6 +
                         requests * c.Hkv * one * ends / sms;
     return (int)std::min(pass * sms / (gain * c.Hkv) * 128, 2147483647.0);
 }

@@ -674,7 +674,7 @@ gdr_status_t gdr_kv8_attn(const void *q, int64_t q_stride, const void *k_cache, 
  *             shared with a call still running on another stream
  * Two passes of two launches each, or gdr_kv8_attn's one where the sizes say that a pass of its own costs
  * more than the common pages (by a cost model; GDR_OPT_SHARED_LEAST forces either): with 32 query and 4
- * cached heads 8 single tokens want some 25 thousand common tokens, 64 some 4 thousand.
+ * cached heads 8 single tokens want some 22 thousand common tokens, 64 some 3 thousand.
  */
 gdr_status_t gdr_kv8_shared_plan(const int *block_table, const int *kv_len, const int *cu_q, const int *cu_group,
                                  int *shared, int *lead, int S, int num_groups, int table_width, int page, void *stream);
