@@ -12,12 +12,13 @@
 // without its whole turns, exactly but for F's own rounding (2^-64 turns times p), and costs
 // three integer multiplications a token and pair, shared by the token's heads.
 //
-// Work.  A head's values are taken by D / 16 lanes, 16 values each in two pieces of 8: pieces
-// that a pair lies across (or within), so that no value changes lanes but in the row's sums.
-// A warp takes 32 / (D / 16) heads of a token at once: a pass.  The passes of a tensor, tokens in
-// order, are divided evenly among the warps of the CTAs that the tensor got, queries and keys by
-// their cost.  A lane copies its pieces asynchronously to a place of its own in shared memory, ST - 1
-// passes ahead, so that no registers wait for memory and nothing synchronises.
+// Work.  A head's values are taken by D / 16 lanes, 16 values each in chunks of 16 bytes: chunks that
+// a pair lies across (or within), so that no value changes lanes but in the row's sums, and
+// neighbouring lanes have neighbouring chunks.  A warp takes 32 / (D / 16) rows (a token's head) at once: a
+// pass.  The rows of a tensor, heads in tokens in order, are divided evenly among the warps of the CTAs that
+// the tensor got, queries and keys by their cost.  A lane copies its chunks asynchronously to a
+// place of its own in shared memory, ST - 1 passes ahead, so that no registers wait for memory and
+// nothing synchronises.
 //
 // Bound: bytes (forward 2, backward 3 times the tensors).  Measured, 16384 tokens, 32 + 8 heads of
 // 128 bf16 values out of one projection, weights and rotation: forward (336 MB, 50 us at the
@@ -28,15 +29,17 @@
 
 #include "gdr_launch.cuh"
 
+#include <algorithm>
+
 namespace gdr {
 namespace {
 
 namespace nr {
 constexpr int NT = 256, NW = NT / 32;
 constexpr int CPS = 2;                                            // CTAs an SM
-template <bool BWD> constexpr int ST = 3;                          // passes of a warp's ring
-template <typename E> constexpr uint32_t PIECE = 256 * sizeof(E); // bytes of a warp's pieces of 8 values
-template <typename E, bool BWD> constexpr uint32_t STAGE = (BWD ? 4 : 2) * PIECE<E>;
+constexpr int ST = 3;                                             // passes of a warp's ring
+template <typename E> constexpr int NC = sizeof(E);               // chunks of a lane's 16 values
+template <typename E, bool BWD> constexpr uint32_t STAGE = (BWD ? 2 : 1) * NC<E> * 512;   // bytes of a warp's pass
 constexpr int RUN = 4;         // passes of a warp where there are few
 }
 
@@ -57,31 +60,22 @@ struct NormArgs {
     bool norm;
 };
 
-// 8 values of a piece: brought to the lane's place in shared memory (none: zeros), taken from there as
-// four packed pairs of floats, stored.
-template <typename E> struct Piece;
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool has) {
+// A chunk: brought to the lane's place in shared memory (none: zeros), taken from there as packed pairs of
+// floats, stored.
+__device__ __forceinline__ void bring_chunk(uint32_t dst, const void *src, bool has) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(has ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void lds128(uint32_t src, uint64_t &a, uint64_t &b) {
     asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];" : "=l"(a), "=l"(b) : "r"(src) : "memory");
 }
-template <> struct Piece<float> {
-    static __device__ __forceinline__ void bring(uint32_t dst, const float *src, bool has) {
-        copy16(dst, src, has);
-        copy16(dst + 512, src + 4, has);
-    }
-    static __device__ __forceinline__ void get(uint32_t src, uint64_t *f) {
-        lds128(src, f[0], f[1]);
-        lds128(src + 512, f[2], f[3]);
-    }
+template <typename E> struct Chunk;
+template <> struct Chunk<float> {
+    static __device__ __forceinline__ void get(uint32_t src, uint64_t *f) { lds128(src, f[0], f[1]); }
     static __device__ __forceinline__ void store(float *p, const uint64_t *f) {
         *reinterpret_cast<ulonglong2 *>(p) = make_ulonglong2(f[0], f[1]);
-        *reinterpret_cast<ulonglong2 *>(p + 4) = make_ulonglong2(f[2], f[3]);
     }
 };
-template <> struct Piece<__nv_bfloat16> {
-    static __device__ __forceinline__ void bring(uint32_t dst, const __nv_bfloat16 *src, bool has) { copy16(dst, src, has); }
+template <> struct Chunk<__nv_bfloat16> {
     static __device__ __forceinline__ void get(uint32_t src, uint64_t *f) {
         uint64_t u[2];
         lds128(src, u[0], u[1]);
@@ -101,6 +95,24 @@ template <> struct Piece<__nv_bfloat16> {
         }
         *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     }
+};
+// Where in a row the chunks of a lane (of `lanes` a row) begin, and a lane's packed pair e.  With pairs (i, i +
+// rot / 2) the first rot / 16 lanes have what is turned, a chunk of the second half for each of the first.
+template <typename E> struct Places {
+    static constexpr int NC = nr::NC<E>, CV = 16 / NC;       // values of a chunk
+    int at[NC];
+    __device__ __forceinline__ Places(int j, int lanes, int rot, bool halves) {
+        const int t = rot >> 4;                              // lanes of the turned part
+        if (halves && j < t) {
+#pragma unroll
+            for (int c = 0; c < NC; ++c) at[c] = CV * (j + t * (c % (NC / 2))) + (c < NC / 2 ? 0 : rot / 2);
+        } else {
+            const int from = halves ? rot : 0, n = halves ? lanes - t : lanes;
+#pragma unroll
+            for (int c = 0; c < NC; ++c) at[c] = from + CV * (j - (halves ? t : 0) + n * c);
+        }
+    }
+    __device__ __forceinline__ int pair(int e) const { return at[e / (8 / NC)] + 2 * (e % (8 / NC)); }
 };
 
 // frac(f / 2 pi) 2^64.  1 / (2 pi) in two doubles, so that F is good to its last bits.
@@ -133,21 +145,28 @@ __device__ __forceinline__ float inverse_root(float x) {
     return rsqrtf(x);
 }
 
-// The rotation of a lane's pairs by its pieces p0 and p1.  ROT 1: pairs (i, i + rot / 2), a piece's values
-// with the other's, two pairs an instruction; ROT 2: pairs (2 i, 2 i + 1) within a piece.
-template <int ROT>
+// The rotation of a lane's pairs.  ROT 1: pairs (i, i + rot / 2), packed pairs e and e + 4, two of them an
+// instruction; ROT 2: pairs (2 i, 2 i + 1).
+template <typename E, int ROT>
 struct Turn {
+    static constexpr int NC = nr::NC<E>;
     float c[8], s[8];
-    bool on[2];           // whether the pieces are turned (ROT 1: both or none)
-    __device__ __forceinline__ Turn(int p0, int p1, int rot) { on[0] = 8 * p0 < rot, on[1] = 8 * p1 < rot; }
-    template <typename E>
-    __device__ __forceinline__ void set(const uint64_t *f, int p0, int p1, uint32_t p) {
+    bool on[NC];          // which chunks are turned (ROT 1: all or none)
+    __device__ __forceinline__ Turn(const Places<E> &p, int rot) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (on[ROT == 1 ? 0 : e >> 2]) {
-                const uint64_t turns = f[ROT == 1 ? 8 * p0 + e : 4 * (e < 4 ? p0 : p1) + (e & 3)];
-                turn_sincos<E>((uint32_t)((turns * (uint64_t)p) >> 32), s[e], c[e]);
-            }
+        for (int i = 0; i < NC; ++i) on[i] = p.at[i] < rot;
+    }
+    __device__ __forceinline__ void set(const uint64_t *f, const Places<E> &pl, uint32_t p) {
+        if constexpr (ROT == 1) {
+            if (on[0])
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    turn_sincos<E>((uint32_t)((f[pl.pair(e >> 1) + (e & 1)] * (uint64_t)p) >> 32), s[e], c[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (on[e / (8 / NC)]) turn_sincos<E>((uint32_t)((f[pl.pair(e) >> 1] * (uint64_t)p) >> 32), s[e], c[e]);
+        }
     }
     template <bool BACK>
     __device__ __forceinline__ void apply(uint64_t (&f)[8]) const {
@@ -163,7 +182,7 @@ struct Turn {
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                if (on[e >> 2]) {
+                if (on[e / (8 / NC)]) {
                     float a, b;
                     f2_unpack(f[e], a, b);
                     const float sn = BACK ? -s[e] : s[e];
@@ -172,8 +191,8 @@ struct Turn {
         }
     }
 };
-template <> struct Turn<0> {
-    __device__ __forceinline__ Turn(int, int, int) {}
+template <typename E> struct Turn<E, 0> {
+    __device__ __forceinline__ Turn(const Places<E> &, int) {}
 };
 
 // The sum of a packed pair over the lanes of a head.  LOG: log2 of these lanes, or -1: `log`.
@@ -201,9 +220,9 @@ __device__ __forceinline__ uint64_t dot8(const uint64_t (&a)[8], const uint64_t 
 // any.  BWD: the backward; DW: and the weights' gradients.
 template <typename E, int ROT, int LOG, bool BWD, bool DW>
 __global__ void __launch_bounds__(nr::NT, nr::CPS) norm_rope_kernel(const NormArgs a) {
-    using nr::NT, nr::NW;
-    constexpr uint32_t PIECE = nr::PIECE<E>, STAGE = nr::STAGE<E, BWD>;
-    constexpr int ST = nr::ST<BWD>;
+    using nr::NT, nr::NW, nr::ST;
+    constexpr int NC = nr::NC<E>;
+    constexpr uint32_t STAGE = nr::STAGE<E, BWD>;
     constexpr bool WSM = BWD && DW && ROT != 0;      // the weights in shared memory: registers are short
     extern __shared__ __align__(16) uint8_t sm[];
     __shared__ uint64_t s_f[ROT ? 256 : 1];
@@ -214,62 +233,52 @@ __global__ void __launch_bounds__(nr::NT, nr::CPS) norm_rope_kernel(const NormAr
     const NormTensor t = a.t[which];
     const int plog2 = LOG >= 0 ? LOG : a.dlog2 - 4, D = 16 << plog2;
     const int j = lane & ((1 << plog2) - 1), grp = lane >> plog2, HB = 32 >> plog2;
-    // the lane's pieces: j and the one that holds the other values of its pairs (ROT 1) or half the head's
-    // on, so that neighbouring lanes have neighbouring pieces; likewise of those that are not turned
-    const int half = ROT == 1 ? a.rot >> 4 : 1 << plog2;
-    const int p0 = j < half ? j : j + half, p1 = p0 + (j < half ? half : (1 << plog2) - half);
+    const Places<E> at(j, 1 << plog2, a.rot, ROT == 1);
 
-    // passes of the tensor in order (token, heads): a warp's run of them
-    const int passes = (t.H + HB - 1) / HB;
-    const int64_t all = (int64_t)a.T * passes, nw = (int64_t)ctas * NW, gw = (int64_t)cta * NW + warp;
-    const int64_t first = all * gw / nw;
+    // a warp's run of passes; this lane's row of the pass that is brought next, and of the one that is
+    // computed next: token, head, and where the row begins
+    const int H = t.H;
+    const int64_t all = ((int64_t)a.T * H + HB - 1) >> (5 - plog2), nw = (int64_t)ctas * NW, gw = (int64_t)cta * NW + warp;
+    const int64_t first = all * gw / nw, row = (first << (5 - plog2)) + grp;
     const int left = (int)(all * (gw + 1) / nw - first);
-    int64_t tok = passes ? first / passes : 0;
-    int c = (int)(first - tok * passes);
-    // this lane's first piece of the pass that is brought next, and of the one that is stored next
-    const int64_t at0 = (c * HB + grp) * D + 8 * p0;
-    const E *xr = static_cast<const E *>(t.x) + tok * t.xs + at0;
-    const E *gr = BWD ? static_cast<const E *>(t.g) + tok * t.gs + at0 : nullptr;
-    E *yr = static_cast<E *>(t.y) + tok * t.ys + at0;
-    const int step = HB * D, back = (passes - 1) * step, p01 = 8 * (p1 - p0);
-    const bool in_last = (passes - 1) * HB + grp < t.H;      // this lane has a head in a token's last pass
+    const int at_t = HB / H, at_h = HB - at_t * H;           // a pass on
+    int tok = (int)(row / H), h = (int)(row - (int64_t)tok * H), tok_b = tok, h_b = h;
+    const int64_t in_row = (int64_t)h << a.dlog2;
+    const E *xr = static_cast<const E *>(t.x) + tok * t.xs + in_row;
+    const E *gr = BWD ? static_cast<const E *>(t.g) + tok * t.gs + in_row : nullptr;
+    E *yr = static_cast<E *>(t.y) + tok * t.ys + in_row;
+    auto next_row = [&](int &tk, int &hd) {                  // true: past the token's last head
+        tk += at_t, hd += at_h;
+        const bool past = hd >= H;
+        if (past) hd -= H, ++tk;
+        return past;
+    };
+    auto move = [&](auto *&p, int64_t stride, bool past) { p += at_t * stride + (at_h << a.dlog2) + (past ? stride - ((int64_t)H << a.dlog2) : 0); };
     const uint32_t ring = smem_u32(sm) + (uint32_t)warp * ST * STAGE + 16u * lane;
-    int cl = c, brought = 0;
+    int brought = 0;
     uint32_t fill = 0;
     auto bring = [&]() {
         if (brought < left) {
-            const bool has = cl < passes - 1 || in_last;
-            const E *x = has ? xr : static_cast<const E *>(t.x);
-            Piece<E>::bring(ring + fill, x, has);
-            Piece<E>::bring(ring + fill + PIECE, x + (has ? p01 : 0), has);
-            if constexpr (BWD) {
-                const E *g = has ? gr : static_cast<const E *>(t.g);
-                Piece<E>::bring(ring + fill + 2 * PIECE, g, has);
-                Piece<E>::bring(ring + fill + 3 * PIECE, g + (has ? p01 : 0), has);
+            const bool has = tok_b < a.T;                    // the last pass may have fewer rows
+#pragma unroll
+            for (int c = 0; c < NC; ++c) {
+                bring_chunk(ring + fill + 512u * c, has ? xr + at.at[c] : t.x, has);
+                if constexpr (BWD) bring_chunk(ring + fill + 512u * (NC + c), has ? gr + at.at[c] : t.g, has);
             }
-            if (++cl == passes) {
-                cl = 0;
-                xr += t.xs - back;
-                if (BWD) gr += t.gs - back;
-            } else {
-                xr += step;
-                if (BWD) gr += step;
-            }
+            const bool past = next_row(tok_b, h_b);
+            move(xr, t.xs, past);
+            if constexpr (BWD) move(gr, t.gs, past);
             ++brought;
         }
         fill = fill == (ST - 1) * STAGE ? 0 : fill + STAGE;
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    auto position = [&](int tk) { return a.positions ? a.positions[min(tk, a.T - 1)] : 0; };
 
     grid_dependency_wait();
 #pragma unroll 1
     for (int i = 0; i < ST - 1; ++i) bring();
-    // the position of the token at hand and of the next one
-    int p = 0, p_next = 0;
-    if (a.positions && left > 0) {
-        p = a.positions[tok];
-        if (tok + 1 < a.T) p_next = a.positions[tok + 1];
-    }
+    int p_next = left > 0 ? position(tok) : 0;
     if constexpr (ROT != 0)
         for (int i = tid; i < a.rot / 2; i += NT) s_f[i] = turn_fraction(a.freq[i]);
     uint64_t w[8];
@@ -277,10 +286,7 @@ __global__ void __launch_bounds__(nr::NT, nr::CPS) norm_rope_kernel(const NormAr
         for (int i = tid; i < D; i += NT) s_w[i] = t.w ? t.w[i] : 1.f;
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int at = 8 * (e < 4 ? p0 : p1) + 2 * (e & 3);
-            w[e] = t.w ? f2_pack(t.w[at], t.w[at + 1]) : f2_pack(1.f, 1.f);
-        }
+        for (int e = 0; e < 8; ++e) w[e] = t.w ? f2_pack(t.w[at.pair(e)], t.w[at.pair(e) + 1]) : f2_pack(1.f, 1.f);
     }
     if constexpr (ROT != 0) __syncthreads();
     uint64_t dw[DW ? 8 : 1];
@@ -288,67 +294,66 @@ __global__ void __launch_bounds__(nr::NT, nr::CPS) norm_rope_kernel(const NormAr
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[e] = 0;
 
-    Turn<ROT> turn(p0, p1, a.rot);
-    bool fresh = true;
+    Turn<E, ROT> turn(at, a.rot);
+    int turned = -1;                  // the token that `turn` is for
     uint32_t stage = 0;
 #pragma unroll 1
     for (int k = 0; k < left; ++k) {
         asm volatile("cp.async.wait_group %0;" ::"n"(ST - 2) : "memory");
         uint64_t f[8], d[BWD ? 8 : 1];
-        Piece<E>::get(ring + stage, f), Piece<E>::get(ring + stage + PIECE, f + 4);
-        if constexpr (BWD) Piece<E>::get(ring + stage + 2 * PIECE, d), Piece<E>::get(ring + stage + 3 * PIECE, d + 4);
+#pragma unroll
+        for (int c = 0; c < NC; ++c) {
+            Chunk<E>::get(ring + stage + 512u * c, f + 8 / NC * c);
+            if constexpr (BWD) Chunk<E>::get(ring + stage + 512u * (NC + c), d + 8 / NC * c);
+        }
         stage = stage == (ST - 1) * STAGE ? 0 : stage + STAGE;
         bring();          // into the place that was read in the pass before
-        const bool has = c < passes - 1 || in_last;
-        if (p < 0) {      // not a token: no output, and a gradient of zero (the warp's lanes agree)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = 0;
-        } else {
-            if constexpr (ROT != 0)
-                if (fresh) turn.template set<E>(s_f, p0, p1, (uint32_t)p);
-            fresh = false;
-            float r = 1.f;
-            if (a.norm) r = inverse_root<E>(fmaf(head_sum<LOG>(dot8(f, f), plog2), a.inv_n, a.eps));
-            const uint64_t r2 = f2_pack(r, r);
-            if constexpr (!BWD) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = f2_mul(f2_mul(f[e], r2), w[e]);
-                if constexpr (ROT != 0) turn.template apply<false>(f);
-            } else {
-                if constexpr (ROT != 0) turn.template apply<true>(d);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = f2_mul(f[e], r2);          // x r
-                if constexpr (DW)      // a lane without a head has zeros, and r may be infinite
-                    if (has)
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) dw[e] = f2_fma(d[e], f[e], dw[e]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (WSM)
-                        lds128(smem_u32(s_w + 8 * (e < 2 ? p0 : p1) + 4 * (e & 1)), w[2 * e], w[2 * e + 1]);
-                    d[2 * e] = f2_mul(d[2 * e], w[2 * e]), d[2 * e + 1] = f2_mul(d[2 * e + 1], w[2 * e + 1]);
-                }
-                if (a.norm) {
-                    const float dot = -head_sum<LOG>(dot8(d, f), plog2) * a.inv_n;
-                    const uint64_t k2 = f2_pack(dot, dot);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = f2_mul(r2, f2_fma(f[e], k2, d[e]));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) f[e] = d[e];
-                }
+        const int p = p_next, here = tok;
+        const bool has = here < a.T, live = has && p >= 0;   // p < 0: not a token, no output and a gradient of zero
+        const bool past = next_row(tok, h);
+        p_next = position(tok);
+        if constexpr (ROT != 0)
+            if (here != turned) {
+                turn.set(s_f, at, (uint32_t)p);
+                turned = here;
             }
-        }
-        if (has && (BWD || p >= 0)) Piece<E>::store(yr, f), Piece<E>::store(yr + p01, f + 4);
-        if (++c == passes) {
-            c = 0;
-            yr += t.ys - back;
-            p = p_next, fresh = true;
-            ++tok;
-            if (a.positions && tok + 1 < a.T) p_next = a.positions[tok + 1];
+        float r = 1.f;
+        if (a.norm) r = inverse_root<E>(fmaf(head_sum<LOG>(dot8(f, f), plog2), a.inv_n, a.eps));
+        const uint64_t r2 = f2_pack(r, r);
+        if constexpr (!BWD) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = f2_mul(f2_mul(f[e], r2), w[e]);
+            if constexpr (ROT != 0) turn.template apply<false>(f);
         } else {
-            yr += step;
+            if constexpr (ROT != 0) turn.template apply<true>(d);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = f2_mul(f[e], r2);          // x r
+            if constexpr (DW)
+                if (live)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) dw[e] = f2_fma(d[e], f[e], dw[e]);
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+                if constexpr (WSM) lds128(smem_u32(s_w + at.pair(e)), w[e], w[e + 1]);
+                d[e] = f2_mul(d[e], w[e]), d[e + 1] = f2_mul(d[e + 1], w[e + 1]);
+            }
+            if (a.norm) {
+                const float dot = -head_sum<LOG>(dot8(d, f), plog2) * a.inv_n;
+                const uint64_t k2 = f2_pack(dot, dot);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = f2_mul(r2, f2_fma(f[e], k2, d[e]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = d[e];
+            }
+            if (!live)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = 0;
         }
+        if (BWD ? has : live)
+#pragma unroll
+            for (int c = 0; c < NC; ++c) Chunk<E>::store(yr + at.at[c], f + 8 / NC * c);
+        move(yr, t.ys, past);
     }
     if constexpr (DW) {
         // lanes with the same values, then the warps, in a fixed order
@@ -364,7 +369,7 @@ __global__ void __launch_bounds__(nr::NT, nr::CPS) norm_rope_kernel(const NormAr
         float *s_dw = reinterpret_cast<float *>(sm);      // [NW][D], over the rings
         if (grp == 0)
 #pragma unroll
-            for (int e = 0; e < 16; ++e) s_dw[warp * D + 8 * (e < 8 ? p0 : p1) + (e & 7)] = d[e];
+            for (int e = 0; e < 16; ++e) s_dw[warp * D + at.pair(e >> 1) + (e & 1)] = d[e];
         __syncthreads();
         for (int i = tid; i < D; i += NT) {
             float s = 0.f;
@@ -400,21 +405,21 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const NormArgs a
 }
 
 // CTAs of both tensors: a warp for every RUN passes while the device has them, else all that are
-// resident, in proportion to the passes and (a token's sines and cosines) half a pass a token.
+// resident, in proportion to the passes and (the sines and cosines) half a pass for each that begins
+// tokens.
 int divide(NormArgs &a, int per_sm) {
     const int HB = 32 >> (a.dlog2 - 4);
-    int64_t passes[2], want[2];
+    int64_t passes[2], want[2], cost[2];      // without the half pass 59 us for the forward above
     for (int i = 0; i < 2; ++i) {
-        passes[i] = (int64_t)((a.t[i].H + HB - 1) / HB) * a.T;
+        passes[i] = ((int64_t)a.T * a.t[i].H + HB - 1) / HB;
         want[i] = (passes[i] + nr::RUN * nr::NW - 1) / (nr::RUN * nr::NW);
+        cost[i] = 2 * passes[i] + (a.rot ? std::min(passes[i], (int64_t)a.T) : 0);
     }
     const int most = per_sm * sm_count();
     if (want[0] + want[1] <= most) {
         a.split = (int)want[0];
         return (int)(want[0] + want[1]);
     }
-    int64_t cost[2];      // without the half pass 59 us for the forward above
-    for (int i = 0; i < 2; ++i) cost[i] = 2 * passes[i] + (a.rot && passes[i] ? a.T : 0);
     int q = (int)((most * cost[0] + (cost[0] + cost[1]) / 2) / (cost[0] + cost[1]));
     if (passes[0] && q < 1) q = 1;
     if (passes[1] && q > most - 1) q = most - 1;
@@ -430,7 +435,7 @@ cudaError_t launch_norm_k(NormArgs &a, float *dwq, float *dwk, float *ws, cudaSt
         a.t[1].part = ws + ((size_t)a.split << a.dlog2);
     }
     if (ctas > 0) {
-        constexpr size_t smem = (size_t)nr::NW * nr::ST<BWD> * nr::STAGE<E, BWD>;
+        constexpr size_t smem = (size_t)nr::NW * nr::ST * nr::STAGE<E, BWD>;
         auto kernel = norm_rope_kernel<E, ROT, LOG, BWD, DW>;
         static std::atomic<uint64_t> allowed{0};
         cudaError_t e = allow_smem(kernel, smem, allowed);
