@@ -83,7 +83,8 @@ gdr_status_t check_norm(const NormShape &n) {
     if (!(n.eps >= 0.0f) || !std::isfinite(n.eps)) return GDR_ERR_INVALID_ARG;
     if (n.norm != GDR_NORM_NONE && n.norm != GDR_NORM_RMS && n.norm != GDR_NORM_L2) return GDR_ERR_INVALID_ARG;
     if (n.pairs != GDR_ROPE_HALF && n.pairs != GDR_ROPE_ADJACENT) return GDR_ERR_INVALID_ARG;
-    if (!dtype_ok(n.dtype) || n.D < 16 || n.D > 512 || (n.D & (n.D - 1)) || n.Hq > 65536 || n.Hk > 65536)
+    if (!dtype_ok(n.dtype) || n.D < 16 || n.D > 512 || (n.D & (n.D - 1)) || n.Hq > 65536 || n.Hk > 65536 ||
+        n.T > (1 << 30))
         return GDR_ERR_UNSUPPORTED;
     if (n.rot_dim > n.D || n.rot_dim % 16) return GDR_ERR_UNSUPPORTED;
     if (n.rot_dim > 0 && n.T > 0 && (!n.positions || !n.freq)) return GDR_ERR_INVALID_ARG;

@@ -22,10 +22,11 @@
 //
 // Bound: bytes (forward 2, backward 3 times the tensors).  Measured, 16384 tokens, 32 + 8 heads of
 // 128 bf16 values out of one projection, weights and rotation: forward (336 MB, 50 us at the
-// measured copy rate) 56 us, backward with the weights' gradients (503 MB, 75 us) 84 us; 65536 tokens of
-// 64 heads to unit length (2147 MB, 322 us) 325 us.  With the pieces in registers, four passes'
-// (forward) or two (backward) in flight: 60 and 98 us, since the backward's registers then spill;
-// rings of 4 passes 62 and 88, of 8 forward 65 us.
+// measured copy rate) 56 us, backward with the weights' gradients (503 MB, 75 us) 82 us; in fp32 105 and
+// 162 us; 65536 tokens of 64 heads to unit length (2147 MB, 322 us) 333 us, of 1 + 1 heads with rotation
+// (67 MB) 16 us, of 8 + 8 heads of 64 values (268 MB) 51 us: a token's sines and cosines then serve one
+// pass.  Rings of 2, 3 and 4 passes: 65, 56 and 58 us bf16, 105, 113 and 114 fp32.  With the values in
+// registers, four passes' (forward) or two (backward) in flight: 60 and 98 us (the backward's spill).
 
 #include "gdr_launch.cuh"
 
@@ -37,7 +38,7 @@ namespace {
 namespace nr {
 constexpr int NT = 256, NW = NT / 32;
 constexpr int CPS = 2;                                            // CTAs an SM
-constexpr int ST = 3;                                             // passes of a warp's ring
+template <typename E> constexpr int ST = sizeof(E) == 4 ? 2 : 3;  // passes of a warp's ring
 template <typename E> constexpr int NC = sizeof(E);               // chunks of a lane's 16 values
 template <typename E, bool BWD> constexpr uint32_t STAGE = (BWD ? 2 : 1) * NC<E> * 512;   // bytes of a warp's pass
 constexpr int RUN = 4;         // passes of a warp where there are few
@@ -220,8 +221,8 @@ __device__ __forceinline__ uint64_t dot8(const uint64_t (&a)[8], const uint64_t 
 // any.  BWD: the backward; DW: and the weights' gradients.
 template <typename E, int ROT, int LOG, bool BWD, bool DW>
 __global__ void __launch_bounds__(nr::NT, nr::CPS) norm_rope_kernel(const NormArgs a) {
-    using nr::NT, nr::NW, nr::ST;
-    constexpr int NC = nr::NC<E>;
+    using nr::NT, nr::NW;
+    constexpr int NC = nr::NC<E>, ST = nr::ST<E>;
     constexpr uint32_t STAGE = nr::STAGE<E, BWD>;
     constexpr bool WSM = BWD && DW && ROT != 0;      // the weights in shared memory: registers are short
     extern __shared__ __align__(16) uint8_t sm[];
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const NormArgs a
 // tokens.
 int divide(NormArgs &a, int per_sm) {
     const int HB = 32 >> (a.dlog2 - 4);
-    int64_t passes[2], want[2], cost[2];      // without the half pass 59 us for the forward above
+    int64_t passes[2], want[2], cost[2];      // without the half pass 59 us for 32 + 8 heads, 56 with it
     for (int i = 0; i < 2; ++i) {
         passes[i] = ((int64_t)a.T * a.t[i].H + HB - 1) / HB;
         want[i] = (passes[i] + nr::RUN * nr::NW - 1) / (nr::RUN * nr::NW);
@@ -435,7 +436,7 @@ cudaError_t launch_norm_k(NormArgs &a, float *dwq, float *dwk, float *ws, cudaSt
         a.t[1].part = ws + ((size_t)a.split << a.dlog2);
     }
     if (ctas > 0) {
-        constexpr size_t smem = (size_t)nr::NW * nr::ST * nr::STAGE<E, BWD>;
+        constexpr size_t smem = (size_t)nr::NW * nr::ST<E> * nr::STAGE<E, BWD>;
         auto kernel = norm_rope_kernel<E, ROT, LOG, BWD, DW>;
         static std::atomic<uint64_t> allowed{0};
         cudaError_t e = allow_smem(kernel, smem, allowed);

@@ -714,7 +714,8 @@ typedef enum {
  *   freq      fp64 [rot_dim / 2], radians a position (for example theta^(-2 i / rot_dim)); may be
  *             NULL with rot_dim 0
  *   q_out, k_out  as q and k, strides of their own; may be q and k themselves (with their strides)
- * D a power of two from 16 to 512, rot_dim a multiple of 16 up to D (GDR_ERR_UNSUPPORTED otherwise);
+ * D a power of two from 16 to 512, rot_dim a multiple of 16 up to D, T up to 2^30, Hq and Hk up to
+ * 65536 (GDR_ERR_UNSUPPORTED otherwise);
  * eps finite, >= 0.  Angles are taken modulo a whole turn in 64-bit fixed point, so they are as good
  * at position 2^31 - 1 as at 1.  Arithmetic in fp32 (|x|^2 overflows where |x| passes 1.8e19),
  * rounded once.  One launch, no workspace.

@@ -38,7 +38,7 @@ BOTH = [
     (dict(rot=144), 2), (dict(rot=8), 2), (dict(rot=40), 2), (dict(pos=None), 1), (dict(freq=None), 1),
     (dict(q=None), 1), (dict(k=None), 1), (dict(qo=None), 1), (dict(ko=None), 1), (dict(q=ODD), 1), (dict(ko=ODD), 1),
     (dict(qs=1023), 1), (dict(qs=1028), 1), (dict(ks=255), 1), (dict(qos=-1024), 1), (dict(kos=252), 1),
-    (dict(qs=2 ** 40), 1),
+    (dict(qs=2 ** 40), 1), (dict(T=2 ** 30 + 1), 2),
 ]
 
 

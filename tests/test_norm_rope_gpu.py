@@ -127,6 +127,10 @@ CASES = [
     (2000, 33, 1, 128, 128, "half", "rms", "bf16", True),
     (2000, 1, 33, 128, 112, "adjacent", "rms", "f32", True),
     (9000, 8, 2, 64, 64, "half", "rms", "bf16", False),
+    (3001, 1, 2, 128, 128, "half", "rms", "bf16", True),         # rows of several tokens in a warp's pass
+    (777, 3, 5, 32, 32, "adjacent", "rms", "f32", True),
+    (1500, 7, 1, 16, 16, "half", "l2", "bf16", False),
+    (400, 3, 3, 256, 128, "half", "rms", "f32", True),
 ]
 
 
