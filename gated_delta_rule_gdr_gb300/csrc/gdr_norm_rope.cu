@@ -118,14 +118,14 @@ template <typename E> struct Places {
 
 // frac(f / 2 pi) 2^64.  1 / (2 pi) in two doubles, so that F is good to its last bits.
 __device__ __forceinline__ uint64_t turn_fraction(double f) {
-    constexpr double c = 0.15915494309189535, c_lo = -9.839338337591978e-18;
+    constexpr double c = 0.15915494309189535, c_lo = -9.839338337591243e-18;
     const double t = f * c, t_lo = fma(f, c, -t) + f * c_lo;
     double x = t - floor(t);
     x = x < 1.0 ? x : 0.0;
     return (uint64_t)(x * 18446744073709551616.0) + (uint64_t)(int64_t)(t_lo * 18446744073709551616.0);
 }
 // Sine and cosine of a 32-bit fraction of a turn.  bf16: the hardware's approximations (absolute error
-// 2^-20, a rounding is 2^-9 of a value).  fp32: the quarter turn is taken off while the angle is
+// 2^-20, a rounding is 2^-8 of a value).  fp32: the quarter turn is taken off while the angle is
 // an integer, so that what remains converts to 2^-25 of an eighth of a turn.
 template <typename E>
 __device__ __forceinline__ void turn_sincos(uint32_t hi, float &s, float &c) {
