@@ -98,7 +98,6 @@ struct SharedRow : TileRow {
 };
 template <bool FIRST>            // the first pass
 struct SharedArgs : AttnArgs {
-    static constexpr bool first = FIRST;
     using Req = SharedRequest;
     using Row = SharedRow;
     const int *group, *shared, *lead;

@@ -291,9 +291,10 @@ __global__ void __launch_bounds__(nr::NT, nr::CPS) norm_rope_kernel(const NormAr
     }
     if constexpr (ROT != 0) __syncthreads();
     uint64_t dw[DW ? 8 : 1];
-    if constexpr (DW)
+    if constexpr (DW) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[e] = 0;
+    }
 
     Turn<E, ROT> turn(at, a.rot);
     int turned = -1;                  // the token that `turn` is for
@@ -329,10 +330,12 @@ __global__ void __launch_bounds__(nr::NT, nr::CPS) norm_rope_kernel(const NormAr
             if constexpr (ROT != 0) turn.template apply<true>(d);
 #pragma unroll
             for (int e = 0; e < 8; ++e) f[e] = f2_mul(f[e], r2);          // x r
-            if constexpr (DW)
-                if (live)
+            if constexpr (DW) {
+                if (live) {
 #pragma unroll
                     for (int e = 0; e < 8; ++e) dw[e] = f2_fma(d[e], f[e], dw[e]);
+                }
+            }
 #pragma unroll
             for (int e = 0; e < 8; e += 2) {
                 if constexpr (WSM) lds128(smem_u32(s_w + at.pair(e)), w[e], w[e + 1]);
