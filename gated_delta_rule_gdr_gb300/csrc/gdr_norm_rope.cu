@@ -23,7 +23,7 @@
 // Bound: bytes (forward 2, backward 3 times the tensors).  Measured, 16384 tokens, 32 + 8 heads of
 // 128 bf16 values out of one projection, weights and rotation: forward (336 MB, 50 us at the
 // measured copy rate) 56 us, backward with the weights' gradients (503 MB, 75 us) 82 us; in fp32 105 and
-// 162 us; 65536 tokens of 64 heads to unit length (2147 MB, 322 us) 333 us, of 1 + 1 heads with rotation
+// 162 us; 65536 tokens of 64 heads to unit length (2147 MB, 322 us) 330 us, of 1 + 1 heads with rotation
 // (67 MB) 16 us, of 8 + 8 heads of 64 values (268 MB) 51 us: a token's sines and cosines then serve one
 // pass.  Rings of 2, 3 and 4 passes: 65, 56 and 58 us bf16, 105, 113 and 114 fp32.  With the values in
 // registers, four passes' (forward) or two (backward) in flight: 60 and 98 us (the backward's spill).
@@ -37,8 +37,11 @@ namespace {
 
 namespace nr {
 constexpr int NT = 256, NW = NT / 32;
-constexpr int CPS = 2;                                            // CTAs an SM
-template <typename E> constexpr int ST = sizeof(E) == 4 ? 2 : 3;  // passes of a warp's ring
+// CTAs an SM, passes of a warp's ring.  Without rotation or gradients three bf16 CTAs have the registers
+// (4096 tokens of 32 heads to unit length, from the L2, 7.8 us against 9.4; 65536 of 64 330 against 332; in
+// fp32 16384 of 32 heads 87 against 83).
+template <typename E, int ROT, bool BWD> constexpr int CPS = sizeof(E) == 2 && ROT == 0 && !BWD ? 3 : 2;
+template <typename E, int ROT, bool BWD> constexpr int ST = sizeof(E) == 4 || CPS<E, ROT, BWD> == 3 ? 2 : 3;
 template <typename E> constexpr int NC = sizeof(E);               // chunks of a lane's 16 values
 template <typename E, bool BWD> constexpr uint32_t STAGE = (BWD ? 2 : 1) * NC<E> * 512;   // bytes of a warp's pass
 constexpr int RUN = 4;         // passes of a warp where there are few
@@ -220,9 +223,9 @@ __device__ __forceinline__ uint64_t dot8(const uint64_t (&a)[8], const uint64_t 
 // ROT: 0 no rotation, 1 pairs (i, i + rot / 2), 2 pairs (2 i, 2 i + 1).  LOG: log2 of D / 16, or -1:
 // any.  BWD: the backward; DW: and the weights' gradients.
 template <typename E, int ROT, int LOG, bool BWD, bool DW>
-__global__ void __launch_bounds__(nr::NT, nr::CPS) norm_rope_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(nr::NT, (nr::CPS<E, ROT, BWD>)) norm_rope_kernel(const NormArgs a) {
     using nr::NT, nr::NW;
-    constexpr int NC = nr::NC<E>, ST = nr::ST<E>;
+    constexpr int NC = nr::NC<E>, ST = nr::ST<E, ROT, BWD>;
     constexpr uint32_t STAGE = nr::STAGE<E, BWD>;
     constexpr bool WSM = BWD && DW && ROT != 0;      // the weights in shared memory: registers are short
     extern __shared__ __align__(16) uint8_t sm[];
@@ -433,13 +436,13 @@ int divide(NormArgs &a, int per_sm) {
 
 template <typename E, int ROT, int LOG, bool BWD, bool DW>
 cudaError_t launch_norm_k(NormArgs &a, float *dwq, float *dwk, float *ws, cudaStream_t s) {
-    const int ctas = divide(a, nr::CPS);
+    const int ctas = divide(a, nr::CPS<E, ROT, BWD>);
     if (DW) {
         a.t[0].part = ws;
         a.t[1].part = ws + ((size_t)a.split << a.dlog2);
     }
     if (ctas > 0) {
-        constexpr size_t smem = (size_t)nr::NW * nr::ST<E> * nr::STAGE<E, BWD>;
+        constexpr size_t smem = (size_t)nr::NW * nr::ST<E, ROT, BWD> * nr::STAGE<E, BWD>;
         auto kernel = norm_rope_kernel<E, ROT, LOG, BWD, DW>;
         static std::atomic<uint64_t> allowed{0};
         cudaError_t e = allow_smem(kernel, smem, allowed);
@@ -482,7 +485,7 @@ NormArgs norm_args(const NormCall &c) {
 
 }  // namespace
 
-size_t norm_rope_workspace_bytes(int D) { return (size_t)nr::CPS * sm_count() * D * sizeof(float); }
+size_t norm_rope_workspace_bytes(int D) { return (size_t)nr::CPS<float, 0, true> * sm_count() * D * sizeof(float); }
 
 cudaError_t launch_norm_rope(const NormCall &c, bool bwd, float *dwq, float *dwk, void *ws, Elem e, cudaStream_t s) {
     NormArgs a = norm_args(c);
