@@ -28,6 +28,6 @@ cudaError_t launch_kv8_attn(const void *q, int64_t q_stride, const void *k_cache
     return launch_split_any(a, sh, k_cache, v_cache, D, e, kv, ws, (int64_t)max_q * a.G, s);
 }
 
-cudaError_t take_kv8_split_error_word(unsigned *value) { return take_error_word(value); }
+cudaError_t take_kv8_split_error_word(unsigned *value) { return take_attn_error_word(value); }
 
 }  // namespace gdr

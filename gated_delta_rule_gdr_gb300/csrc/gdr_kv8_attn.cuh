@@ -613,6 +613,15 @@ SharedArgs<FIRST> shared_args(const KvSharedCall &c, float *pre_o, float2 *pre_m
     return a;
 }
 
+// Whether this translation unit has launched an attention kernel.  Until it has, its error word is zero,
+// and reading it would load the unit's kernels for nothing (with the words of all five units the first
+// gdr_last_device_error of a process took 54 ms, later ones 125 us; without them 1.6 ms and 79 us).
+std::atomic<bool> attended{false};
+cudaError_t take_attn_error_word(unsigned *value) {
+    *value = 0;
+    return attended.load(std::memory_order_relaxed) ? take_error_word(value) : cudaSuccess;
+}
+
 // Entries, then {M, l}, then the sums.
 size_t part_bytes(int ctas, int RB, int D) {
     return (size_t)ctas * (sizeof(int4) + (size_t)2 * RB * (2 + D) * sizeof(float));

@@ -215,6 +215,6 @@ cudaError_t launch_kv8_shared(const KvSharedCall &call, void *ws, cudaStream_t s
     return launch_pass<false>(c, pre_o, pre_ml, parts, s);
 }
 
-cudaError_t take_kv8_shared_error_word(unsigned *value) { return take_error_word(value); }
+cudaError_t take_kv8_shared_error_word(unsigned *value) { return take_attn_error_word(value); }
 
 }  // namespace gdr

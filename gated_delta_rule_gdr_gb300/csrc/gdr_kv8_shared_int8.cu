@@ -14,6 +14,6 @@ cudaError_t launch_kv8_shared_int8(const KvSharedCall &c, bool first, float *pre
     return launch_tile_kv<Kv8::INT8>(a, c.D, parts, (int64_t)c.max_q * a.G, s);
 }
 
-cudaError_t take_kv8_shared_int8_error_word(unsigned *value) { return take_error_word(value); }
+cudaError_t take_kv8_shared_int8_error_word(unsigned *value) { return take_attn_error_word(value); }
 
 }  // namespace gdr

@@ -587,6 +587,7 @@ cudaError_t launch_split_r(A &a, const void *kc, const void *vc, void *ws, int64
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(kernel, sp::SMEM<R, D>, allowed);
     if (e != cudaSuccess) return e;
+    attended.store(true, std::memory_order_relaxed);
     if ((e = launch_after(kernel, dim3((unsigned)ctas), 32 * sp::NW, sp::SMEM<R, D>, s, mk, mv, a)) != cudaSuccess)
         return e;
     return launch_merge<E, D, RB>(a, rows, s);

@@ -23,6 +23,6 @@ cudaError_t launch_kv8_tile(const void *q, int64_t q_stride, const void *k_cache
     return kv == Kv8::E4M3 ? launch_tile_kv<Kv8::E4M3>(a, D, ws, rows, s) : launch_tile_kv<Kv8::INT8>(a, D, ws, rows, s);
 }
 
-cudaError_t take_kv8_tile_error_word(unsigned *value) { return take_error_word(value); }
+cudaError_t take_kv8_tile_error_word(unsigned *value) { return take_attn_error_word(value); }
 
 }  // namespace gdr

@@ -1245,6 +1245,7 @@ cudaError_t launch_tile_g(A &a, void *ws, int ctas, int64_t rows, cudaStream_t s
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(kernel, L::SMEM, allowed);
     if (e != cudaSuccess) return e;
+    attended.store(true, std::memory_order_relaxed);
     if ((e = launch_after(kernel, dim3((unsigned)ctas), tl::NT, L::SMEM, s, a)) != cudaSuccess) return e;
     return launch_merge<__nv_bfloat16, D, L::RB>(a, rows, s);
 }
