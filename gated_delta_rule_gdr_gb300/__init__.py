@@ -626,6 +626,12 @@ def _rows(t, name):
     return t.data_ptr(), st[0] if n > 1 else h * d
 
 
+def _scratch(workspace, need):
+    """A workspace that was given: `need` bytes in a row, which an expanded or strided tensor has not."""
+    if workspace.dtype is not torch.uint8 or not workspace.is_cuda or workspace.numel() < need or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous uint8 CUDA tensor of at least {need} bytes")
+
+
 def _kv8_cache(k_cache, v_cache, k_scale, v_scale):
     code = KV8.get(k_cache.dtype)
     if code is None or v_cache.dtype is not k_cache.dtype:
@@ -728,8 +734,8 @@ def kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, scale: 
     need = lib.gdr_kv8_attn_workspace_size(S, max_q, T, Hq, Hkv, D, el)
     if workspace is None:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    elif workspace.dtype is not torch.uint8 or not workspace.is_cuda or workspace.numel() < need:
-        raise ValueError(f"workspace must be a uint8 CUDA tensor of at least {need} bytes")
+    else:
+        _scratch(workspace, need)
     code = lib.gdr_kv8_attn(qp, qst, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
                             v_scale.data_ptr(), _int(block_table, "block_table"),
                             _int(kv_len, "kv_len", (S,)),
@@ -797,8 +803,8 @@ def kv8_attn_shared(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, 
     need = lib.gdr_kv8_attn_shared_workspace_size(S, max_q, groups, max_group_q, T, Hq, Hkv, D, el)
     if workspace is None:
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
-    elif workspace.dtype is not torch.uint8 or not workspace.is_cuda or workspace.numel() < need:
-        raise ValueError(f"workspace must be a uint8 CUDA tensor of at least {need} bytes")
+    else:
+        _scratch(workspace, need)
     here = _all_here(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, cu_q, cu_group, shared, lead, out,
                      workspace)
     code = lib.gdr_kv8_attn_shared(qp, qst, k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
@@ -910,8 +916,8 @@ def qk_norm_rope_bwd(q, k, d_q_out, d_k_out, *, norm="rms", q_weight=None, k_wei
         wn = lib.gdr_qk_norm_rope_bwd_workspace_size(D)
         if workspace is None:
             workspace = torch.empty(max(wn, 16), dtype=torch.uint8, device=q.device)
-        elif workspace.dtype is not torch.uint8 or not workspace.is_cuda or workspace.numel() < wn:
-            raise ValueError(f"workspace must be a uint8 CUDA tensor of at least {wn} bytes")
+        else:
+            _scratch(workspace, wn)
         wp = workspace.data_ptr()
     here = _all_here(q, k, q_weight, k_weight, positions, freq, d_q_out, d_k_out if k is not None else None, d_q,
                      d_k if k is not None else None, workspace if wp is not None else None)
