@@ -31,7 +31,8 @@ __all__ = ["GdrError", "load", "chunk_fwd", "decode_step", "chunk_decay", "chunk
            "set_option", "get_option", "option", "mla_decode", "mla_decode_workspace_size",
            "chunk_bwd", "chunk_bwd_workspace_size", "chunk_saved_size", "chunk_fwd_train",
            "chunk_bwd_saved", "page_plan", "kv8_append", "kv8_attn", "kv8_attn_workspace_size",
-           "KV8", "kv8_shared_plan", "kv8_attn_shared", "kv8_attn_shared_workspace_size", "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_size", "NORM", "PAIRS"]
+           "KV8", "kv8_shared_plan", "kv8_attn_shared", "kv8_attn_shared_workspace_size",
+           "qk_norm_rope", "qk_norm_rope_bwd", "qk_norm_rope_bwd_workspace_size", "NORM", "PAIRS"]
 
 DECAY = {"affine": 0, "log": 1}   # gdr_decay_t
 STATUS = {0: "GDR_OK", 1: "GDR_ERR_INVALID_ARG", 2: "GDR_ERR_UNSUPPORTED", 3: "GDR_ERR_RANGE",
@@ -751,8 +752,10 @@ def kv8_attn(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, scale: 
 def kv8_shared_plan(block_table, kv_len, cu_group, page: int, *, cu_q=None):
     """What the requests of each group have in common, for kv8_attn_shared (once a step for all
     layers).  block_table [S,W], kv_len [S], cu_group [groups + 1] (group g: the requests cu_group[g]
-    up to cu_group[g + 1]) and cu_q [S+1] (None: one query a request) int32.  Returns int32 (shared [S]:
-    tokens of the pages in common, lead [groups]: the request whose row they are read by, -1: none)."""
+    up to cu_group[g + 1]; ascending) and cu_q [S+1] (None: one query a request) int32.  A group has in
+    common what all of its requests with queries have, so one that leaves the prefix early belongs in
+    another.  Returns int32 (shared [S]: tokens of the pages in common, lead [groups]: the request whose row
+    they are read by, -1: none)."""
     lib = _lib or load()
     S, W = block_table.shape
     groups, dev = cu_group.numel() - 1, block_table.device
@@ -775,10 +778,10 @@ def kv8_attn_shared_workspace_size(S, max_q, groups, max_group_q, total_q, Hq, H
 def kv8_attn_shared(q, k_cache, v_cache, k_scale, v_scale, block_table, kv_len, scale: float, cu_group, shared, lead, *,
                     cu_q=None, max_q: int = None, max_group_q: int, out=None, want_lse: bool = False, workspace=None):
     """kv8_attn for requests that share prefixes: the pages that the requests of a group have in common
-    are read once for all of them.  cu_group, shared, lead: kv8_shared_plan's, for these tables and
-    lengths; max_group_q: the most queries that the requests of a group have together; the rest as
-    kv8_attn.  workspace: None (allocated here) or a uint8 CUDA tensor of kv8_attn_shared_workspace_size
-    bytes.  Returns out, or (out, lse) if want_lse."""
+    are read once for all of them.  cu_group, shared, lead: kv8_shared_plan's, for these very tables,
+    lengths, cu_q and groups (another step's give wrong results); max_group_q: the most queries that the
+    requests of a group have together; the rest as kv8_attn.  workspace: None (allocated here) or a uint8
+    CUDA tensor of kv8_attn_shared_workspace_size bytes.  Returns out, or (out, lse) if want_lse."""
     lib = _lib or load()
     kv, (N, Hkv, P, D) = _kv8_cache(k_cache, v_cache, k_scale, v_scale)
     qp, qst = _rows(q, "q")
@@ -865,9 +868,9 @@ def qk_norm_rope(q, k=None, *, norm="rms", q_weight=None, k_weight=None, eps: fl
     """Norms of queries and keys for each head and the rotation by position, in one pass.  q [T,Hq,D]
     and k [T,Hk,D] (or None) fp32 or bf16, tokens may be strided; norm "rms" (mean square), "l2" (unit
     length) or "none"; q_weight, k_weight [D] fp32 or None; positions [T] int32 (negative: not a token,
-    its outputs are left as they were); freq [rot_dim / 2] fp64, radians a position (None: no
-    rotation); pairs "half" (i, i + rot_dim / 2) or "adjacent" (2 i, 2 i + 1).  q_out, k_out may be q and
-    k.  Returns (q_out, k_out)."""
+    its rows of q_out and k_out are left as they were, and hold anything where these are allocated here);
+    freq [rot_dim / 2] fp64, radians a position (None: no rotation); pairs "half" (i, i + rot_dim / 2) or
+    "adjacent" (2 i, 2 i + 1).  q_out, k_out may be q and k.  Returns (q_out, k_out)."""
     lib = _lib or load()
     qp, qst = _rows(q, "q")
     kp, kst = (None, 0) if k is None else _rows(k, "k")

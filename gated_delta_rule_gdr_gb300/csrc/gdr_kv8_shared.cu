@@ -15,10 +15,12 @@
 // Measured: 256 single tokens of 8 heads a cached head, four groups with 17 to 32 k common tokens and up to
 // 2000 of their own (372 MB, 107 GFLOP: 56 us either way) 237 us, gdr_kv8_attn 928: the tile kernel 154 (four
 // of eleven blocks of 256 rows are half empty; 2.6 us a block and 128 keys), its merge 10, the own tokens 72
-// (270 MB, 1000 keys an item: its ends weigh), their merge 7.  24 questions of up to 200 tokens of 4 heads a
+// (270 MB, 1000 keys an item: its ends weigh; 3.8 TB/s), their merge 7.  24 questions of up to 200 tokens of 4 heads a
 // cached head on 20 k (595 GFLOP, 310 us) 647 us, gdr_kv8_attn 800: 1000 TFLOP/s in the first pass (570 us),
 // the rest the questions' own tiles and 60 MB of sums on their way.
-// The plan: 256 requests in 8 groups 3.5 us, 1000 rows of 4096 entries (16.4 MB) 7.4 us, two launches.
+// The plan: 256 requests in 8 groups 3.5 us, 1000 rows of 4096 entries (16.4 MB) 7.4 us, two launches; every
+// CTA of the first goes through all groups and its own group's requests, which 8192 requests in one group
+// make 51 us (in 8 groups 14, in 64 or 512 12).
 
 #include "gdr_kv8_split.cuh"
 
@@ -147,7 +149,12 @@ size_t pre_bytes(int total_q, int Hq, int D) { return align32((size_t)total_q * 
 // takes pairs, the sums' way through memory, and the ends of items that are twice as many.
 // Where the two are even, measured / by this rule, with 4 cached heads of 8 query heads: 8, 16, 32, 64 decodes
 // 22 / 22, 9 / 10, 5.2 / 5.7, 2.9 / 2.9 thousand common tokens; 24 x 5 drafted 6 / 6; prompts of 64 or 300
-// tokens: none up to 16 k / none, 20.
+// tokens: none up to 16 k / none, 20.  (2.4 a pair fits these; whole passes of many blocks took 2.6, above.)
+// What the rule leaves out: lengths, so it does not see work that does not fill the SMs, nor a batch with
+// groups on both sides of the bound.  75 decodes of 8 heads and one cached head in 6 groups of 10 to 21 k
+// common tokens 46 us, gdr_kv8_attn 34; 18 x 2 to 5 drafted in groups of 0 to 31 k 99 and 36 (the short items of
+// the second pass stand together, and with fewer units than 9 a CTA their ends do not count in the division).
+// Of 7543 drawn batches 3.1 % were more than a tenth slower than gdr_kv8_attn, 0.3 % more than half.
 // (`rows` of one request or group on average, at most `most`; alike: all have that many, else the last
 // block of each is half full; ends: what the ends of its items cost in units)
 double keys_cost(int64_t most, double rows, bool alike, int D, Elem e, double *ends) {

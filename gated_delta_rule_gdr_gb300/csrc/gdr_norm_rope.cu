@@ -22,8 +22,8 @@
 //
 // Bound: bytes (forward 2, backward 3 times the tensors).  Measured, 16384 tokens, 32 + 8 heads of
 // 128 bf16 values out of one projection, weights and rotation: forward (336 MB, 50 us at the
-// measured copy rate) 56 us, backward with the weights' gradients (503 MB, 75 us) 82 us; in fp32 105 and
-// 162 us; 65536 tokens of 64 heads to unit length (2147 MB, 322 us) 330 us, of 1 + 1 heads with rotation
+// measured copy rate) 56 us, backward with the weights' gradients (503 MB, 75 us) 82 us; in fp32 106 and
+// 163 us; 65536 tokens of 64 heads to unit length (2147 MB, 322 us) 326 us, of 1 + 1 heads with rotation
 // (67 MB) 16 us, of 8 + 8 heads of 64 values (268 MB) 51 us: a token's sines and cosines then serve one
 // pass.  Rings of 2, 3 and 4 passes: 65, 56 and 58 us bf16, 105, 113 and 114 fp32.  With the values in
 // registers, four passes' (forward) or two (backward) in flight: 60 and 98 us (the backward's spill).

@@ -648,13 +648,17 @@ gdr_status_t gdr_kv8_attn(const void *q, int64_t q_stride, const void *k_cache, 
  * The same attention for requests that share a prefix: a system prompt, a document that many requests
  * ask about, samples of one prompt.  Their rows of the block table begin with the same pages (the
  * prefix's own entries, copied; page_plan then counts them as the request's, so set them to -1 before a
- * request ends, or the prefix's pages return to the free ring).  gdr_kv8_attn_shared reads such pages
- * once for all queries of a group of requests instead of once a request; its result is gdr_kv8_attn's
- * but for rounding.
+ * request ends, or the prefix's pages return to the free ring).  Full pages only: a page that a request's
+ * new tokens go to is its own.  gdr_kv8_attn_shared reads such pages once for all queries of a group of
+ * requests instead of once a request; its result is gdr_kv8_attn's but for rounding.
+ * There is one level, and a group has in common what all of its requests with queries have: one that
+ * leaves the prefix early, or has no more than a few tokens yet, costs the whole group what comes after
+ * that, so such a request belongs in a group of its own (or in none).
  *
  * gdr_kv8_shared_plan finds what there is to share, once a step for all layers:
- *   cu_group  [num_groups + 1] int32, ascending: group g is the requests cu_group[g] .. cu_group[g + 1] - 1,
- *             which stand together in the batch; requests outside every group share nothing
+ *   cu_group  [num_groups + 1] int32, ascending (so no request is in two groups): group g is the requests
+ *             cu_group[g] .. cu_group[g + 1] - 1, which stand together in the batch; requests outside every
+ *             group share nothing
  *   cu_q      [S+1] or NULL (one query a request), kv_len [S], block_table: as gdr_kv8_attn
  *   shared    [S] out: tokens of the first pages that the request has in common with all requests of its
  *             group that have queries: whole pages, equal entries in all these rows, and seen by every
@@ -665,16 +669,19 @@ gdr_status_t gdr_kv8_attn(const void *q, int64_t q_stride, const void *k_cache, 
  * > 8192, another page size, table_width * page > 2^31 - 256: GDR_ERR_UNSUPPORTED.
  *
  * gdr_kv8_attn_shared: the arguments of gdr_kv8_attn, the plan's cu_group, and its shared and lead
- *   for these block_table, kv_len and cu_q (others give wrong results, but read nothing outside the
- *   tensors).
+ *   for these very block_table, kv_len, cu_q and cu_group: nothing is compared again, and a plan of an
+ *   earlier step or of other groups, or a cu_group that is not ascending, gives wrong results (but reads
+ *   and writes nothing outside the tensors).
  *   max_group_q  the most queries that the requests of a group have together: it chooses a kernel, as
  *             max_q does
  *   workspace  16-byte aligned, gdr_kv8_attn_shared_workspace_size bytes: the sums over the common pages
- *             (fp32, Hq * (D + 2) values a query) and partial results; scratch on entry and exit, not
- *             shared with a call still running on another stream
+ *             (fp32, Hq * (D + 2) values a query, whether a call then uses them or not) and partial
+ *             results; scratch on entry and exit, not shared with a call still running on another stream
  * Two passes of two launches each, or gdr_kv8_attn's one where the sizes say that a pass of its own costs
  * more than the common pages (by a cost model; GDR_OPT_SHARED_LEAST forces either): with 32 query and 4
- * cached heads 8 single tokens want some 22 thousand common tokens, 64 some 3 thousand.
+ * cached heads 8 single tokens want some 22 thousand common tokens, 64 some 3 thousand.  The model knows
+ * sizes, no lengths: a batch of few long prefixes, or of prefixes on both sides of its bound, can take
+ * longer than gdr_kv8_attn (3 of 100 drawn batches by more than a tenth, the worst 2.8 times as long).
  */
 gdr_status_t gdr_kv8_shared_plan(const int *block_table, const int *kv_len, const int *cu_q, const int *cu_group,
                                  int *shared, int *lead, int S, int num_groups, int table_width, int page, void *stream);
@@ -717,8 +724,9 @@ typedef enum {
  * D a power of two from 16 to 512, rot_dim a multiple of 16 up to D, T up to 2^30, Hq and Hk up to
  * 65536 (GDR_ERR_UNSUPPORTED otherwise);
  * eps finite, >= 0.  Angles are taken modulo a whole turn in 64-bit fixed point, so they are as good
- * at position 2^31 - 1 as at 1.  Arithmetic in fp32 (|x|^2 overflows where |x| passes 1.8e19),
- * rounded once.  One launch, no workspace.
+ * at position 2^31 - 1 as at 1.  Arithmetic in fp32 (|x|^2 overflows where |x| passes 1.8e19; below 3e-18
+ * it loses bits and at last is 0, which matters where eps does not cover it; a row of zeros with eps 0 is
+ * NaN), rounded once.  One launch, no workspace.
  *
  * gdr_qk_norm_rope_bwd: the gradients, given those of the outputs (d_q_out, d_k_out, laid out as
  *   the outputs): with g = R(p)^T dy,  dx = r (w g - x r^2 <w g, x> / N),  dw = the sum of g x r over
