@@ -152,8 +152,10 @@ size_t pre_bytes(int total_q, int Hq, int D) { return align32((size_t)total_q * 
 // tokens: none up to 16 k / none, 20.  (2.4 a pair fits these; whole passes of many blocks took 2.6, above.)
 // What the rule leaves out: lengths, so it does not see work that does not fill the SMs, nor a batch with
 // groups on both sides of the bound.  75 decodes of 8 heads and one cached head in 6 groups of 10 to 21 k
-// common tokens 46 us, gdr_kv8_attn 34; 18 x 2 to 5 drafted in groups of 0 to 31 k 99 and 36 (the short items of
-// the second pass stand together, and with fewer units than 9 a CTA their ends do not count in the division).
+// common tokens 46 us, gdr_kv8_attn 34; 18 x 2 to 5 drafted in groups of 0 to 31 k 99 and 36: some groups
+// are below the bound, and the second pass's tile kernel takes 75 us for 8 requests' 16 k keys and 9 short items
+// (without short ones, or in gdr_kv8_attn with 10 of them, the like takes 24; short items stand together, their
+// ends read the first pass's sums in turn, and with so few units a CTA ends do not count in the division).
 // Of 7543 drawn batches 3.1 % were more than a tenth slower than gdr_kv8_attn, 0.3 % more than half.
 // (`rows` of one request or group on average, at most `most`; alike: all have that many, else the last
 // block of each is half full; ends: what the ends of its items cost in units)
